@@ -1,7 +1,8 @@
 /*
  * mamba3_ssm.h -- C ABI of the MI355X (gfx950) Mamba-3 SSM layer core.
  *
- * Five operations, all asynchronous on a caller-given HIP stream:
+ * Five operations of the layer core and three of the residual block around
+ * it, all asynchronous on a caller-given HIP stream:
  *
  *   mamba3_ssm_chunked_fwd   whole-sequence forward (prefill / training
  *                            forward) by the chunked parallel form;
@@ -9,9 +10,16 @@
  *   mamba3_ssm_decode_step   one-token state update (generation);
  *   mamba3_rope_bc           the cumulative-angle rotation of B and C;
  *   mamba3_bc_prologue       the projection to B and C with their
- *                            normalisation, bias and rotation fused.
+ *                            normalisation, bias and rotation fused;
+ *   mamba3_layer_norm_*      layer norm over the model width;
+ *   mamba3_linear_*          a matrix product with bias, activation and
+ *                            residual;
+ *   mamba3_gated_ffn_*       both projections of a gated feed-forward, its
+ *                            activation and product (each of the three with
+ *                            its backward; their own conventions stand with
+ *                            them, at the end of this file).
  *
- * What they compute (pages cited by title and section):
+ * What the core computes (pages cited by title and section):
  *
  *  - linkstar.cloud/article/869, "第一刀：指数梯形离散化": with
  *    alpha_t = exp(dt_t A_t), beta_t = (1 - lam_t) dt_t alpha_t and
@@ -308,6 +316,123 @@ m3_status mamba3_bc_prologue(const m3_dims* d, int64_t d_model, const void* u, c
                              void* B_rot, void* C_rot, float* angle_final,
                              void* workspace, size_t workspace_bytes, void* stream);
 size_t mamba3_bc_prologue_workspace_size(const m3_dims* d);
+
+/* ---------------------------------------------------------------------------
+ * The residual block around the core: norm, products, gated feed-forward.
+ *
+ * A row is one token's vector; every operand below is a matrix of rows.
+ * Row-major; io operands (x, W, residual, y, pre, dy, dx, dW) are fp32 or bf16,
+ * all of one call the same type.  gain, bias, mean, rstd, dgain, dbias are
+ * fp32.  Sums, statistics and activations are held in fp32; bf16 outputs are
+ * rounded once (nearest even); the backward's products take
+ * dP (below) rounded to bf16 when io is bf16.
+ *
+ * Strides: x, y (or dy) and residual (or dskip) may have rows further apart
+ * than they are wide (a column slice of a wider matrix): the stride fields
+ * count elements from row to row, 0 stands for contiguous rows, and a stride
+ * below the width is M3_ERR_SHAPE.  Every other operand is contiguous.
+ *
+ * Any row count from 0, any width from 1, odd ones included: no alignment
+ * beyond the element's is required of any pointer.  Rows that lie on 16 bytes
+ * (pointer, stride and width) are read the fastest.  Limits
+ * (M3_ERR_UNSUPPORTED): widths and strides at most 2^20, rows at most 2^24,
+ * and at most 2^24 - 1 tiles of 64 x 64 outputs in any product of a call.
+ * With rows = 0 nothing is read and no row written; gradients summed over the
+ * rows (dW, dgain, dbias) are written as zeros.
+ *
+ * Outputs must not alias inputs, save y over residual and dx over dskip (same
+ * strides).  Results do not depend on the launch's timing: every sum is taken
+ * in a fixed order. */
+typedef enum {
+  M3_ACT_NONE = 0,
+  M3_ACT_RELU = 1,      /* max(z, 0); derivative 0 at 0 */
+  M3_ACT_SILU = 2,      /* z sigmoid(z) */
+  M3_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+  M3_ACT_GELU_TANH = 4, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  M3_ACT_SIGMOID = 5
+} m3_act;
+
+typedef struct {
+  int64_t rows;
+  int64_t width;       /* D */
+  int64_t x_stride;    /* of x */
+  int64_t y_stride;    /* of y (forward) or dy (backward) */
+  int64_t skip_stride; /* of dskip (backward) and dx; ignored forward */
+  int32_t io_dtype;
+  int32_t flags;       /* must be 0 */
+} m3_norm_dims;
+
+/* y = (x - mean) rstd gain + bias with mean and rstd = 1/sqrt(var + eps) of
+ * each row (var about the mean, divided by D).
+ * gain, bias: nullable (D) (NULL: 1 and 0).  eps: >= 0 and finite
+ * (M3_ERR_UNSUPPORTED otherwise).  mean, rstd: nullable pair (rows), written
+ * when given (the backward takes them). */
+m3_status mamba3_layer_norm_fwd(const m3_norm_dims* d, const void* x, const float* gain, const float* bias,
+                                float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Its backward: with xh = (x - mean) rstd and a = dy gain,
+ *   dx = rstd (a - mean_D(a) - xh mean_D(a xh)) + dskip,
+ *   dgain = sum over rows of dy xh,  dbias = sum over rows of dy.
+ * dskip: nullable, the gradient that reaches x past the norm (the residual
+ * path), with row stride skip_stride, which is dx's too.  dx: nullable.
+ * dgain, dbias: nullable, each by itself.  workspace: at least
+ * mamba3_layer_norm_bwd_workspace_size(d) bytes (partial column sums), needed
+ * when dgain or dbias is given; contents on entry do not matter. */
+m3_status mamba3_layer_norm_bwd(const m3_norm_dims* d, const void* x, const float* gain, const float* mean,
+                                const float* rstd, const void* dy, const void* dskip, void* dx, float* dgain,
+                                float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba3_layer_norm_bwd_workspace_size(const m3_norm_dims* d);
+
+typedef struct {
+  int64_t rows;            /* M */
+  int64_t d_in;            /* K: width of x */
+  int64_t d_out;           /* N: width of y (gated_ffn: F, of h) */
+  int64_t x_stride;        /* of x */
+  int64_t y_stride;        /* of y or h (forward), dy or dh (backward) */
+  int64_t residual_stride; /* of residual (linear_fwd only) */
+  int32_t io_dtype;
+  int32_t act;             /* m3_act */
+  int32_t flags;           /* must be 0 */
+  int32_t reserved;        /* must be 0 */
+} m3_linear_dims;
+
+/* pre = x W^T + bias, y = act(pre) + residual.
+ * W: (N, K).  bias: nullable (N).  residual: nullable (M, N).
+ * pre: nullable (M, N), written when given (the backward takes it for any
+ * activation but M3_ACT_NONE).
+ * workspace: at least mamba3_linear_fwd_workspace_size(d) bytes (fp32 partial
+ * sums of products whose K is split over several blocks; may be 0). */
+m3_status mamba3_linear_fwd(const m3_linear_dims* d, const void* x, const void* W, const float* bias,
+                            const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t mamba3_linear_fwd_workspace_size(const m3_linear_dims* d);
+
+/* Its backward: dP = dy act'(pre), dx = dP W, dW = dP^T x, dbias = sum over
+ * rows of dP (the residual's gradient is dy itself).
+ * pre: required unless act is M3_ACT_NONE (then ignored).  dx (M, K), dW
+ * (N, K), dbias (N): nullable, each by itself; x is needed for dW, W for dx.
+ * workspace: at least mamba3_linear_bwd_workspace_size(d) bytes (dP, partial
+ * sums). */
+m3_status mamba3_linear_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre, const void* dy,
+                            void* dx, void* dW, float* dbias, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t mamba3_linear_bwd_workspace_size(const m3_linear_dims* d);
+
+/* Gated feed-forward: pre = [g u] = x W^T + bias, h = act(g) u (entry by
+ * entry).  W: (2F, K), the F rows of the gate's projection, then the F of the
+ * other.  bias: nullable (2F), in the same order.  pre: nullable (M, 2F), g
+ * then u in each row, written when given (the backward takes it). */
+m3_status mamba3_gated_ffn_fwd(const m3_linear_dims* d, const void* x, const void* W, const float* bias, void* h,
+                               void* pre, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba3_gated_ffn_fwd_workspace_size(const m3_linear_dims* d);
+
+/* Its backward: dP = [dh u act'(g), dh act(g)], dx = dP W, dW = dP^T x,
+ * dbias = sum over rows of dP.  pre is required; the rest as linear_bwd with
+ * 2F rows of W. */
+m3_status mamba3_gated_ffn_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre,
+                               const void* dh, void* dx, void* dW, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t mamba3_gated_ffn_bwd_workspace_size(const m3_linear_dims* d);
 
 const char* mamba3_status_string(m3_status s);
 int mamba3_abi_version(void);

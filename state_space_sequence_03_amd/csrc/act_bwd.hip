@@ -1,0 +1,111 @@
+// The elementwise part of the backward of the linear and gated feed-forward
+// operators, in one pass over dy and the stored pre-activations:
+//   linear: dP = dy act'(pre);   gated: dP = [dy u act'(g), dy act(g)],
+// rounded once to the io type (the products that follow take their operands
+// in it), and the column sums of the unrounded dP (the bias' gradient).
+// Bound by HBM.  A block owns 32 vectors of columns and a slab of rows, eight
+// rows at a time; each thread sums its columns over its rows, the eight row
+// groups are added in LDS and the slabs by launch_reduce_parts, all in a
+// fixed order.
+#include "act.hpp"
+#include "m3_launch.hpp"
+#include "m3_rows.hpp"
+
+namespace m3 {
+
+namespace {
+
+template <typename T, int ACT, bool GATED>
+__global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int64_t slab) {
+  constexpr int V = io<T>::VEC;
+  constexpr bool FINE = io<T>::BYTES == 4;
+  constexpr int W = GATED ? 2 : 1;
+  __shared__ float sh[7][32][W * V + 1];
+  const int cv = threadIdx.x & 31, rg = threadIdx.x >> 5;
+  const int64_t c = ((int64_t)blockIdx.x * 32 + cv) * V, C = a.cols, ld = W * C;
+  const int64_t r0 = (int64_t)blockIdx.y * slab, r1 = r0 + slab < a.rows ? r0 + slab : a.rows;
+  float s[W][V];
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[w][j] = 0.0f;
+  if (c < C)
+#pragma unroll 2
+    for (int64_t r = r0 + rg; r < r1; r += 8) {
+      float d[V], z[V], u[V];
+      row_load<T>((const char*)a.dy + r * a.ldy * io<T>::BYTES, c, C, d);
+      const char* pre = (const char*)a.pre + r * ld * io<T>::BYTES;
+      if constexpr (GATED || ACT != ACT_NONE) row_load<T>(pre, c, C, z);
+      if constexpr (GATED) row_load<T>(pre + C * io<T>::BYTES, c, C, u);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float f, df;
+        if constexpr (GATED || ACT != ACT_NONE) act_both<ACT, FINE>(z[j], f, df);
+        if constexpr (GATED) {
+          z[j] = d[j] * f;
+          d[j] = d[j] * u[j] * df;
+          s[1][j] += z[j];
+        } else if constexpr (ACT != ACT_NONE) {
+          d[j] *= df;
+        }
+        s[0][j] += d[j];
+      }
+      if (a.dp) {
+        char* dp = (char*)a.dp + r * ld * io<T>::BYTES;
+        row_store<T>(dp, c, C, d);
+        if constexpr (GATED) row_store<T>(dp + C * io<T>::BYTES, c, C, z);
+      }
+    }
+  if (!a.part) return;
+  if (rg > 0)
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sh[rg - 1][cv][w * V + j] = s[w][j];
+  __syncthreads();
+  if (rg > 0 || c >= C) return;
+  float* part = a.part + (int64_t)blockIdx.y * ld;
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      for (int g = 0; g < 7; ++g) s[w][j] += sh[g][cv][w * V + j];
+      if (c + j < C) part[w * C + c + j] = s[w][j];
+    }
+}
+
+template <typename T>
+hipError_t act_bwd_run(const ActBwdArgs& a, hipStream_t s) {
+  const int64_t parts = act_bwd_parts(a.rows), per = 32 * io<T>::VEC;
+  const int64_t slab = (a.rows + parts - 1) / parts;
+  const dim3 grid((unsigned)((a.cols + per - 1) / per), (unsigned)parts), blk(256);
+  with_act(a.act, [&](auto act) {
+    if (a.gated) hipLaunchKernelGGL((act_bwd_kernel<T, act.value, true>), grid, blk, 0, s, a, slab);
+    else hipLaunchKernelGGL((act_bwd_kernel<T, act.value, false>), grid, blk, 0, s, a, slab);
+  });
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(u16* dst, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) dst[i] = 0;
+}
+
+}  // namespace
+
+hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s) {
+  const int64_t blocks = (bytes / 2 + 255) / 256;
+  hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, (u16*)dst,
+                     bytes / 2);
+  return hipGetLastError();
+}
+
+int64_t act_bwd_parts(int64_t rows) {
+  const int64_t p = (rows + 63) / 64;
+  return p < 64 ? p : 64;
+}
+
+hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s) {
+  return io_bf16 ? act_bwd_run<bf16_t>(a, s) : act_bwd_run<float>(a, s);
+}
+
+}  // namespace m3

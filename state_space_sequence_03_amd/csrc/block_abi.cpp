@@ -1,0 +1,250 @@
+// C ABI of the residual block's operators (layer norm, linear, gated
+// feed-forward): argument validation on the host, before any HIP call,
+// workspace layout and dispatch.  Specified in include/mamba3_ssm.h.
+#include "../../include/mamba3_ssm.h"
+
+#include <hip/hip_runtime.h>
+
+#include "m3_launch.hpp"
+
+namespace {
+
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxRows = int64_t(1) << 24;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool aligned_all(std::initializer_list<const void*> ps, uintptr_t a) {
+  for (const void* p : ps)
+    if (!aligned(p, a)) return false;
+  return true;
+}
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// A width and the row strides that go with it (0: contiguous).
+m3_status check_width(int64_t width, std::initializer_list<int64_t> strides) {
+  if (width <= 0) return M3_ERR_SHAPE;
+  for (int64_t s : strides)
+    if (s != 0 && s < width) return M3_ERR_SHAPE;
+  if (width > kMaxWidth) return M3_ERR_UNSUPPORTED;
+  for (int64_t s : strides)
+    if (s > kMaxWidth) return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
+int64_t or_width(int64_t stride, int64_t width) { return stride ? stride : width; }
+
+m3_status check_rows_type(int64_t rows, int32_t io_dtype, int32_t flags) {
+  if (rows < 0) return M3_ERR_SHAPE;
+  if (io_dtype != M3_F32 && io_dtype != M3_BF16) return M3_ERR_UNSUPPORTED;
+  if (flags != 0 || rows > kMaxRows) return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
+m3_status check_norm(const m3_norm_dims* d) {
+  if (!d) return M3_ERR_NULL;
+  const m3_status st = check_rows_type(d->rows, d->io_dtype, d->flags);
+  return st != M3_OK ? st : check_width(d->width, {d->x_stride, d->y_stride, d->skip_stride});
+}
+
+// The smallest tile any product kernel uses is 64 x 64.
+bool tiles_fit(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) < (int64_t(1) << 24); }
+
+m3_status check_linear(const m3_linear_dims* d, bool gated, bool backward) {
+  if (!d) return M3_ERR_NULL;
+  m3_status st = check_rows_type(d->rows, d->io_dtype, d->flags);
+  if (st != M3_OK) return st;
+  if (d->reserved != 0 || d->act < M3_ACT_NONE || d->act > M3_ACT_SIGMOID) return M3_ERR_UNSUPPORTED;
+  st = check_width(d->d_in, {d->x_stride});
+  if (st == M3_OK) st = check_width(d->d_out, {d->y_stride, gated || backward ? 0 : d->residual_stride});
+  if (st != M3_OK) return st;
+  const int64_t n = gated ? 2 * d->d_out : d->d_out;
+  if (n > kMaxWidth) return M3_ERR_UNSUPPORTED;
+  if (!tiles_fit(d->rows, n) || (backward && (!tiles_fit(d->rows, d->d_in) || !tiles_fit(n, d->d_in))))
+    return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
+int bf16(int32_t io_dtype) { return io_dtype == M3_BF16 ? 1 : 0; }
+uintptr_t esize(int32_t io_dtype) { return io_dtype == M3_BF16 ? 2 : 4; }
+
+m3_status hip_status(hipError_t e) { return e == hipSuccess ? M3_OK : M3_ERR_HIP; }
+
+m3_status linear_fwd(const m3_linear_dims* d, bool gated, const void* x, const void* W, const float* bias,
+                     const void* residual, void* y, void* pre, void* stream) {
+  const m3_status st = check_linear(d, gated, false);
+  if (st != M3_OK) return st;
+  if (d->rows > 0 && (!x || !W || !y)) return M3_ERR_NULL;
+  if (!aligned_all({x, W, residual, y, pre}, esize(d->io_dtype)) || !aligned(bias, 4)) return M3_ERR_ALIGN;
+  if (d->rows == 0) return M3_OK;
+  m3::MmArgs a{};
+  a.P = x; a.ldp = or_width(d->x_stride, d->d_in);
+  a.Q = W; a.ldq = d->d_in;
+  a.M = d->rows; a.N = d->d_out; a.K = d->d_in;
+  a.out = y; a.ldo = or_width(d->y_stride, d->d_out);
+  a.bias = bias; a.res = residual; a.ldr = or_width(d->residual_stride, d->d_out);
+  a.pre = pre; a.act = d->act;
+  return hip_status(m3::launch_mm(bf16(d->io_dtype), m3::MM_PQ_K, gated ? m3::MM_GATED : m3::MM_LINEAR, a,
+                                  (hipStream_t)stream));
+}
+
+// Workspace of the backward: dP in the io type, then the partial column sums.
+struct BwdWs {
+  size_t dp, part, bytes;
+};
+BwdWs bwd_ws(const m3_linear_dims* d, bool gated) {
+  const size_t n = (size_t)(gated ? 2 * d->d_out : d->d_out), rows = (size_t)d->rows;
+  BwdWs w{};
+  const bool has_dp = gated || d->act != M3_ACT_NONE;
+  w.part = has_dp ? up256(rows * n * esize(d->io_dtype)) : 0;
+  w.bytes = w.part + up256(4 * n * (size_t)m3::act_bwd_parts(d->rows));
+  return w;
+}
+
+m3_status linear_bwd(const m3_linear_dims* d, bool gated, const void* x, const void* W, const void* pre,
+                     const void* dy, void* dx, void* dW, float* dbias, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  m3_status st = check_linear(d, gated, true);
+  if (st != M3_OK) return st;
+  const bool has_dp = gated || d->act != M3_ACT_NONE;
+  if (d->rows > 0 && ((dx && !W) || (dW && !x) || ((dx || dW || dbias) && (!dy || (has_dp && !pre)))))
+    return M3_ERR_NULL;
+  if (!aligned_all({x, W, pre, dy, dx, dW}, esize(d->io_dtype)) || !aligned(dbias, 4) || !aligned(workspace, 16))
+    return M3_ERR_ALIGN;
+  const BwdWs w = bwd_ws(d, gated);
+  const hipStream_t s = (hipStream_t)stream;
+  const int64_t n = gated ? 2 * d->d_out : d->d_out;
+  const int io = bf16(d->io_dtype);
+  if (d->rows == 0) {
+    hipError_t e = hipSuccess;
+    if (dW) e = m3::launch_zero(dW, n * d->d_in * (int64_t)esize(d->io_dtype), s);
+    if (dbias && e == hipSuccess) e = m3::launch_zero(dbias, 4 * n, s);
+    return hip_status(e);
+  }
+  if ((has_dp && (dx || dW)) || dbias)
+    if (!workspace || workspace_bytes < w.bytes) return M3_ERR_WORKSPACE;
+  const void* dp = dy;
+  int64_t ldp = or_width(d->y_stride, d->d_out);
+  if ((has_dp && (dx || dW)) || dbias) {
+    m3::ActBwdArgs b{};
+    b.pre = pre; b.dy = dy; b.ldy = ldp;
+    b.dp = has_dp && (dx || dW) ? (char*)workspace + w.dp : nullptr;
+    b.part = dbias ? (float*)((char*)workspace + w.part) : nullptr;
+    b.rows = d->rows; b.cols = d->d_out; b.act = d->act; b.gated = gated;
+    hipError_t e = m3::launch_act_bwd(io, b, s);
+    if (e == hipSuccess && dbias)
+      e = m3::launch_reduce_parts(b.part, m3::act_bwd_parts(d->rows), n, n, dbias, n, nullptr, s);
+    if (e != hipSuccess) return M3_ERR_HIP;
+    if (has_dp) {
+      dp = b.dp;
+      ldp = n;
+    }
+  }
+  m3::MmArgs a{};
+  a.P = dp; a.ldp = ldp;
+  if (dx) {  // dx[m][k] = sum_n dP[m][n] W[n][k]
+    a.Q = W; a.ldq = d->d_in;
+    a.M = d->rows; a.N = d->d_in; a.K = n;
+    a.out = dx; a.ldo = d->d_in;
+    if (m3::launch_mm(io, m3::MM_P_K, m3::MM_STORE, a, s) != hipSuccess) return M3_ERR_HIP;
+  }
+  if (dW) {  // dW[n][k] = sum_m dP[m][n] x[m][k]
+    a.Q = x; a.ldq = or_width(d->x_stride, d->d_in);
+    a.M = n; a.N = d->d_in; a.K = d->rows;
+    a.out = dW; a.ldo = d->d_in;
+    if (m3::launch_mm(io, m3::MM_NONE_K, m3::MM_STORE, a, s) != hipSuccess) return M3_ERR_HIP;
+  }
+  return M3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+m3_status mamba3_layer_norm_fwd(const m3_norm_dims* d, const void* x, const float* gain, const float* bias,
+                                float eps, void* y, float* mean, float* rstd, void* stream) {
+  const m3_status st = check_norm(d);
+  if (st != M3_OK) return st;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return M3_ERR_UNSUPPORTED;
+  if ((mean == nullptr) != (rstd == nullptr)) return M3_ERR_NULL;
+  if (d->rows > 0 && (!x || !y)) return M3_ERR_NULL;
+  if (!aligned_all({x, y}, esize(d->io_dtype)) || !aligned_all({gain, bias, mean, rstd}, 4)) return M3_ERR_ALIGN;
+  if (d->rows == 0) return M3_OK;
+  m3::NormArgs a{};
+  a.x = x; a.gain = gain; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.eps = eps;
+  a.rows = d->rows; a.width = d->width;
+  a.x_stride = or_width(d->x_stride, d->width);
+  a.y_stride = or_width(d->y_stride, d->width);
+  return hip_status(m3::launch_norm_fwd(bf16(d->io_dtype), a, (hipStream_t)stream));
+}
+
+size_t mamba3_layer_norm_bwd_workspace_size(const m3_norm_dims* d) {
+  if (check_norm(d) != M3_OK) return 0;
+  return sizeof(float) * 2 * (size_t)d->width * (size_t)m3::norm_bwd_parts(d->rows);
+}
+
+m3_status mamba3_layer_norm_bwd(const m3_norm_dims* d, const void* x, const float* gain, const float* mean,
+                                const float* rstd, const void* dy, const void* dskip, void* dx, float* dgain,
+                                float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  const m3_status st = check_norm(d);
+  if (st != M3_OK) return st;
+  if (d->rows > 0 && (!x || !mean || !rstd || !dy)) return M3_ERR_NULL;
+  if (!aligned_all({x, dy, dskip, dx}, esize(d->io_dtype)) ||
+      !aligned_all({gain, mean, rstd, dgain, dbias, workspace}, 4))
+    return M3_ERR_ALIGN;
+  const hipStream_t s = (hipStream_t)stream;
+  if (d->rows == 0) {
+    hipError_t e = hipSuccess;
+    if (dgain) e = m3::launch_zero(dgain, 4 * d->width, s);
+    if (dbias && e == hipSuccess) e = m3::launch_zero(dbias, 4 * d->width, s);
+    return hip_status(e);
+  }
+  const bool cols = dgain || dbias;
+  if (cols && (!workspace || workspace_bytes < mamba3_layer_norm_bwd_workspace_size(d))) return M3_ERR_WORKSPACE;
+  if (!cols && !dx) return M3_OK;
+  m3::NormBwdArgs a{};
+  a.x = x; a.gain = gain; a.mean = mean; a.rstd = rstd; a.dy = dy; a.dskip = dskip; a.dx = dx;
+  a.part = cols ? (float*)workspace : nullptr;
+  a.rows = d->rows; a.width = d->width;
+  a.x_stride = or_width(d->x_stride, d->width);
+  a.y_stride = or_width(d->y_stride, d->width);
+  a.skip_stride = or_width(d->skip_stride, d->width);
+  return hip_status(m3::launch_norm_bwd(bf16(d->io_dtype), a, dgain, dbias, s));
+}
+
+size_t mamba3_linear_fwd_workspace_size(const m3_linear_dims*) { return 0; }
+
+m3_status mamba3_linear_fwd(const m3_linear_dims* d, const void* x, const void* W, const float* bias,
+                            const void* residual, void* y, void* pre, void*, size_t, void* stream) {
+  return linear_fwd(d, false, x, W, bias, residual, y, pre, stream);
+}
+
+size_t mamba3_linear_bwd_workspace_size(const m3_linear_dims* d) {
+  return check_linear(d, false, true) == M3_OK ? bwd_ws(d, false).bytes : 0;
+}
+
+m3_status mamba3_linear_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre, const void* dy,
+                            void* dx, void* dW, float* dbias, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  return linear_bwd(d, false, x, W, pre, dy, dx, dW, dbias, workspace, workspace_bytes, stream);
+}
+
+size_t mamba3_gated_ffn_fwd_workspace_size(const m3_linear_dims*) { return 0; }
+
+m3_status mamba3_gated_ffn_fwd(const m3_linear_dims* d, const void* x, const void* W, const float* bias, void* h,
+                               void* pre, void*, size_t, void* stream) {
+  return linear_fwd(d, true, x, W, bias, nullptr, h, pre, stream);
+}
+
+size_t mamba3_gated_ffn_bwd_workspace_size(const m3_linear_dims* d) {
+  return check_linear(d, true, true) == M3_OK ? bwd_ws(d, true).bytes : 0;
+}
+
+m3_status mamba3_gated_ffn_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre,
+                               const void* dh, void* dx, void* dW, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return linear_bwd(d, true, x, W, pre, dh, dx, dW, dbias, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -150,6 +150,67 @@ hipError_t launch_segment_fixups(int io_bf16, int N, int P, const WalkArgs& a, h
 // The segment scan alone (seg_end, seg_tot -> seg_in and h_final when set).
 hipError_t launch_seg_scan(int N, int P, const WalkArgs& a, hipStream_t s);
 
+// Layer norm over rows of `width` elements (row strides in elements).
+struct NormArgs {
+  const void* x;
+  const float *gain, *bias;  // nullable
+  void* y;
+  float *mean, *rstd;  // nullable pair
+  float eps;
+  int64_t rows, width, x_stride, y_stride;
+};
+hipError_t launch_norm_fwd(int io_bf16, const NormArgs& a, hipStream_t s);
+struct NormBwdArgs {
+  const void* x;
+  const float *gain, *mean, *rstd;  // gain nullable
+  const void *dy, *dskip;           // dskip nullable
+  void* dx;                         // nullable; row stride skip_stride
+  float* part;                      // nullable: (norm_bwd_parts(rows), 2, width) partial column sums
+  int64_t rows, width, x_stride, y_stride, skip_stride;
+};
+int64_t norm_bwd_parts(int64_t rows);
+hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, float* dgain, float* dbias, hipStream_t s);
+// out[c] = sum over p < np of part[p * stride + c] for c < n; the first n0 go
+// to out0, the rest to out1 (each nullable).
+hipError_t launch_reduce_parts(const float* part, int64_t np, int64_t stride, int64_t n, float* out0, int64_t n0,
+                               float* out1, hipStream_t s);
+
+// out[m][n] = sum_k P(m, k) Q(n, k) with an epilogue.  P is (M, K) row-major,
+// or (K, M) where its k is not contiguous; Q likewise.  Strides in elements.
+enum MmLayout { MM_PQ_K = 0, MM_P_K = 1, MM_NONE_K = 2 };  // whose rows run along k: both, P only, neither
+enum MmEpilogue { MM_STORE = 0, MM_LINEAR = 1, MM_GATED = 2 };
+struct MmArgs {
+  const void *P, *Q;
+  int64_t ldp, ldq;
+  int64_t M, N, K;
+  void* out;
+  int64_t ldo;
+  // MM_LINEAR: out = act(acc + bias) + res, pre = acc + bias.
+  // MM_GATED: Q has 2N rows; out = act(g) u with g row n, u row N + n of Q;
+  // pre (M, 2N) holds g then u.
+  const float* bias;  // nullable
+  const void* res;    // nullable
+  int64_t ldr;
+  void* pre;  // nullable, contiguous
+  int act;
+};
+hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, hipStream_t s);
+
+// dP of the linear (gated = 0: dy act'(pre)) or gated (dy u act'(g), dy act(g))
+// operator, and the partial column sums of it.
+struct ActBwdArgs {
+  const void* pre;  // (rows, cols or 2 cols); null when act is none and gated is 0
+  const void* dy;   // row stride ldy
+  void* dp;         // nullable: as pre
+  float* part;      // nullable: (act_bwd_parts(rows), cols or 2 cols)
+  int64_t rows, cols, ldy;
+  int act, gated;
+};
+int64_t act_bwd_parts(int64_t rows);
+hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s);
+// Zeros to `bytes` bytes of dst (2-byte aligned, an even count).
+hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s);
+
 // Fill n floats of dst with src (or zeros when src is NULL).
 hipError_t launch_copy_f32(float* dst, const float* src, int64_t n, hipStream_t s);
 

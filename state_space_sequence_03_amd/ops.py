@@ -7,9 +7,12 @@ If the library is missing this module raises; there is no fallback.
 
 Entry points keep the ABI's names:
   mamba3_ssm_chunked_fwd, mamba3_ssm_chunked_bwd, mamba3_ssm_decode_step,
-  mamba3_rope_bc, mamba3_bc_prologue
-(and the friendlier aliases chunked_fwd, chunked_bwd, decode_step, rope_bc,
-bc_prologue), plus the workspace size queries.
+  mamba3_rope_bc, mamba3_bc_prologue,
+  mamba3_layer_norm_fwd, mamba3_layer_norm_bwd, mamba3_linear_fwd,
+  mamba3_linear_bwd, mamba3_gated_ffn_fwd, mamba3_gated_ffn_bwd
+(and the friendlier aliases without the prefix: chunked_fwd, chunked_bwd,
+decode_step, rope_bc, bc_prologue, layer_norm_fwd, ...), plus the workspace
+size queries.
 """
 from __future__ import annotations
 
@@ -32,13 +35,32 @@ ABI_SYMBOLS = ("mamba3_ssm_chunked_fwd", "mamba3_ssm_chunked_fwd_workspace_size"
                "mamba3_ssm_chunked_bwd",
                "mamba3_ssm_chunked_bwd_workspace_size", "mamba3_ssm_decode_step",
                "mamba3_rope_bc", "mamba3_rope_bc_workspace_size", "mamba3_bc_prologue",
-               "mamba3_bc_prologue_workspace_size", "mamba3_status_string", "mamba3_abi_version")
+               "mamba3_bc_prologue_workspace_size", "mamba3_layer_norm_fwd", "mamba3_layer_norm_bwd",
+               "mamba3_layer_norm_bwd_workspace_size", "mamba3_linear_fwd", "mamba3_linear_fwd_workspace_size",
+               "mamba3_linear_bwd", "mamba3_linear_bwd_workspace_size", "mamba3_gated_ffn_fwd",
+               "mamba3_gated_ffn_fwd_workspace_size", "mamba3_gated_ffn_bwd", "mamba3_gated_ffn_bwd_workspace_size",
+               "mamba3_status_string", "mamba3_abi_version")
+# activations of linear and gated_ffn
+M3_ACT_NONE, M3_ACT_RELU, M3_ACT_SILU, M3_ACT_GELU, M3_ACT_GELU_TANH, M3_ACT_SIGMOID = range(6)
 
 
 class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("rank", ctypes.c_int64),
                 ("chunk", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("skip_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class Mamba3Error(RuntimeError):
@@ -80,6 +102,18 @@ def lib() -> ctypes.CDLL:
         L.mamba3_bc_prologue.restype = ctypes.c_int
         L.mamba3_bc_prologue_workspace_size.argtypes = [dp]
         L.mamba3_bc_prologue_workspace_size.restype = sz
+        nd, ld = ctypes.POINTER(NormDims), ctypes.POINTER(LinearDims)
+        L.mamba3_layer_norm_fwd.argtypes = [nd, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]
+        L.mamba3_layer_norm_bwd.argtypes = [nd] + [vp] * 9 + [vp, sz, vp]
+        L.mamba3_linear_fwd.argtypes = [ld] + [vp] * 6 + [vp, sz, vp]
+        L.mamba3_linear_bwd.argtypes = [ld] + [vp] * 7 + [vp, sz, vp]
+        L.mamba3_gated_ffn_fwd.argtypes = [ld] + [vp] * 5 + [vp, sz, vp]
+        L.mamba3_gated_ffn_bwd.argtypes = [ld] + [vp] * 7 + [vp, sz, vp]
+        for name, dims in (("layer_norm_bwd", nd), ("linear_fwd", ld), ("linear_bwd", ld), ("gated_ffn_fwd", ld),
+                           ("gated_ffn_bwd", ld)):
+            query = getattr(L, f"mamba3_{name}_workspace_size")
+            query.argtypes = [dims]
+            query.restype = sz
         L.mamba3_status_string.argtypes = [ctypes.c_int]
         L.mamba3_status_string.restype = ctypes.c_char_p
         L.mamba3_abi_version.restype = ctypes.c_int
@@ -361,9 +395,246 @@ def mamba3_bc_prologue(u, W, dt, theta, nheads, rank, dstate, gain=None, bias=No
     return B_rot, C_rot, angle_final
 
 
+# ---------------------------------------------------------------------------
+# the residual block around the core: layer norm, linear, gated feed-forward
+# ---------------------------------------------------------------------------
+def _rows(name, t, width, rows, dtype, device):
+    """(pointer, row stride in elements; 0: contiguous) of a matrix of rows:
+    (..., width) contiguous, or (rows, width) with rows further apart."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape[-1] != width or t.numel() != rows * width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {rows} rows of {width}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= width:
+        return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{name}: must be contiguous, or 2-d with contiguous rows")
+
+
+def _vec(name, t, shape, dtype, device):
+    """Pointer of a contiguous operand of the given shape (None: absent)."""
+    if t is None:
+        return None
+    _expect(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(query, dims, workspace, device):
+    need = query(ctypes.byref(dims))
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _torch().empty(need, device=device, dtype=_torch().uint8)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _raw_stream(stream, device):
+    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
+
+
+def _shape_rows(x):
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (..., width) with a width from 1")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=None, rstd=None, want_stats=False,
+                          stream=None):
+    """Layer norm of the rows of x (..., D).  Returns (y, mean, rstd); the
+    statistics ((rows) fp32, for the backward) are None unless wanted or given."""
+    torch = _torch()
+    rows, D = _shape_rows(x)
+    io, dev, f32 = x.dtype, x.device, torch.float32
+    code = _io_code(x)
+    px, sx = _rows("x", x, D, rows, io, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=io, device=dev)
+    if want_stats or mean is not None or rstd is not None:
+        mean = torch.empty(rows, dtype=f32, device=dev) if mean is None else mean
+        rstd = torch.empty(rows, dtype=f32, device=dev) if rstd is None else rstd
+    py, sy = _rows("y", y, D, rows, io, dev)
+    st = lib().mamba3_layer_norm_fwd(NormDims(rows, D, sx, sy, 0, code, 0), px, _vec("gain", gain, (D,), f32, dev),
+                                     _vec("bias", bias, (D,), f32, dev), eps, py,
+                                     _vec("mean", mean, (rows,), f32, dev), _vec("rstd", rstd, (rows,), f32, dev),
+                                     _raw_stream(stream, dev))
+    _check(st, "mamba3_layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd_workspace_size(dims: NormDims) -> int:
+    return int(lib().mamba3_layer_norm_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=True, want_dgain=True,
+                          want_dbias=True, dx=None, dgain=None, dbias=None, workspace=None, stream=None):
+    """Backward of layer_norm_fwd.  dskip: a gradient that reaches x past the
+    norm, added to dx.  Returns a dict with dx (io dtype), dgain and dbias (fp32),
+    as wanted.  dskip and dx have the same row stride."""
+    torch = _torch()
+    rows, D = _shape_rows(x)
+    io, dev, f32 = x.dtype, x.device, torch.float32
+    code = _io_code(x)
+    px, sx = _rows("x", x, D, rows, io, dev)
+    pdy, sdy = _rows("dy", dy, D, rows, io, dev)
+    psk, ssk = _rows("dskip", dskip, D, rows, io, dev)
+    out = {}
+    pdx = pg = pb = pws = None
+    nws = 0
+    if want_dx or dx is not None:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=io, device=dev) if ssk == 0 else torch.empty_strided(
+                (rows, D), (ssk, 1), dtype=io, device=dev)
+        pdx, sdx = _rows("dx", dx, D, rows, io, dev)
+        if dskip is not None and (sdx or D) != (ssk or D):
+            raise ValueError("dx and dskip must have the same row stride")
+        ssk = sdx
+        out["dx"] = dx
+    if want_dgain or dgain is not None:
+        out["dgain"] = dgain = torch.empty(D, dtype=f32, device=dev) if dgain is None else dgain
+        pg = _vec("dgain", dgain, (D,), f32, dev)
+    if want_dbias or dbias is not None:
+        out["dbias"] = dbias = torch.empty(D, dtype=f32, device=dev) if dbias is None else dbias
+        pb = _vec("dbias", dbias, (D,), f32, dev)
+    dims = NormDims(rows, D, sx, sdy, ssk, code, 0)
+    if pg or pb:
+        workspace, pws, nws = _workspace(lib().mamba3_layer_norm_bwd_workspace_size, dims, workspace, dev)
+    st = lib().mamba3_layer_norm_bwd(dims, px, _vec("gain", gain, (D,), f32, dev),
+                                     _vec("mean", mean, (rows,), f32, dev), _vec("rstd", rstd, (rows,), f32, dev),
+                                     pdy, psk, pdx, pg, pb, pws, nws, _raw_stream(stream, dev))
+    _check(st, "mamba3_layer_norm_bwd")
+    return out
+
+
+def linear_fwd_workspace_size(dims: LinearDims) -> int:
+    return int(lib().mamba3_linear_fwd_workspace_size(ctypes.byref(dims)))
+
+
+def linear_bwd_workspace_size(dims: LinearDims) -> int:
+    return int(lib().mamba3_linear_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def gated_ffn_fwd_workspace_size(dims: LinearDims) -> int:
+    return int(lib().mamba3_gated_ffn_fwd_workspace_size(ctypes.byref(dims)))
+
+
+def gated_ffn_bwd_workspace_size(dims: LinearDims) -> int:
+    return int(lib().mamba3_gated_ffn_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def _weight_shape(x, W, gated):
+    if W.dim() != 2:
+        raise ValueError(f"W: shape {tuple(W.shape)}, expected (rows of W, d_in)")
+    if gated and W.shape[0] % 2:
+        raise ValueError(f"W: {W.shape[0]} rows, expected the gate's and as many more")
+    rows, K = _shape_rows(x)
+    return rows, K, W.shape[0], W.shape[0] // 2 if gated else W.shape[0]
+
+
+def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, workspace, stream):
+    torch = _torch()
+    rows, K, wrows, N = _weight_shape(x, W, gated)
+    io, dev, L = x.dtype, x.device, lib()
+    code = _io_code(x)
+    px, sx = _rows("x", x, K, rows, io, dev)
+    lead = x.shape[:-1]
+    if y is None:
+        y = torch.empty(lead + (N,), dtype=io, device=dev)
+    py, sy = _rows("y", y, N, rows, io, dev)
+    pr, sr = _rows("residual", residual, N, rows, io, dev)
+    if pre is None and want_pre:
+        pre = torch.empty(lead + (wrows,), dtype=io, device=dev)
+    ppre = _vec("pre", pre, lead + (wrows,), io, dev)
+    dims = LinearDims(rows, K, N, sx, sy, sr, code, act, 0, 0)
+    query = L.mamba3_gated_ffn_fwd_workspace_size if gated else L.mamba3_linear_fwd_workspace_size
+    workspace, pws, nws = _workspace(query, dims, workspace, dev)
+    pW, pb = _vec("W", W, (wrows, K), io, dev), _vec("bias", bias, (wrows,), torch.float32, dev)
+    s = _raw_stream(stream, dev)
+    st = (L.mamba3_gated_ffn_fwd(dims, px, pW, pb, py, ppre, pws, nws, s) if gated else
+          L.mamba3_linear_fwd(dims, px, pW, pb, pr, py, ppre, pws, nws, s))
+    _check(st, name)
+    return y, pre
+
+
+def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, dx, dW, dbias, workspace, stream):
+    torch = _torch()
+    rows, K, wrows, N = _weight_shape(x, W, gated)
+    io, dev, L = x.dtype, x.device, lib()
+    code = _io_code(x)
+    px, sx = _rows("x", x, K, rows, io, dev)
+    pdy, sdy = _rows("dy", dy, N, rows, io, dev)
+    if pre is None and (gated or act != M3_ACT_NONE):
+        raise ValueError("pre is required (the forward's want_pre)")
+    ppre = _rows("pre", pre, wrows, rows, io, dev)
+    if ppre[1]:
+        raise ValueError("pre: must be contiguous")
+    out = {}
+    pdx = pdW = pb = None
+    if want_dx or dx is not None:
+        out["dx"] = dx = torch.empty(x.shape, dtype=io, device=dev) if dx is None else dx
+        pdx = _vec("dx", dx, x.shape, io, dev)
+    if want_dW or dW is not None:
+        out["dW"] = dW = torch.empty((wrows, K), dtype=io, device=dev) if dW is None else dW
+        pdW = _vec("dW", dW, (wrows, K), io, dev)
+    if want_dbias or dbias is not None:
+        out["dbias"] = dbias = torch.empty(wrows, dtype=torch.float32, device=dev) if dbias is None else dbias
+        pb = _vec("dbias", dbias, (wrows,), torch.float32, dev)
+    dims = LinearDims(rows, K, N, sx, sdy, 0, code, act, 0, 0)
+    query = L.mamba3_gated_ffn_bwd_workspace_size if gated else L.mamba3_linear_bwd_workspace_size
+    workspace, pws, nws = _workspace(query, dims, workspace, dev)
+    call = L.mamba3_gated_ffn_bwd if gated else L.mamba3_linear_bwd
+    st = call(dims, px, _vec("W", W, (wrows, K), io, dev), ppre[0], pdy, pdx, pdW, pb, pws, nws,
+              _raw_stream(stream, dev))
+    _check(st, name)
+    return out
+
+
+def mamba3_linear_fwd(x, W, bias=None, residual=None, *, act=M3_ACT_NONE, y=None, pre=None, want_pre=False,
+                      workspace=None, stream=None):
+    """act(x W^T + bias) + residual for x (..., d_in), W (d_out, d_in).  Returns
+    (y, pre); pre = x W^T + bias (for the backward) is None unless wanted or given."""
+    return _product_fwd("mamba3_linear_fwd", False, x, W, bias, residual, act, y, pre, want_pre, workspace, stream)
+
+
+def mamba3_linear_bwd(x, W, dy, pre=None, *, act=M3_ACT_NONE, want_dx=True, want_dW=True, want_dbias=True, dx=None,
+                      dW=None, dbias=None, workspace=None, stream=None):
+    """Backward of linear_fwd.  Returns a dict with dx, dW (io dtype) and dbias
+    (fp32), as wanted.  pre is required unless act is M3_ACT_NONE."""
+    return _product_bwd("mamba3_linear_bwd", False, x, W, dy, pre, act, want_dx, want_dW, want_dbias, dx, dW, dbias,
+                        workspace, stream)
+
+
+def mamba3_gated_ffn_fwd(x, W, bias=None, *, act=M3_ACT_SILU, h=None, pre=None, want_pre=False, workspace=None,
+                         stream=None):
+    """act(g) u with [g u] = x W^T + bias for x (..., d_in), W (2F, d_in): the
+    gate's rows, then the other F.  Returns (h, pre); pre (..., 2F) (for the
+    backward) is None unless wanted or given."""
+    return _product_fwd("mamba3_gated_ffn_fwd", True, x, W, bias, None, act, h, pre, want_pre, workspace, stream)
+
+
+def mamba3_gated_ffn_bwd(x, W, dh, pre, *, act=M3_ACT_SILU, want_dx=True, want_dW=True, want_dbias=True, dx=None,
+                         dW=None, dbias=None, workspace=None, stream=None):
+    """Backward of gated_ffn_fwd.  Returns a dict with dx, dW (io dtype) and
+    dbias (2F, fp32), as wanted."""
+    return _product_bwd("mamba3_gated_ffn_bwd", True, x, W, dh, pre, act, want_dx, want_dW, want_dbias, dx, dW, dbias,
+                        workspace, stream)
+
+
 chunked_fwd = mamba3_ssm_chunked_fwd
 chunked_fwd_noalloc = mamba3_ssm_chunked_fwd_noalloc
 chunked_bwd = mamba3_ssm_chunked_bwd
 decode_step = mamba3_ssm_decode_step
 rope_bc = mamba3_rope_bc
 bc_prologue = mamba3_bc_prologue
+layer_norm_fwd = mamba3_layer_norm_fwd
+layer_norm_bwd = mamba3_layer_norm_bwd
+linear_fwd = mamba3_linear_fwd
+linear_bwd = mamba3_linear_bwd
+gated_ffn_fwd = mamba3_gated_ffn_fwd
+gated_ffn_bwd = mamba3_gated_ffn_bwd
