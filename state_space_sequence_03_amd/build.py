@@ -21,7 +21,9 @@ LIB = os.path.join(HERE, "libmamba3_ssm.so")
 FLOOR_LIB = os.path.join(HERE, "libm3_floor.so")
 FLOOR_SOURCES = ["floor.hip"]
 SOURCES = ["abi.cpp", "decode.hip", "rope.hip", "chunk.hip", "chunk_fast.hip", "chunk_subwalk.hip", "segments.hip", "backward.hip", "prologue.hip", "short_chunk.hip", "noalloc.cpp",
-           "block_abi.cpp", "norm.hip", "linear.hip", "act_bwd.hip"]
+           "block_abi.cpp", "norm.hip", "linear.hip", "act_bwd.hip",
+           "mm_store_bf16.hip", "mm_store_f32.hip", "mm_linear_bf16.hip", "mm_linear_f32.hip", "mm_gated_bf16.hip",
+           "mm_gated_f32.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",
          "-packed-fp32-ops", "-Wno-unused-result", "-I", os.path.join(ROOT, "include")]

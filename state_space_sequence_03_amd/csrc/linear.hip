@@ -1,30 +1,11 @@
 // Matrix products of the linear and gated feed-forward operators:
 //   out[m][n] = epilogue(sum_k P(m, k) Q(n, k)).
-#include "act.hpp"
-#include "m3_launch.hpp"
-#include "m3_rows.hpp"
+#include "mm_tile.hpp"
+#include "mm_parts.hpp"
 
 namespace m3 {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 namespace {
-
-// acc += the product over the 32 bytes of k that a fragment pair holds: lane
-// l carries row l mod 32 of its operand and 16 of those bytes, chunk l / 32.
-template <typename T>
-__device__ __forceinline__ void mma32(const uint4& p, const uint4& q, f32x16& acc);
-template <>
-__device__ __forceinline__ void mma32<bf16_t>(const uint4& p, const uint4& q, f32x16& acc) {
-  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(p), as_bf16x8(q), acc, 0, 0, 0);
-}
-template <>
-__device__ __forceinline__ void mma32<float>(const uint4& p, const uint4& q, f32x16& acc) {
-  acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.x), __uint_as_float(q.x), acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.y), __uint_as_float(q.y), acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.z), __uint_as_float(q.z), acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.w), __uint_as_float(q.w), acc, 0, 0, 0);
-}
 
 template <typename T>
 __device__ __forceinline__ void move1(void* dst, int64_t i, const void* src, int64_t j, bool in) {
@@ -73,7 +54,7 @@ __global__ __launch_bounds__(256) void mm_kernel(MmArgs a) {
     for (int s = 0; s < BK * ES / 32; ++s) {
       const uint4 p = *(const uint4*)(Ps + ((wave & 1) * 32 + r) * PITCH * ES + (2 * s + h) * 16);
       const uint4 q = *(const uint4*)(Qs + ((wave >> 1) * 32 + r) * PITCH * ES + (2 * s + h) * 16);
-      mma32<T>(q, p, acc);
+      acc = mma32<T>(q, p, acc);
     }
   }
   // lane l holds output row l mod 32 and columns 8(v / 4) + 4(l / 32) + v mod 4
@@ -126,6 +107,15 @@ hipError_t mm_run(MmLayout layout, MmEpilogue epi, const MmArgs& a, hipStream_t 
 }  // namespace
 
 hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, hipStream_t s) {
+  const int es = io_bf16 ? 2 : 4;
+  auto on16 = [&](const void* p, int64_t ld, int64_t width) {
+    return ((uintptr_t)p & 15) == 0 && ld * es % 16 == 0 && width * es % 16 == 0;
+  };
+  if (on16(a.P, a.ldp, layout == MM_NONE_K ? a.M : a.K) && on16(a.Q, a.ldq, layout == MM_PQ_K ? a.K : a.N)) {
+    if (epi == MM_STORE) return io_bf16 ? mm_store_bf16(layout, a, s) : mm_store_f32(layout, a, s);
+    if (epi == MM_LINEAR) return io_bf16 ? mm_linear_bf16(a, s) : mm_linear_f32(a, s);
+    return io_bf16 ? mm_gated_bf16(a, s) : mm_gated_f32(a, s);
+  }
   return io_bf16 ? mm_run<bf16_t>(layout, epi, a, s) : mm_run<float>(layout, epi, a, s);
 }
 

@@ -1,0 +1,11 @@
+// Tiled products with the gated epilogue, f32 io.
+#include "mm_parts.hpp"
+#include "mm_tile.hpp"
+
+namespace m3 {
+
+hipError_t mm_gated_f32(const MmArgs& a, hipStream_t s) {
+  return with_act(a.act, [&](auto act) { return mm_tile_run<float, MM_PQ_K, MM_GATED, act.value>(a, s); });
+}
+
+}  // namespace m3

@@ -1,0 +1,11 @@
+// Tiled products with the linear epilogue, bf16 io.
+#include "mm_parts.hpp"
+#include "mm_tile.hpp"
+
+namespace m3 {
+
+hipError_t mm_linear_bf16(const MmArgs& a, hipStream_t s) {
+  return with_act(a.act, [&](auto act) { return mm_tile_run<bf16_t, MM_PQ_K, MM_LINEAR, act.value>(a, s); });
+}
+
+}  // namespace m3

@@ -1,0 +1,13 @@
+// Tiled products of the backward (no epilogue), bf16 io.
+#include "mm_parts.hpp"
+#include "mm_tile.hpp"
+
+namespace m3 {
+
+hipError_t mm_store_bf16(MmLayout layout, const MmArgs& a, hipStream_t s) {
+  if (layout == MM_P_K) return mm_tile_run<bf16_t, MM_P_K, MM_STORE, ACT_NONE>(a, s);
+  if (layout == MM_NONE_K) return mm_tile_run<bf16_t, MM_NONE_K, MM_STORE, ACT_NONE>(a, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace m3

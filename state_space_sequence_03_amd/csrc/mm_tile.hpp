@@ -1,0 +1,440 @@
+// Tiled matrix products out[m][n] = epilogue(sum_k P(m, k) Q(n, k)) for
+// operands whose rows lie on 16 bytes.
+#pragma once
+
+#include "act.hpp"
+#include "m3_launch.hpp"
+#include "m3_rows.hpp"
+
+namespace m3 {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// acc += the product over the 32 bytes of k that a fragment pair holds: lane
+// l carries row l mod 32 of its operand and 16 of those bytes, chunk l / 32.
+// For fp32 the four words of a lane go to four products, whose k are those of
+// both halves' same word: any order of k is right when both operands share it.
+template <typename T>
+__device__ __forceinline__ f32x16 mma32(const uint4& p, const uint4& q, f32x16 acc) {
+  if constexpr (io<T>::BYTES == 2) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(p), as_bf16x8(q), acc, 0, 0, 0);
+  } else {
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.x), __uint_as_float(q.x), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.y), __uint_as_float(q.y), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.z), __uint_as_float(q.z), acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(p.w), __uint_as_float(q.w), acc, 0, 0, 0);
+  }
+}
+
+// Fragment reads.  The pointers are restrict-qualified so that the compiler
+// does not hold these reads back until every load into LDS still in flight
+// has landed: which stage they read has been published by the kernel's own
+// wait and barrier.
+__device__ __forceinline__ u32x4 read16(const u32x4* __restrict p) { return *p; }
+__device__ __forceinline__ uint32_t read4(const uint32_t* __restrict p) { return *p; }
+__device__ __forceinline__ uint2 read_tr(const void* __restrict p) { return lds_tr16(p); }
+
+// One operand's tile of ROWS rows (of m or n) and 128 bytes of k per stage:
+// where its pieces lie in memory, in LDS and in a wave's fragments.
+//
+// KC (rows run along k): LDS holds ROWS rows of 128 bytes, 16-byte chunk c of
+// row r at chunk c ^ fsw(r), so that the 32 rows of a fragment read fall into
+// distinct bank groups.
+// Otherwise (rows of memory run along m or n): LDS holds 128 / ES rows of k,
+// each ROWS elements wide.  bf16 fragments come out of the transpose read,
+// chunk c of row k stored at c ^ 4 (k mod 4), so that the four rows a 16-lane
+// group addresses fall into distinct banks; fp32 fragments are four words.
+template <typename T, bool KC, int ROWS>
+struct Operand {
+  static constexpr int ES = io<T>::BYTES;
+  static constexpr int BK = 128 / ES;          // k per stage
+  static constexpr int BYTES = ROWS * 128;     // per stage
+  static constexpr int NI = BYTES / 4096;      // 1 KB loads per wave and stage
+  static constexpr int LPR = KC ? 8 : ROWS * ES / 16;  // lanes per row of LDS
+  static constexpr int RPI = 64 / LPR;         // rows per 1 KB load
+
+  int voff;   // lane's byte offset within the tile
+  int kpos;   // KC: lane's first byte of k within the stage
+  int ldb;
+
+  __device__ __forceinline__ void init(int64_t ld, int lane, int wave) {
+    ldb = (int)(ld * ES);
+    const int row = wave * RPI + lane / LPR, slot = lane % LPR;
+    int chunk = slot;
+    if constexpr (KC) chunk = slot ^ fsw<8>(row);  // rows 32 apart share it
+    else if constexpr (ES == 2) chunk = slot ^ ((row & 3) << 2);  // rows 4 RPI apart share it
+    kpos = chunk * 16;
+    voff = row * ldb + chunk * 16;
+  }
+  // Loads of stage kb into LDS, straight from memory (one wave instruction
+  // fills 1 KB, lane l's 16 bytes at l * 16).  `base` is the tile's first
+  // element: row 0 of the tile at k = 0 (KC), or the tile's first column at
+  // k = 0.  `rows`: rows of the tile that exist; what lies past them or past
+  // K reads as zero.  Instructions [I0, I1) of the stage.
+  template <int I0, int I1>
+  __device__ __forceinline__ void load(const char* base, int64_t rows, int64_t K, int kb, char* lds, int wave) const {
+    if constexpr (KC) {
+      const int64_t n = rows < (I1 - I0) * 4 * RPI ? rows : (I1 - I0) * 4 * RPI;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)base, 0, (uint32_t)((n - 1) * ldb + K * ES), 0x00020000);
+      const int vo = kpos < (int)(K * ES) - kb * 128 ? voff : 0x7ff00000;
+#pragma unroll
+      for (int i = I0; i < I1; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * 4 + wave) * 1024), 16, vo,
+                                                 (i - I0) * 4 * RPI * ldb + kb * 128, 0, 0);
+    } else {
+      const int64_t all = (int64_t)kb * BK, k0 = all < K ? all : K;
+      const int left = K - k0 < BK ? (int)(K - k0) : BK;
+      const int bytes = (left - 1) * ldb + (int)(rows * ES);  // at most 0 where nothing is left
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(base + k0 * ldb), 0, bytes > 0 ? bytes : 0, 0x00020000);
+#pragma unroll
+      for (int i = I0; i < I1; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * 4 + wave) * 1024), 16, voff,
+                                                 i * 4 * RPI * ldb, 0, 0);
+    }
+  }
+};
+
+// A wave's fragments of one operand: NT tiles of 32 rows from row r0 of the
+// tile (tiles t >= NT / 2 lie GAP rows further, the second half of a gated
+// block's rows).
+template <typename T, bool KC, int ROWS, int NT, int GAP>
+struct Fragments {
+  static constexpr int ES = io<T>::BYTES;
+  static constexpr int NB = KC ? 4 : (ES == 2 ? 4 : 1);
+  int at[NB];  // KC: per k-step of 32 bytes; transposed: per tile position
+
+  __device__ __forceinline__ void init(int r0, int lane) {
+    if constexpr (KC) {
+      const int r = lane & 31, h = lane >> 5, f = fsw<8>(r);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) at[s] = (r0 + r) * 128 + (((2 * s + h) ^ f) << 4);
+    } else if constexpr (ES == 2) {
+      const int g = lane >> 4, i = lane & 15, q = i >> 2;
+      const int row = 8 * (g >> 1) + q, c = (g & 1) * 2 + ((i & 3) >> 1);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        at[t] = row * ROWS * 2 + ((((r0 / 32 + t) ^ q) * 4 + c) << 4) + (i & 1) * 8;
+    } else {
+      at[0] = (4 * (lane >> 5)) * ROWS * 4 + (r0 + (lane & 31)) * 4;
+    }
+  }
+  // fragment of tile t, k-step s (32 bytes of k)
+  __device__ __forceinline__ uint4 read(const char* lds, int t, int s) const {
+    const int tt = t * 32 + (t >= NT / 2 ? GAP : 0);
+    if constexpr (KC) {
+      return __builtin_bit_cast(uint4, read16((const u32x4*)(lds + at[s] + tt * 128)));
+    } else if constexpr (ES == 2) {
+      const char* p = lds + at[t & 3] + s * 16 * ROWS * 2;
+      const uint2 a = read_tr(p), b = read_tr(p + 4 * ROWS * 2);
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      const char* p = lds + at[0] + s * 8 * ROWS * 4 + tt * 4;
+      return make_uint4(read4((const uint32_t*)p), read4((const uint32_t*)(p + ROWS * 4)),
+                        read4((const uint32_t*)(p + 2 * ROWS * 4)), read4((const uint32_t*)(p + 3 * ROWS * 4)));
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Epilogue of one 32 x 32 tile: lane l holds row m = m0 + l mod 32 and, in
+// v[4q + j], column n0 + 8q + 4 (l / 32) + j.  For bf16 the halves of the wave
+// exchange every second quadruple, so that a lane stores 8 columns (16 bytes)
+// at a time: columns 16p + 8 (l / 32) .. + 7.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = s[0];
+  b = s[1];
+}
+
+template <typename T>
+__device__ __forceinline__ void tile_store(char* row, bool in, int64_t n0, int64_t N, const float* v, int h) {
+  if constexpr (io<T>::BYTES == 2) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t a0 = pack_bf2(v[8 * p], v[8 * p + 1]), a1 = pack_bf2(v[8 * p + 2], v[8 * p + 3]);
+      uint32_t b0 = pack_bf2(v[8 * p + 4], v[8 * p + 5]), b1 = pack_bf2(v[8 * p + 6], v[8 * p + 7]);
+      swap_halves(a0, b0);
+      swap_halves(a1, b1);
+      const int64_t n = n0 + 16 * p + 8 * h;
+      const u32x4 o = {a0, a1, b0, b1};
+      if (in && n + 8 <= N) {
+        *(u32x4_any*)(row + n * 2) = o;
+      } else if (in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n + j < N) ((u16*)row)[n + j] = (u16)(o[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  } else {
+    typedef f32x4 f32x4_any __attribute__((aligned(4)));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t n = n0 + 8 * q + 4 * h;
+      if (in && n + 4 <= N) {
+        *(f32x4_any*)(row + n * 4) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      } else if (in) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < N) ((float*)row)[n + j] = v[4 * q + j];
+      }
+    }
+  }
+}
+
+// v += the row's entries of a matrix of the io type
+template <typename T>
+__device__ __forceinline__ void tile_add(const char* row, bool in, int64_t n0, int64_t N, float* v, int h) {
+  if constexpr (io<T>::BYTES == 2) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int64_t n = n0 + 16 * p + 8 * h;
+      u32x4 o = {0u, 0u, 0u, 0u};
+      if (in && n + 8 <= N) {
+        o = *(const u32x4_any*)(row + n * 2);
+      } else if (in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n + j < N) o[j >> 1] |= (uint32_t)((const u16*)row)[n + j] << (16 * (j & 1));
+      }
+      uint32_t a0 = o[0], a1 = o[1], b0 = o[2], b1 = o[3];
+      swap_halves(a0, b0);
+      swap_halves(a1, b1);
+      v[8 * p] += bf_lo(a0); v[8 * p + 1] += bf_hi(a0); v[8 * p + 2] += bf_lo(a1); v[8 * p + 3] += bf_hi(a1);
+      v[8 * p + 4] += bf_lo(b0); v[8 * p + 5] += bf_hi(b0); v[8 * p + 6] += bf_lo(b1); v[8 * p + 7] += bf_hi(b1);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = n0 + 8 * q + 4 * h + j;
+        if (in && n < N) v[4 * q + j] += ((const float*)row)[n];
+      }
+  }
+}
+
+// v += bias (the same for every row)
+__device__ __forceinline__ void tile_bias(const float* bias, int64_t n0, int64_t N, float* v, int h) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = n0 + 8 * q + 4 * h + j;
+      v[4 * q + j] += bias[n < N ? n : N - 1];
+    }
+}
+
+// The epilogue of one tile (u: the second half's values of a gated block).
+template <typename T, int EPI, int ACT>
+__device__ __forceinline__ void tile_epilogue(const MmArgs& a, int64_t m, int64_t n0, float* z, float* u, int h) {
+  constexpr int ES = io<T>::BYTES;
+  constexpr bool FINE = ES == 4;
+  const bool in = m < a.M;
+  const int64_t mc = in ? m : a.M - 1;
+  if (n0 >= a.N) return;
+  if constexpr (EPI == MM_LINEAR) {
+    if (a.bias) tile_bias(a.bias, n0, a.N, z, h);
+    if (a.pre) tile_store<T>((char*)a.pre + mc * a.N * ES, in, n0, a.N, z, h);
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]);
+    if (a.res) tile_add<T>((const char*)a.res + mc * a.ldr * ES, in, n0, a.N, z, h);
+  }
+  if constexpr (EPI == MM_GATED) {
+    if (a.bias) {
+      tile_bias(a.bias, n0, a.N, z, h);
+      tile_bias(a.bias + a.N, n0, a.N, u, h);
+    }
+    if (a.pre) {
+      char* row = (char*)a.pre + mc * 2 * a.N * ES;
+      tile_store<T>(row, in, n0, a.N, z, h);
+      tile_store<T>(row + a.N * ES, in, n0, a.N, u, h);
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]) * u[v];
+  }
+  tile_store<T>((char*)a.out + mc * a.ldo * ES, in, n0, a.N, z, h);
+}
+
+// Instruction order of a k-step: the LDS reads for the next one spread over
+// the first half of its matrix instructions (so that they have arrived by its
+// end), the loads of a later stage over the second half.
+template <int MASK, int STEPS, int COUNT, int I = 0>
+__device__ __forceinline__ void mix() {  // COUNT instructions of the kind over STEPS products
+  if constexpr (I < STEPS) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int N = (I + 1) * COUNT / STEPS - I * COUNT / STEPS;
+    if constexpr (N > 0) __builtin_amdgcn_sched_group_barrier(MASK, N, 0);
+    mix<MASK, STEPS, COUNT, I + 1>();
+  }
+}
+template <int NM, int NR, int NL>
+__device__ __forceinline__ void mix_k_step() {
+  mix<0x100, NM / 2, NR>();
+  mix<0x010, NM - NM / 2, NL>();
+}
+
+// ---------------------------------------------------------------------------
+// The tiled kernel: BM x BN outputs per block (gated: BN / 2 columns of each
+// half), four waves, each BM / 2 x BN / 2 of them on 32 x 32 products, one
+// wave per SIMD for the 256 x 256 tile (256 accumulators).
+//
+// k advances by 128 bytes per stage through two stages of LDS.  A stage has
+// four k-steps of 32 bytes; a wave reads the fragments of the next k-step
+// while the products of this one run, across the stage's end too: after the
+// third k-step every wave holds the fragments of the fourth in registers, so
+// one barrier there frees this stage's LDS for the loads of the stage after
+// next (which so have a whole stage's products to land in) and publishes the
+// next stage, whose first fragments are read under the fourth k-step's
+// products.
+// ---------------------------------------------------------------------------
+template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs a, int ntm, int ntn) {
+  constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
+  constexpr int ES = io<T>::BYTES;
+  constexpr bool G = EPI == MM_GATED;
+  constexpr int MT = BM / 64, NT = BN / 64;  // 32 x 32 tiles of a wave
+  constexpr int BC = G ? BN / 2 : BN;        // columns of out per block
+  typedef Operand<T, PK, BM> OP;
+  typedef Operand<T, QK, BN> OQ;
+  constexpr int STAGE = OP::BYTES + OQ::BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+
+  // Tile order: workgroups go to the 8 XCDs in turn; each XCD gets a
+  // contiguous run of an order that walks groups of 4 rows of tiles, so that
+  // its 32 blocks in flight share about 4 + 8 operand tiles in its L2.
+  const int total = ntm * ntn, xcd = blockIdx.x & 7, per = total >> 3, more = total & 7;
+  const int id = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
+  const int group = id / (4 * ntn), first = group * 4, rows = ntm - first < 4 ? ntm - first : 4;
+  const int rest = id - group * 4 * ntn;
+  const int64_t m0 = (int64_t)(first + rest % rows) * BM, n0 = (int64_t)(rest / rows) * BC;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  OP op;
+  OQ oq;
+  op.init(a.ldp, lane, wave);
+  oq.init(a.ldq, lane, wave);
+  const char* pb = (const char*)a.P + (PK ? m0 * a.ldp : m0) * ES;
+  const char* qb = (const char*)a.Q + (QK ? n0 * a.ldq : n0) * ES;
+  const char* qb2 = (const char*)a.Q + (a.N + n0) * a.ldq * ES;  // gated: the second half's rows
+  const int64_t pr = a.M - m0, qr = a.N - n0;
+  auto load = [&](int kb, int at) {
+    char* l = smem + at;
+    op.template load<0, OP::NI>(pb, pr, a.K, kb, l, wave);
+    if constexpr (G) {
+      oq.template load<0, OQ::NI / 2>(qb, qr, a.K, kb, l + OP::BYTES, wave);
+      oq.template load<OQ::NI / 2, OQ::NI>(qb2, qr, a.K, kb, l + OP::BYTES, wave);
+    } else {
+      oq.template load<0, OQ::NI>(qb, qr, a.K, kb, l + OP::BYTES, wave);
+    }
+  };
+  Fragments<T, PK, BM, MT, 0> fp;
+  Fragments<T, QK, BN, NT, G ? BN / 4 : 0> fq;
+  fp.init(wm * (BM / 2), lane);
+  fq.init(G ? wn * (BN / 4) : wn * (BN / 2), lane);
+
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  // of one k-step: matrix instructions and LDS reads
+  constexpr int NM = MT * NT * (ES == 2 ? 1 : 4);
+  constexpr int NR = MT * (PK ? 1 : ES == 2 ? 2 : 4) + NT * (QK ? 1 : ES == 2 ? 2 : 4);
+  const int nk = (int)((a.K + OP::BK - 1) / OP::BK);
+  uint4 p[2][MT], q[2][NT];
+  auto read = [&](int at, int s, int to) {
+    const char* l = smem + at;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) p[to][j] = fp.read(l, j, s);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) q[to][i] = fq.read(l + OP::BYTES, i, s);
+  };
+  auto multiply = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
+  };
+  auto stage = [&](int kb, auto cur) {
+    constexpr int B = decltype(cur)::value;
+    read(B * STAGE, 1, 1);
+    multiply(0);
+    mix_k_step<NM, NR, 0>();
+    read(B * STAGE, 2, 0);
+    multiply(1);
+    mix_k_step<NM, NR, 0>();
+    read(B * STAGE, 3, 1);
+    multiply(0);
+    mix_k_step<NM, NR, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    read((B ^ 1) * STAGE, 0, 0);
+    load(kb + 2, B * STAGE);
+    multiply(1);
+    mix_k_step<NM, NR, OP::NI + OQ::NI>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // an odd count of stages starts in the second buffer, so that the buffers
+  // of the loop's two stages are constants
+  const int odd = nk & 1;
+  load(0, odd * STAGE);
+  load(1, (odd ^ 1) * STAGE);
+  constexpr int NL = OP::NI + OQ::NI;  // loads of a stage
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (NL & 15) | (NL >> 4) << 14);  // stage 0 has landed
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(odd * STAGE, 0, 0);
+  if (odd) stage(0, std::integral_constant<int, 1>{});
+  for (int kb = odd; kb < nk; kb += 2) {
+    stage(kb, std::integral_constant<int, 0>{});
+    stage(kb + 1, std::integral_constant<int, 1>{});
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last stage (zeros) have landed
+
+  const int h = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t m = m0 + wm * (BM / 2) + j * 32 + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < (G ? NT / 2 : NT); ++i) {
+      float z[16], u[16];
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        z[v] = acc[i][j][v];
+        u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
+      }
+      tile_epilogue<T, EPI, ACT>(a, m, n0 + wn * (BC / 2) + i * 32, z, u, h);
+    }
+  }
+}
+
+template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
+hipError_t mm_tile_launch(const MmArgs& a, hipStream_t s) {
+  const int bc = EPI == MM_GATED ? BN / 2 : BN;
+  const int64_t ntm = (a.M + BM - 1) / BM, ntn = (a.N + bc - 1) / bc;
+  hipLaunchKernelGGL((mm_tile_kernel<T, LAYOUT, EPI, ACT, BM, BN>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, s, a,
+                     (int)ntm, (int)ntn);
+  return hipGetLastError();
+}
+
+template <typename T, int LAYOUT, int EPI, int ACT>
+hipError_t mm_tile_run(const MmArgs& a, hipStream_t s) {
+  const int bc = EPI == MM_GATED ? 128 : 256;
+  const int64_t t256 = ((a.M + 255) / 256) * ((a.N + bc - 1) / bc);
+  if (t256 >= 192) return mm_tile_launch<T, LAYOUT, EPI, ACT, 256, 256>(a, s);
+  return mm_tile_launch<T, LAYOUT, EPI, ACT, 128, 128>(a, s);
+}
+
+}  // namespace m3
