@@ -332,9 +332,14 @@ size_t mamba3_bc_prologue_workspace_size(const m3_dims* d);
  * count elements from row to row, 0 stands for contiguous rows, and a stride
  * below the width is M3_ERR_SHAPE.  Every other operand is contiguous.
  *
- * Any row count from 0, any width from 1, odd ones included: no alignment
- * beyond the element's is required of any pointer.  Rows that lie on 16 bytes
- * (pointer, stride and width) are read the fastest.  Limits
+ * Any row count from 0, any width from 1, odd ones included.  The products
+ * read x, W and dy (as dP) 16 bytes at a time; where a width or stride of them
+ * is no multiple of 16 bytes they are first copied into the workspace, so such
+ * sizes cost a pass over those operands.  Alignment: x and W, and dy of
+ * linear_bwd with M3_ACT_NONE, 16 bytes where their rows lie on 16 bytes,
+ * unless flags holds M3_FLAG_UNALIGNED, which makes the call copy them (the
+ * workspace queries count it in); every other pointer its element's size,
+ * the workspaces 16.  Limits
  * (M3_ERR_UNSUPPORTED): widths and strides at most 2^20, rows at most 2^24,
  * and at most 2^24 - 1 tiles of 64 x 64 outputs in any product of a call.
  * With rows = 0 nothing is read and no row written; gradients summed over the
@@ -343,6 +348,7 @@ size_t mamba3_bc_prologue_workspace_size(const m3_dims* d);
  * Outputs must not alias inputs, save y over residual and dx over dskip (same
  * strides).  Results do not depend on the launch's timing: every sum is taken
  * in a fixed order. */
+#define M3_FLAG_UNALIGNED 0x40000
 typedef enum {
   M3_ACT_NONE = 0,
   M3_ACT_RELU = 1,      /* max(z, 0); derivative 0 at 0 */
@@ -392,7 +398,7 @@ typedef struct {
   int64_t residual_stride; /* of residual (linear_fwd only) */
   int32_t io_dtype;
   int32_t act;             /* m3_act */
-  int32_t flags;           /* must be 0 */
+  int32_t flags;           /* 0 or M3_FLAG_UNALIGNED */
   int32_t reserved;        /* must be 0 */
 } m3_linear_dims;
 
@@ -400,8 +406,9 @@ typedef struct {
  * W: (N, K).  bias: nullable (N).  residual: nullable (M, N).
  * pre: nullable (M, N), written when given (the backward takes it for any
  * activation but M3_ACT_NONE).
- * workspace: at least mamba3_linear_fwd_workspace_size(d) bytes (fp32 partial
- * sums of products whose K is split over several blocks; may be 0). */
+ * workspace: at least mamba3_linear_fwd_workspace_size(d) bytes (copies of x
+ * and W where their rows need them, fp32 partial sums of tiles whose K is
+ * split over several blocks; may be 0); contents on entry do not matter. */
 m3_status mamba3_linear_fwd(const m3_linear_dims* d, const void* x, const void* W, const float* bias,
                             const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
                             void* stream);
@@ -411,8 +418,8 @@ size_t mamba3_linear_fwd_workspace_size(const m3_linear_dims* d);
  * rows of dP (the residual's gradient is dy itself).
  * pre: required unless act is M3_ACT_NONE (then ignored).  dx (M, K), dW
  * (N, K), dbias (N): nullable, each by itself; x is needed for dW, W for dx.
- * workspace: at least mamba3_linear_bwd_workspace_size(d) bytes (dP, partial
- * sums). */
+ * workspace: at least mamba3_linear_bwd_workspace_size(d) bytes (dP, copies,
+ * partial sums), whichever gradients are asked for. */
 m3_status mamba3_linear_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre, const void* dy,
                             void* dx, void* dW, float* dbias, void* workspace, size_t workspace_bytes,
                             void* stream);

@@ -51,9 +51,11 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int64_t slab
         s[0][j] += d[j];
       }
       if (a.dp) {
-        char* dp = (char*)a.dp + r * ld * io<T>::BYTES;
+        char* dp = (char*)a.dp + r * a.ldp * io<T>::BYTES;
         row_store<T>(dp, c, C, d);
         if constexpr (GATED) row_store<T>(dp + C * io<T>::BYTES, c, C, z);
+        if (c + V >= C)
+          for (int64_t k = ld; k < a.ldp; ++k) io<T>::store1(dp, k, 0.0f);
       }
     }
   if (!a.part) return;
@@ -90,7 +92,33 @@ __global__ __launch_bounds__(256) void zero_kernel(u16* dst, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) dst[i] = 0;
 }
 
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
+  constexpr int V = io<T>::VEC;
+  const auto& m = a.m[blockIdx.y];
+  const int64_t vecs = m.ld / V, n = m.rows * vecs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / vecs, c = (i - r * vecs) * V;
+    float f[V];
+    row_load<T>((const char*)m.src + r * m.src_ld * io<T>::BYTES, c, m.width, f);
+    stg16<T>(m.dst, r * m.ld + c, io<T>::pack(f));
+  }
+}
+
 }  // namespace
+
+hipError_t launch_pack(int io_bf16, const PackArgs& a, hipStream_t s) {
+  if (a.count == 0) return hipSuccess;
+  int64_t most = 1;
+  for (int i = 0; i < a.count; ++i) {
+    const int64_t blocks = (a.m[i].rows * (a.m[i].ld / (io_bf16 ? 8 : 4)) + 255) / 256;
+    if (blocks > most) most = blocks;
+  }
+  const dim3 grid((unsigned)(most < 4096 ? most : 4096), (unsigned)a.count);
+  if (io_bf16) hipLaunchKernelGGL((pack_kernel<bf16_t>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((pack_kernel<float>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
 
 hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s) {
   const int64_t blocks = (bytes / 2 + 255) / 256;

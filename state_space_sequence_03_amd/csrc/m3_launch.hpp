@@ -193,17 +193,46 @@ struct MmArgs {
   int64_t ldr;
   void* pre;  // nullable, contiguous
   int act;
+  float* part;  // workspace of plan.part_bytes
 };
-hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, hipStream_t s);
+// How a product is cut: tiles of `tile` x `tile` outputs (0: the few-row
+// kernel), the first `full` of them whole, the others split over k into
+// `split` parts of `stages` stages of 128 bytes, which a second kernel joins.
+struct MmPlan {
+  int tile, ntm, ntn, full, split;
+  int stages, whole;  // stages of a part and of a whole tile (both even)
+  int items;          // full + split parts
+  size_t part_bytes;
+};
+template <int BM>
+constexpr int MmTileBlocks = BM == 256 ? 1 : BM == 128 ? 2 : 4;  // resident per CU
+MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K);
+// The tiled kernels need rows of P and Q that start on 16 bytes; a row along
+// k whose last 16 bytes are partial must be backed by zeros up to there.
+hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, const MmPlan& plan, hipStream_t s);
+// The few-row kernel (rows of P and Q along k) takes any alignment.
+constexpr int MM_FEW_ROWS = 64;
+
+// Copies of up to three matrices with rows padded by zeros to `ld` elements
+// (a multiple of 16 bytes).
+struct PackArgs {
+  struct {
+    const void* src;
+    void* dst;
+    int64_t rows, width, src_ld, ld;
+  } m[3];
+  int count;
+};
+hipError_t launch_pack(int io_bf16, const PackArgs& a, hipStream_t s);
 
 // dP of the linear (gated = 0: dy act'(pre)) or gated (dy u act'(g), dy act(g))
 // operator, and the partial column sums of it.
 struct ActBwdArgs {
   const void* pre;  // (rows, cols or 2 cols); null when act is none and gated is 0
   const void* dy;   // row stride ldy
-  void* dp;         // nullable: as pre
+  void* dp;         // nullable: as pre, rows ldp apart, padded by zeros
   float* part;      // nullable: (act_bwd_parts(rows), cols or 2 cols)
-  int64_t rows, cols, ldy;
+  int64_t rows, cols, ldy, ldp;
   int act, gated;
 };
 int64_t act_bwd_parts(int64_t rows);

@@ -1,11 +1,15 @@
-// Tiled products with the linear epilogue, bf16 io.
+// Products with the linear epilogue, bf16 io.
+#include "mm_few.hpp"
 #include "mm_parts.hpp"
 #include "mm_tile.hpp"
 
 namespace m3 {
 
-hipError_t mm_linear_bf16(const MmArgs& a, hipStream_t s) {
-  return with_act(a.act, [&](auto act) { return mm_tile_run<bf16_t, MM_PQ_K, MM_LINEAR, act.value>(a, s); });
+hipError_t mm_linear_bf16(const MmArgs& a, const MmPlan& plan, hipStream_t s) {
+  return with_act(a.act, [&](auto act) {
+    return plan.tile == 0 ? mm_few_run<bf16_t, MM_LINEAR, act.value>(a, s)
+                          : mm_tile_run<bf16_t, MM_PQ_K, MM_LINEAR, act.value>(a, plan, s);
+  });
 }
 
 }  // namespace m3

@@ -1,12 +1,12 @@
-// Tiled products of the backward (no epilogue), f32 io.
+// Products of the backward (no epilogue), f32 io.
 #include "mm_parts.hpp"
 #include "mm_tile.hpp"
 
 namespace m3 {
 
-hipError_t mm_store_f32(MmLayout layout, const MmArgs& a, hipStream_t s) {
-  if (layout == MM_P_K) return mm_tile_run<float, MM_P_K, MM_STORE, ACT_NONE>(a, s);
-  if (layout == MM_NONE_K) return mm_tile_run<float, MM_NONE_K, MM_STORE, ACT_NONE>(a, s);
+hipError_t mm_store_f32(MmLayout layout, const MmArgs& a, const MmPlan& plan, hipStream_t s) {
+  if (layout == MM_P_K) return mm_tile_run<float, MM_P_K, MM_STORE, ACT_NONE>(a, plan, s);
+  if (layout == MM_NONE_K) return mm_tile_run<float, MM_NONE_K, MM_STORE, ACT_NONE>(a, plan, s);
   return hipErrorInvalidValue;
 }
 

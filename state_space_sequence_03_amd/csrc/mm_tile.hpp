@@ -9,6 +9,7 @@
 namespace m3 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 // acc += the product over the 32 bytes of k that a fragment pair holds: lane
@@ -76,8 +77,10 @@ struct Operand {
   __device__ __forceinline__ void load(const char* base, int64_t rows, int64_t K, int kb, char* lds, int wave) const {
     if constexpr (KC) {
       const int64_t n = rows < (I1 - I0) * 4 * RPI ? rows : (I1 - I0) * 4 * RPI;
+      // a last, partial 16 bytes of k exists in memory (the caller's rows end
+      // on 16 bytes) and holds zeros past K
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)base, 0, (uint32_t)((n - 1) * ldb + K * ES), 0x00020000);
+          (void*)base, 0, (uint32_t)((n - 1) * ldb + ((K * ES + 15) & ~(int64_t)15)), 0x00020000);
       const int vo = kpos < (int)(K * ES) - kb * 128 ? voff : 0x7ff00000;
 #pragma unroll
       for (int i = I0; i < I1; ++i)
@@ -86,7 +89,8 @@ struct Operand {
     } else {
       const int64_t all = (int64_t)kb * BK, k0 = all < K ? all : K;
       const int left = K - k0 < BK ? (int)(K - k0) : BK;
-      const int bytes = (left - 1) * ldb + (int)(rows * ES);  // at most 0 where nothing is left
+      // at most 0 where nothing is left; a partial last 16 bytes exists, as above
+      const int bytes = (left - 1) * ldb + (int)((rows * ES + 15) & ~(int64_t)15);
       const __amdgpu_buffer_rsrc_t rs =
           __builtin_amdgcn_make_buffer_rsrc((void*)(base + k0 * ldb), 0, bytes > 0 ? bytes : 0, 0x00020000);
 #pragma unroll
@@ -150,7 +154,8 @@ __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
   b = s[1];
 }
 
-template <typename T>
+// INNER: every row and column of the tile exists.
+template <typename T, bool INNER>
 __device__ __forceinline__ void tile_store(char* row, bool in, int64_t n0, int64_t N, const float* v, int h) {
   if constexpr (io<T>::BYTES == 2) {
 #pragma unroll
@@ -161,7 +166,7 @@ __device__ __forceinline__ void tile_store(char* row, bool in, int64_t n0, int64
       swap_halves(a1, b1);
       const int64_t n = n0 + 16 * p + 8 * h;
       const u32x4 o = {a0, a1, b0, b1};
-      if (in && n + 8 <= N) {
+      if (INNER || (in && n + 8 <= N)) {
         *(u32x4_any*)(row + n * 2) = o;
       } else if (in) {
 #pragma unroll
@@ -170,11 +175,10 @@ __device__ __forceinline__ void tile_store(char* row, bool in, int64_t n0, int64
       }
     }
   } else {
-    typedef f32x4 f32x4_any __attribute__((aligned(4)));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t n = n0 + 8 * q + 4 * h;
-      if (in && n + 4 <= N) {
+      if (INNER || (in && n + 4 <= N)) {
         *(f32x4_any*)(row + n * 4) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
       } else if (in) {
 #pragma unroll
@@ -185,78 +189,122 @@ __device__ __forceinline__ void tile_store(char* row, bool in, int64_t n0, int64
   }
 }
 
-// v += the row's entries of a matrix of the io type
+// The row's entries of a matrix of the io type, as loaded ...
 template <typename T>
-__device__ __forceinline__ void tile_add(const char* row, bool in, int64_t n0, int64_t N, float* v, int h) {
-  if constexpr (io<T>::BYTES == 2) {
+struct TileRow {
+  static constexpr int NV = io<T>::BYTES == 2 ? 2 : 4;
+  u32x4 o[NV];
+  template <bool INNER>
+  __device__ __forceinline__ void load(const char* row, bool in, int64_t n0, int64_t N, int h) {
+    constexpr int ES = io<T>::BYTES, V = 16 / ES;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int64_t n = n0 + 16 * p + 8 * h;
-      u32x4 o = {0u, 0u, 0u, 0u};
-      if (in && n + 8 <= N) {
-        o = *(const u32x4_any*)(row + n * 2);
+    for (int p = 0; p < NV; ++p) {
+      const int64_t n = n0 + (32 / NV) * p + V * h;
+      o[p] = u32x4{0u, 0u, 0u, 0u};
+      if (INNER || (in && n + V <= N)) {
+        o[p] = *(const u32x4_any*)(row + n * ES);
       } else if (in) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (n + j < N) o[j >> 1] |= (uint32_t)((const u16*)row)[n + j] << (16 * (j & 1));
+        for (int j = 0; j < V; ++j)
+          if (n + j < N) {
+            if constexpr (ES == 2) o[p][j >> 1] |= (uint32_t)((const u16*)row)[n + j] << (16 * (j & 1));
+            else o[p][j] = ((const uint32_t*)row)[n + j];
+          }
       }
-      uint32_t a0 = o[0], a1 = o[1], b0 = o[2], b1 = o[3];
-      swap_halves(a0, b0);
-      swap_halves(a1, b1);
-      v[8 * p] += bf_lo(a0); v[8 * p + 1] += bf_hi(a0); v[8 * p + 2] += bf_lo(a1); v[8 * p + 3] += bf_hi(a1);
-      v[8 * p + 4] += bf_lo(b0); v[8 * p + 5] += bf_hi(b0); v[8 * p + 6] += bf_lo(b1); v[8 * p + 7] += bf_hi(b1);
     }
-  } else {
+  }
+  // ... and added to v
+  __device__ __forceinline__ void add(float* v) const {
+    if constexpr (io<T>::BYTES == 2) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + 8 * q + 4 * h + j;
-        if (in && n < N) v[4 * q + j] += ((const float*)row)[n];
+      for (int p = 0; p < 2; ++p) {
+        uint32_t a0 = o[p][0], a1 = o[p][1], b0 = o[p][2], b1 = o[p][3];
+        swap_halves(a0, b0);
+        swap_halves(a1, b1);
+        v[8 * p] += bf_lo(a0); v[8 * p + 1] += bf_hi(a0); v[8 * p + 2] += bf_lo(a1); v[8 * p + 3] += bf_hi(a1);
+        v[8 * p + 4] += bf_lo(b0); v[8 * p + 5] += bf_hi(b0); v[8 * p + 6] += bf_lo(b1); v[8 * p + 7] += bf_hi(b1);
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * q + j] += __uint_as_float(o[q][j]);
+    }
+  }
+};
+
+// The lane's 16 columns of a bias (the same for every row; 0 without one).
+template <bool INNER>
+__device__ __forceinline__ void tile_bias(const float* bias, int64_t n0, int64_t N, float* b, int h) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = n0 + 8 * q + 4 * h;
+    if (!bias) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[4 * q + j] = 0.0f;
+    } else if (INNER) {
+      const f32x4 x = *(const f32x4_any*)(bias + n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[4 * q + j] = x[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[4 * q + j] = bias[n + j < N ? n + j : N - 1];
+    }
   }
 }
 
-// v += bias (the same for every row)
-__device__ __forceinline__ void tile_bias(const float* bias, int64_t n0, int64_t N, float* v, int h) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + 8 * q + 4 * h + j;
-      v[4 * q + j] += bias[n < N ? n : N - 1];
-    }
-}
-
-// The epilogue of one tile (u: the second half's values of a gated block).
-template <typename T, int EPI, int ACT>
-__device__ __forceinline__ void tile_epilogue(const MmArgs& a, int64_t m, int64_t n0, float* z, float* u, int h) {
+// The epilogue of COUNT tiles below each other (rows 32 apart from m on) in
+// columns n0 .. n0 + 31; get(j, z, u) yields tile j's values (u: the second
+// half's of a gated block).  What has to be loaded is requested first.
+template <typename T, int EPI, int ACT, int COUNT, bool INNER, typename Get>
+__device__ __forceinline__ void tile_column(const MmArgs& a, int64_t m, int64_t n0, int h, Get&& get) {
   constexpr int ES = io<T>::BYTES;
-  constexpr bool FINE = ES == 4;
-  const bool in = m < a.M;
-  const int64_t mc = in ? m : a.M - 1;
-  if (n0 >= a.N) return;
-  if constexpr (EPI == MM_LINEAR) {
-    if (a.bias) tile_bias(a.bias, n0, a.N, z, h);
-    if (a.pre) tile_store<T>((char*)a.pre + mc * a.N * ES, in, n0, a.N, z, h);
+  constexpr bool FINE = ES == 4, G = EPI == MM_GATED;
+  if (!INNER && n0 >= a.N) return;
+  float b0[16], b1[16];
+  TileRow<T> res[COUNT];
+  asm volatile("" ::: "memory");  // this column's loads are not requested earlier: registers
+  if constexpr (EPI != MM_STORE) tile_bias<INNER>(a.bias, n0, a.N, b0, h);
+  if constexpr (G) tile_bias<INNER>(a.bias ? a.bias + a.N : nullptr, n0, a.N, b1, h);
+  if constexpr (EPI == MM_LINEAR)
+    if (a.res) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]);
-    if (a.res) tile_add<T>((const char*)a.res + mc * a.ldr * ES, in, n0, a.N, z, h);
-  }
-  if constexpr (EPI == MM_GATED) {
-    if (a.bias) {
-      tile_bias(a.bias, n0, a.N, z, h);
-      tile_bias(a.bias + a.N, n0, a.N, u, h);
-    }
-    if (a.pre) {
-      char* row = (char*)a.pre + mc * 2 * a.N * ES;
-      tile_store<T>(row, in, n0, a.N, z, h);
-      tile_store<T>(row + a.N * ES, in, n0, a.N, u, h);
+      for (int j = 0; j < COUNT; ++j) {
+        const int64_t r = m + 32 * j;
+        res[j].template load<INNER>((const char*)a.res + (INNER || r < a.M ? r : a.M - 1) * a.ldr * ES, r < a.M, n0,
+                                    a.N, h);
+      }
     }
 #pragma unroll
-    for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]) * u[v];
+  for (int j = 0; j < COUNT; ++j) {
+    const bool in = m + 32 * j < a.M;
+    const int64_t r = INNER || in ? m + 32 * j : a.M - 1;
+    float z[16], u[16];
+    get(j, z, u);
+    if constexpr (EPI == MM_LINEAR) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) z[v] += b0[v];
+      if (a.pre) tile_store<T, INNER>((char*)a.pre + r * a.N * ES, in, n0, a.N, z, h);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]);
+      if (a.res) res[j].add(z);
+    }
+    if constexpr (G) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        z[v] += b0[v];
+        u[v] += b1[v];
+      }
+      if (a.pre) {
+        char* row = (char*)a.pre + r * 2 * a.N * ES;
+        tile_store<T, INNER>(row, in, n0, a.N, z, h);
+        tile_store<T, INNER>(row + a.N * ES, in, n0, a.N, u, h);
+      }
+#pragma unroll
+      for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, FINE>(z[v]) * u[v];
+    }
+    tile_store<T, INNER>((char*)a.out + r * a.ldo * ES, in, n0, a.N, z, h);
   }
-  tile_store<T>((char*)a.out + mc * a.ldo * ES, in, n0, a.N, z, h);
 }
 
 // Instruction order of a k-step: the LDS reads for the next one spread over
@@ -278,9 +326,9 @@ __device__ __forceinline__ void mix_k_step() {
 }
 
 // ---------------------------------------------------------------------------
-// The tiled kernel: BM x BN outputs per block (gated: BN / 2 columns of each
-// half), four waves, each BM / 2 x BN / 2 of them on 32 x 32 products, one
-// wave per SIMD for the 256 x 256 tile (256 accumulators).
+// The tiled kernel: BM x BN outputs per tile (gated: BN / 2 columns of each
+// half), four waves, each BM / 2 x BN / 2 of them on 32 x 32 products; the
+// 256 x 256 tile runs one wave per SIMD with 256 accumulators each.
 //
 // k advances by 128 bytes per stage through two stages of LDS.  A stage has
 // four k-steps of 32 bytes; a wave reads the fragments of the next k-step
@@ -290,27 +338,55 @@ __device__ __forceinline__ void mix_k_step() {
 // next (which so have a whole stage's products to land in) and publishes the
 // next stage, whose first fragments are read under the fourth k-step's
 // products.
+//
+// Blocks stay: each walks several items (a tile, or a tile's part of k), and
+// the stage after an item's last is the next item's first, so that its loads
+// are in flight during the epilogue.  An item has an even number of stages
+// (one past K reads zeros), so that the two buffers are constants of the loop.
 // ---------------------------------------------------------------------------
+struct MmItem {
+  int64_t m0, n0;  // first row and column of out
+  int kb;          // first stage
+  int part;        // index of the partial tile, -1: whole
+};
+
+template <int BM, int BC>
+__device__ __forceinline__ MmItem mm_item(const MmPlan& pl, int id) {
+  // tiles in groups of 4 rows of tiles, column after column
+  int tile = id, part = -1, kb = 0;
+  if (id >= pl.full) {
+    const int r = id - pl.full, cut = pl.ntm * pl.ntn - pl.full;
+    tile = pl.full + r % cut;
+    part = r;
+    kb = r / cut * pl.stages;
+  }
+  const int group = tile / (4 * pl.ntn), first = group * 4, rows = pl.ntm - first < 4 ? pl.ntm - first : 4;
+  const int rest = tile - group * 4 * pl.ntn;
+  return {(int64_t)(first + rest % rows) * BM, (int64_t)(rest / rows) * BC, kb, part};
+}
+
 template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs a, int ntm, int ntn) {
+__global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a, MmPlan pl) {
   constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
   constexpr int ES = io<T>::BYTES;
   constexpr bool G = EPI == MM_GATED;
   constexpr int MT = BM / 64, NT = BN / 64;  // 32 x 32 tiles of a wave
-  constexpr int BC = G ? BN / 2 : BN;        // columns of out per block
+  constexpr int BC = G ? BN / 2 : BN;        // columns of out per tile
   typedef Operand<T, PK, BM> OP;
   typedef Operand<T, QK, BN> OQ;
   constexpr int STAGE = OP::BYTES + OQ::BYTES;
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
 
-  // Tile order: workgroups go to the 8 XCDs in turn; each XCD gets a
-  // contiguous run of an order that walks groups of 4 rows of tiles, so that
-  // its 32 blocks in flight share about 4 + 8 operand tiles in its L2.
-  const int total = ntm * ntn, xcd = blockIdx.x & 7, per = total >> 3, more = total & 7;
-  const int id = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
-  const int group = id / (4 * ntn), first = group * 4, rows = ntm - first < 4 ? ntm - first : 4;
-  const int rest = id - group * 4 * ntn;
-  const int64_t m0 = (int64_t)(first + rest % rows) * BM, n0 = (int64_t)(rest / rows) * BC;
+  // Workgroups go to the 8 XCDs in turn; each XCD gets a contiguous run of
+  // the whole tiles and one of the parts, so that its blocks in flight share
+  // operand tiles in its L2.
+  const int xcd = blockIdx.x & 7, step = (gridDim.x + 7 - xcd) >> 3;  // blocks of this XCD
+  auto first = [&](int n) { return xcd * (n >> 3) + (xcd < (n & 7) ? xcd : (n & 7)); };
+  auto count = [&](int n) { return (n >> 3) + (xcd < (n & 7) ? 1 : 0); };
+  const int f0 = first(pl.full), nf = count(pl.full), p0 = pl.full + first(pl.items - pl.full);
+  const int end = nf + count(pl.items - pl.full);
+  auto item = [&](int v) { return mm_item<BM, BC>(pl, v < nf ? f0 + v : p0 + v - nf); };
+  int id = blockIdx.x >> 3;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -319,14 +395,15 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs 
   OQ oq;
   op.init(a.ldp, lane, wave);
   oq.init(a.ldq, lane, wave);
-  const char* pb = (const char*)a.P + (PK ? m0 * a.ldp : m0) * ES;
-  const char* qb = (const char*)a.Q + (QK ? n0 * a.ldq : n0) * ES;
-  const char* qb2 = (const char*)a.Q + (a.N + n0) * a.ldq * ES;  // gated: the second half's rows
-  const int64_t pr = a.M - m0, qr = a.N - n0;
-  auto load = [&](int kb, int at) {
+  const int past = (int)((a.K + OP::BK - 1) / OP::BK);  // a stage that reads zeros
+  auto load = [&](const MmItem& it, int kb, int at) {
     char* l = smem + at;
+    const char* pb = (const char*)a.P + (PK ? it.m0 * a.ldp : it.m0) * ES;
+    const char* qb = (const char*)a.Q + (QK ? it.n0 * a.ldq : it.n0) * ES;
+    const int64_t pr = a.M - it.m0, qr = a.N - it.n0;
     op.template load<0, OP::NI>(pb, pr, a.K, kb, l, wave);
     if constexpr (G) {
+      const char* qb2 = (const char*)a.Q + (a.N + it.n0) * a.ldq * ES;  // the second half's rows
       oq.template load<0, OQ::NI / 2>(qb, qr, a.K, kb, l + OP::BYTES, wave);
       oq.template load<OQ::NI / 2, OQ::NI>(qb2, qr, a.K, kb, l + OP::BYTES, wave);
     } else {
@@ -339,17 +416,9 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs 
   fq.init(G ? wn * (BN / 4) : wn * (BN / 2), lane);
 
   f32x16 acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-
   // of one k-step: matrix instructions and LDS reads
   constexpr int NM = MT * NT * (ES == 2 ? 1 : 4);
   constexpr int NR = MT * (PK ? 1 : ES == 2 ? 2 : 4) + NT * (QK ? 1 : ES == 2 ? 2 : 4);
-  const int nk = (int)((a.K + OP::BK - 1) / OP::BK);
   uint4 p[2][MT], q[2][NT];
   auto read = [&](int at, int s, int to) {
     const char* l = smem + at;
@@ -358,22 +427,27 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs 
 #pragma unroll
     for (int i = 0; i < NT; ++i) q[to][i] = fq.read(l + OP::BYTES, i, s);
   };
-  auto multiply = [&](int from) {
+  auto multiply = [&](int from, auto fresh) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
+      for (int j = 0; j < MT; ++j) {
+        if constexpr (decltype(fresh)::value) acc[i][j] = mma32<T>(q[from][i], p[from][j], f32x16{});
+        else acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
+      }
   };
-  auto stage = [&](int kb, auto cur) {
+  typedef std::integral_constant<bool, false> no;
+  // One stage in buffer B; `next` is loaded into it once it is free.
+  auto stage = [&](auto cur, auto fresh, const MmItem& next, int kb) {
     constexpr int B = decltype(cur)::value;
     read(B * STAGE, 1, 1);
-    multiply(0);
+    multiply(0, fresh);
     mix_k_step<NM, NR, 0>();
     read(B * STAGE, 2, 0);
-    multiply(1);
+    multiply(1, no{});
     mix_k_step<NM, NR, 0>();
     read(B * STAGE, 3, 1);
-    multiply(0);
+    multiply(0, no{});
     mix_k_step<NM, NR, 0>();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
@@ -381,60 +455,141 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void mm_tile_kernel(MmArgs 
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     read((B ^ 1) * STAGE, 0, 0);
-    load(kb + 2, B * STAGE);
-    multiply(1);
+    load(next, kb, B * STAGE);
+    multiply(1, no{});
     mix_k_step<NM, NR, OP::NI + OQ::NI>();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // an odd count of stages starts in the second buffer, so that the buffers
-  // of the loop's two stages are constants
-  const int odd = nk & 1;
-  load(0, odd * STAGE);
-  load(1, (odd ^ 1) * STAGE);
+  std::integral_constant<int, 0> b0;
+  std::integral_constant<int, 1> b1;
+  std::integral_constant<bool, true> yes;
+
+  if (id >= end) return;
+  MmItem it = item(id);
+  load(it, it.kb, 0);
+  load(it, it.kb + 1, STAGE);
   constexpr int NL = OP::NI + OQ::NI;  // loads of a stage
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (NL & 15) | (NL >> 4) << 14);  // stage 0 has landed
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (NL & 15) | (NL >> 4) << 14);  // the first stage has landed
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  read(odd * STAGE, 0, 0);
-  if (odd) stage(0, std::integral_constant<int, 1>{});
-  for (int kb = odd; kb < nk; kb += 2) {
-    stage(kb, std::integral_constant<int, 0>{});
-    stage(kb + 1, std::integral_constant<int, 1>{});
+  read(0, 0, 0);
+  for (;;) {
+    id += step;
+    const bool last = id >= end;
+    MmItem nx = item(last ? 0 : id);
+    if (last) nx.kb = past;
+    const int nk = it.part < 0 ? pl.whole : pl.stages;
+    const bool two = nk == 2;
+    stage(b0, yes, two ? nx : it, two ? nx.kb : it.kb + 2);
+    stage(b1, no{}, two ? nx : it, two ? nx.kb + 1 : it.kb + 3);
+    for (int t = 2; t < nk; t += 2) {
+      const bool over = t + 2 >= nk;
+      stage(b0, no{}, over ? nx : it, over ? nx.kb : it.kb + t + 2);
+      stage(b1, no{}, over ? nx : it, over ? nx.kb + 1 : it.kb + t + 3);
+    }
+    // opaque, so that the epilogue's addresses are not kept in registers
+    // across the products
+    int el = lane, ew = wave;
+    asm volatile("" : "+v"(el), "+s"(ew));
+    const int h = el >> 5, wm = ew & 1, wn = ew >> 1;
+    if (it.part >= 0) {
+      f32x4* part = (f32x4*)a.part + (int64_t)it.part * (BM * BN / 4) + ew * 64 + el;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          if constexpr (BM == 256) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            part[((i * MT + j) * 4 + v) * 256] =
+                f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+        }
+    } else {
+      const int64_t m = it.m0 + wm * (BM / 2) + (el & 31);
+      auto columns = [&](auto inner) {
+#pragma unroll
+        for (int i = 0; i < (G ? NT / 2 : NT); ++i)
+          tile_column<T, EPI, ACT, MT, decltype(inner)::value>(
+              a, m, it.n0 + wn * (BC / 2) + i * 32, h, [&](int j, float* z, float* u) {
+                // leaves the accumulation registers only now: all at once would not fit
+                if constexpr (BM == 256) {
+                  asm volatile("" : "+a"(acc[i][j]));
+                  if constexpr (G) asm volatile("" : "+a"(acc[i + NT / 2][j]));
+                }
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                  z[v] = acc[i][j][v];
+                  u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
+                }
+              });
+      };
+      if (it.m0 + BM <= a.M && it.n0 + BC <= a.N) columns(yes);
+      else columns(no{});
+    }
+    if (last) break;
+    it = nx;
   }
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last stage (zeros) have landed
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last item (zeros) have landed
+}
 
-  const int h = lane >> 5;
+// Adds the parts of the split tiles in order and applies the epilogue: one
+// block per tile and 32 x 32 piece of each wave.
+template <typename T, int EPI, int ACT, int BM, int BN>
+__global__ __launch_bounds__(256) void mm_join_kernel(MmArgs a, MmPlan pl) {
+  constexpr bool G = EPI == MM_GATED;
+  constexpr int MT = BM / 64, NT = BN / 64, BC = G ? BN / 2 : BN, PIECES = MT * (G ? NT / 2 : NT);
+  const int r = blockIdx.x / PIECES, piece = blockIdx.x % PIECES, i = piece / MT, j = piece % MT;
+  const int cut = pl.ntm * pl.ntn - pl.full;
+  const MmItem it = mm_item<BM, BC>(pl, pl.full + r);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  float z[16], u[16];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t m = m0 + wm * (BM / 2) + j * 32 + (lane & 31);
+  for (int v = 0; v < 16; ++v) z[v] = u[v] = 0.0f;
+  for (int s = 0; s < pl.split; ++s) {
+    const f32x4* part = (const f32x4*)a.part + ((int64_t)s * cut + r) * (BM * BN / 4) + tid;
 #pragma unroll
-    for (int i = 0; i < (G ? NT / 2 : NT); ++i) {
-      float z[16], u[16];
+    for (int v = 0; v < 4; ++v) {
+      const f32x4 x = part[((i * MT + j) * 4 + v) * 256];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        z[v] = acc[i][j][v];
-        u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
+      for (int e = 0; e < 4; ++e) z[4 * v + e] += x[e];
+      if constexpr (G) {
+        const f32x4 y = part[(((i + NT / 2) * MT + j) * 4 + v) * 256];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * v + e] += y[e];
       }
-      tile_epilogue<T, EPI, ACT>(a, m, n0 + wn * (BC / 2) + i * 32, z, u, h);
     }
   }
+  const int64_t m = it.m0 + (wave & 1) * (BM / 2) + j * 32 + (lane & 31);
+  tile_column<T, EPI, ACT, 1, false>(a, m, it.n0 + (wave >> 1) * (BC / 2) + i * 32, lane >> 5,
+                                     [&](int, float* zz, float* uu) {
+#pragma unroll
+                                       for (int v = 0; v < 16; ++v) {
+                                         zz[v] = z[v];
+                                         uu[v] = u[v];
+                                       }
+                                     });
 }
 
 template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
-hipError_t mm_tile_launch(const MmArgs& a, hipStream_t s) {
-  const int bc = EPI == MM_GATED ? BN / 2 : BN;
-  const int64_t ntm = (a.M + BM - 1) / BM, ntn = (a.N + bc - 1) / bc;
-  hipLaunchKernelGGL((mm_tile_kernel<T, LAYOUT, EPI, ACT, BM, BN>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, s, a,
-                     (int)ntm, (int)ntn);
+hipError_t mm_tile_launch(const MmArgs& a, const MmPlan& pl, hipStream_t s) {
+  constexpr int room = 256 * MmTileBlocks<BM>;  // blocks the chip holds
+  hipLaunchKernelGGL((mm_tile_kernel<T, LAYOUT, EPI, ACT, BM, BN>), dim3((unsigned)(pl.items < room ? pl.items : room)),
+                     dim3(256), 0, s, a, pl);
+  const int cut = pl.ntm * pl.ntn - pl.full;
+  if (cut > 0) {
+    constexpr int pieces = BM / 64 * (EPI == MM_GATED ? BN / 128 : BN / 64);
+    hipLaunchKernelGGL((mm_join_kernel<T, EPI, ACT, BM, BN>), dim3((unsigned)(cut * pieces)), dim3(256), 0, s, a, pl);
+  }
   return hipGetLastError();
 }
 
 template <typename T, int LAYOUT, int EPI, int ACT>
-hipError_t mm_tile_run(const MmArgs& a, hipStream_t s) {
-  const int bc = EPI == MM_GATED ? 128 : 256;
-  const int64_t t256 = ((a.M + 255) / 256) * ((a.N + bc - 1) / bc);
-  if (t256 >= 192) return mm_tile_launch<T, LAYOUT, EPI, ACT, 256, 256>(a, s);
-  return mm_tile_launch<T, LAYOUT, EPI, ACT, 128, 128>(a, s);
+hipError_t mm_tile_run(const MmArgs& a, const MmPlan& pl, hipStream_t s) {
+  switch (pl.tile) {
+    case 256: return mm_tile_launch<T, LAYOUT, EPI, ACT, 256, 256>(a, pl, s);
+    case 128: return mm_tile_launch<T, LAYOUT, EPI, ACT, 128, 128>(a, pl, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace m3

@@ -40,6 +40,7 @@ ABI_SYMBOLS = ("mamba3_ssm_chunked_fwd", "mamba3_ssm_chunked_fwd_workspace_size"
                "mamba3_linear_bwd", "mamba3_linear_bwd_workspace_size", "mamba3_gated_ffn_fwd",
                "mamba3_gated_ffn_fwd_workspace_size", "mamba3_gated_ffn_bwd", "mamba3_gated_ffn_bwd_workspace_size",
                "mamba3_status_string", "mamba3_abi_version")
+M3_FLAG_UNALIGNED = 0x40000    # linear, gated_ffn: operands off 16 bytes are copied first
 # activations of linear and gated_ffn
 M3_ACT_NONE, M3_ACT_RELU, M3_ACT_SILU, M3_ACT_GELU, M3_ACT_GELU_TANH, M3_ACT_SIGMOID = range(6)
 
@@ -551,10 +552,11 @@ def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, works
     if pre is None and want_pre:
         pre = torch.empty(lead + (wrows,), dtype=io, device=dev)
     ppre = _vec("pre", pre, lead + (wrows,), io, dev)
-    dims = LinearDims(rows, K, N, sx, sy, sr, code, act, 0, 0)
+    pW = _vec("W", W, (wrows, K), io, dev)
+    dims = LinearDims(rows, K, N, sx, sy, sr, code, act, M3_FLAG_UNALIGNED if (px | pW) & 15 else 0, 0)
     query = L.mamba3_gated_ffn_fwd_workspace_size if gated else L.mamba3_linear_fwd_workspace_size
     workspace, pws, nws = _workspace(query, dims, workspace, dev)
-    pW, pb = _vec("W", W, (wrows, K), io, dev), _vec("bias", bias, (wrows,), torch.float32, dev)
+    pb = _vec("bias", bias, (wrows,), torch.float32, dev)
     s = _raw_stream(stream, dev)
     st = (L.mamba3_gated_ffn_fwd(dims, px, pW, pb, py, ppre, pws, nws, s) if gated else
           L.mamba3_linear_fwd(dims, px, pW, pb, pr, py, ppre, pws, nws, s))
@@ -585,11 +587,12 @@ def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, 
     if want_dbias or dbias is not None:
         out["dbias"] = dbias = torch.empty(wrows, dtype=torch.float32, device=dev) if dbias is None else dbias
         pb = _vec("dbias", dbias, (wrows,), torch.float32, dev)
-    dims = LinearDims(rows, K, N, sx, sdy, 0, code, act, 0, 0)
+    pW = _vec("W", W, (wrows, K), io, dev)
+    dims = LinearDims(rows, K, N, sx, sdy, 0, code, act, M3_FLAG_UNALIGNED if (px | pW | pdy) & 15 else 0, 0)
     query = L.mamba3_gated_ffn_bwd_workspace_size if gated else L.mamba3_linear_bwd_workspace_size
     workspace, pws, nws = _workspace(query, dims, workspace, dev)
     call = L.mamba3_gated_ffn_bwd if gated else L.mamba3_linear_bwd
-    st = call(dims, px, _vec("W", W, (wrows, K), io, dev), ppre[0], pdy, pdx, pdW, pb, pws, nws,
+    st = call(dims, px, pW, ppre[0], pdy, pdx, pdW, pb, pws, nws,
               _raw_stream(stream, dev))
     _check(st, name)
     return out
