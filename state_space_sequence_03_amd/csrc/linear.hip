@@ -20,8 +20,9 @@ MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
   };
   int64_t tiles = cut(256);
   if (tiles < 192) tiles = cut(128);
-  const int room = 256 * (p.tile == 256 ? 1 : 2);
+  const int room = mm_room(p.tile);
   p.whole = even(total);
+  if (p.tile == 256 && p.whole < 4) p.whole = 4;
   p.stages = p.whole;
   p.split = 1;
   // The last, partial round of tiles: split over k so that its parts fill the

@@ -204,8 +204,8 @@ struct MmPlan {
   int items;          // full + split parts
   size_t part_bytes;
 };
-template <int BM>
-constexpr int MmTileBlocks = BM == 256 ? 1 : BM == 128 ? 2 : 4;  // resident per CU
+constexpr int mm_blocks(int tile) { return tile == 256 ? 1 : 2; }       // resident per CU
+constexpr int mm_room(int tile) { return 256 * mm_blocks(tile); }       // ... and on the chip
 MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K);
 // The tiled kernels need rows of P and Q that start on 16 bytes; a row along
 // k whose last 16 bytes are partial must be backed by zeros up to there.

@@ -1,7 +1,7 @@
 // Products with the gated epilogue, bf16 io.
 #include "mm_few.hpp"
 #include "mm_parts.hpp"
-#include "mm_tile.hpp"
+#include "mm_run.hpp"
 
 namespace m3 {
 

@@ -1,6 +1,6 @@
 // Products of the backward (no epilogue), f32 io.
 #include "mm_parts.hpp"
-#include "mm_tile.hpp"
+#include "mm_run.hpp"
 
 namespace m3 {
 

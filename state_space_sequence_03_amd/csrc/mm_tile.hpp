@@ -365,8 +365,72 @@ __device__ __forceinline__ MmItem mm_item(const MmPlan& pl, int id) {
   return {(int64_t)(first + rest % rows) * BM, (int64_t)(rest / rows) * BC, kb, part};
 }
 
+// Workgroups go to the 8 XCDs in turn; each XCD gets a contiguous run of the
+// whole tiles and one of the parts, so that its blocks in flight share operand
+// tiles in its L2.
+struct MmWalk {
+  int step, f0, nf, p0, end;  // the block's items: blockIdx / 8, + step, ... below end
+  __device__ __forceinline__ explicit MmWalk(const MmPlan& pl) {
+    const int xcd = blockIdx.x & 7;
+    auto first = [&](int n) { return xcd * (n >> 3) + (xcd < (n & 7) ? xcd : (n & 7)); };
+    auto count = [&](int n) { return (n >> 3) + (xcd < (n & 7) ? 1 : 0); };
+    step = (gridDim.x + 7 - xcd) >> 3;  // blocks of this XCD
+    f0 = first(pl.full);
+    nf = count(pl.full);
+    p0 = pl.full + first(pl.items - pl.full);
+    end = nf + count(pl.items - pl.full);
+  }
+  template <int BM, int BC>
+  __device__ __forceinline__ MmItem item(const MmPlan& pl, int v) const {
+    return mm_item<BM, BC>(pl, v < nf ? f0 + v : p0 + v - nf);
+  }
+};
+
+// The end of an item: its epilogue, or its part's sums to the workspace.
+template <typename T, int EPI, int ACT, int BM, int BN>
+__device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32x16 (&acc)[BN / 64][BM / 64], int lane,
+                                          int wave) {
+  constexpr bool G = EPI == MM_GATED;
+  constexpr int MT = BM / 64, NT = BN / 64, BC = G ? BN / 2 : BN;
+  const int h = lane >> 5, wm = wave & 1, wn = wave >> 1;
+  if (it.part >= 0) {
+    f32x4* part = (f32x4*)a.part + (int64_t)it.part * (BM * BN / 4) + wave * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if constexpr (BM == 256) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          part[((i * MT + j) * 4 + v) * 256] =
+              f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+      }
+    return;
+  }
+  const int64_t m = it.m0 + wm * (BM / 2) + (lane & 31);
+  auto columns = [&](auto inner) {
+#pragma unroll
+    for (int i = 0; i < (G ? NT / 2 : NT); ++i)
+      tile_column<T, EPI, ACT, MT, decltype(inner)::value>(
+          a, m, it.n0 + wn * (BC / 2) + i * 32, h, [&](int j, float* z, float* u) {
+            // leaves the accumulation registers only now: all at once would not fit
+            if constexpr (BM == 256) {
+              asm volatile("" : "+a"(acc[i][j]));
+              if constexpr (G) asm volatile("" : "+a"(acc[i + NT / 2][j]));
+            }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              z[v] = acc[i][j][v];
+              u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
+            }
+          });
+  };
+  if (it.m0 + BM <= a.M && it.n0 + BC <= a.N) columns(std::integral_constant<bool, true>{});
+  else columns(std::integral_constant<bool, false>{});
+}
+
 template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
-__global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a, MmPlan pl) {
+__global__ __launch_bounds__(256, mm_blocks(BM)) void mm_tile_kernel(MmArgs a, MmPlan pl) {
   constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
   constexpr int ES = io<T>::BYTES;
   constexpr bool G = EPI == MM_GATED;
@@ -377,17 +441,8 @@ __global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a
   constexpr int STAGE = OP::BYTES + OQ::BYTES;
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
 
-  // Workgroups go to the 8 XCDs in turn; each XCD gets a contiguous run of
-  // the whole tiles and one of the parts, so that its blocks in flight share
-  // operand tiles in its L2.
-  const int xcd = blockIdx.x & 7, step = (gridDim.x + 7 - xcd) >> 3;  // blocks of this XCD
-  auto first = [&](int n) { return xcd * (n >> 3) + (xcd < (n & 7) ? xcd : (n & 7)); };
-  auto count = [&](int n) { return (n >> 3) + (xcd < (n & 7) ? 1 : 0); };
-  const int f0 = first(pl.full), nf = count(pl.full), p0 = pl.full + first(pl.items - pl.full);
-  const int end = nf + count(pl.items - pl.full);
-  auto item = [&](int v) { return mm_item<BM, BC>(pl, v < nf ? f0 + v : p0 + v - nf); };
+  const MmWalk walk(pl);
   int id = blockIdx.x >> 3;
-
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -464,8 +519,8 @@ __global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a
   std::integral_constant<int, 1> b1;
   std::integral_constant<bool, true> yes;
 
-  if (id >= end) return;
-  MmItem it = item(id);
+  if (id >= walk.end) return;
+  MmItem it = walk.item<BM, BC>(pl, id);
   load(it, it.kb, 0);
   load(it, it.kb + 1, STAGE);
   constexpr int NL = OP::NI + OQ::NI;  // loads of a stage
@@ -474,9 +529,9 @@ __global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a
   asm volatile("" ::: "memory");
   read(0, 0, 0);
   for (;;) {
-    id += step;
-    const bool last = id >= end;
-    MmItem nx = item(last ? 0 : id);
+    id += walk.step;
+    const bool last = id >= walk.end;
+    MmItem nx = walk.item<BM, BC>(pl, last ? 0 : id);
     if (last) nx.kb = past;
     const int nk = it.part < 0 ? pl.whole : pl.stages;
     const bool two = nk == 2;
@@ -491,41 +546,7 @@ __global__ __launch_bounds__(256, MmTileBlocks<BM>) void mm_tile_kernel(MmArgs a
     // across the products
     int el = lane, ew = wave;
     asm volatile("" : "+v"(el), "+s"(ew));
-    const int h = el >> 5, wm = ew & 1, wn = ew >> 1;
-    if (it.part >= 0) {
-      f32x4* part = (f32x4*)a.part + (int64_t)it.part * (BM * BN / 4) + ew * 64 + el;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          if constexpr (BM == 256) asm volatile("" : "+a"(acc[i][j]));
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            part[((i * MT + j) * 4 + v) * 256] =
-                f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
-        }
-    } else {
-      const int64_t m = it.m0 + wm * (BM / 2) + (el & 31);
-      auto columns = [&](auto inner) {
-#pragma unroll
-        for (int i = 0; i < (G ? NT / 2 : NT); ++i)
-          tile_column<T, EPI, ACT, MT, decltype(inner)::value>(
-              a, m, it.n0 + wn * (BC / 2) + i * 32, h, [&](int j, float* z, float* u) {
-                // leaves the accumulation registers only now: all at once would not fit
-                if constexpr (BM == 256) {
-                  asm volatile("" : "+a"(acc[i][j]));
-                  if constexpr (G) asm volatile("" : "+a"(acc[i + NT / 2][j]));
-                }
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                  z[v] = acc[i][j][v];
-                  u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
-                }
-              });
-      };
-      if (it.m0 + BM <= a.M && it.n0 + BC <= a.N) columns(yes);
-      else columns(no{});
-    }
+    mm_finish<T, EPI, ACT, BM, BN>(a, it, acc, el, ew);
     if (last) break;
     it = nx;
   }
@@ -568,28 +589,6 @@ __global__ __launch_bounds__(256) void mm_join_kernel(MmArgs a, MmPlan pl) {
                                          uu[v] = u[v];
                                        }
                                      });
-}
-
-template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
-hipError_t mm_tile_launch(const MmArgs& a, const MmPlan& pl, hipStream_t s) {
-  constexpr int room = 256 * MmTileBlocks<BM>;  // blocks the chip holds
-  hipLaunchKernelGGL((mm_tile_kernel<T, LAYOUT, EPI, ACT, BM, BN>), dim3((unsigned)(pl.items < room ? pl.items : room)),
-                     dim3(256), 0, s, a, pl);
-  const int cut = pl.ntm * pl.ntn - pl.full;
-  if (cut > 0) {
-    constexpr int pieces = BM / 64 * (EPI == MM_GATED ? BN / 128 : BN / 64);
-    hipLaunchKernelGGL((mm_join_kernel<T, EPI, ACT, BM, BN>), dim3((unsigned)(cut * pieces)), dim3(256), 0, s, a, pl);
-  }
-  return hipGetLastError();
-}
-
-template <typename T, int LAYOUT, int EPI, int ACT>
-hipError_t mm_tile_run(const MmArgs& a, const MmPlan& pl, hipStream_t s) {
-  switch (pl.tile) {
-    case 256: return mm_tile_launch<T, LAYOUT, EPI, ACT, 256, 256>(a, pl, s);
-    case 128: return mm_tile_launch<T, LAYOUT, EPI, ACT, 128, 128>(a, pl, s);
-    default: return hipErrorInvalidValue;
-  }
 }
 
 }  // namespace m3

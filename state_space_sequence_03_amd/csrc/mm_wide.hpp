@@ -1,0 +1,248 @@
+// The 256 x 256 tile of the matrix products (mm_tile.hpp has the smaller one,
+// the epilogue and the order of the work).
+//
+// Four waves, one per SIMD, each 128 x 128 of the tile: 16 products of 32 x 32
+// with 256 accumulators, fed by 128 bytes of k per stage.  What bounds the
+// loop is keeping the matrix core of a lone wave busy: a stage's 64 KB take
+// about half a stage to come through the CU's 64-byte path, after a latency
+// of about as long, so loads have to be in flight the whole time.  Hence a
+// stage is cut into four pieces of 16 KB (of each operand, the first and the
+// second half of every wave's rows) and four phases of one quadrant each:
+//   phase 0: P0 Q0, reads Q1         phase 2: P1 Q1, reads the next P0
+//   phase 1: P0 Q1, reads P1         phase 3: P1 Q0, reads the next Q0
+// where a "read" takes the piece from LDS into registers, for the phase after.
+// A piece's place in LDS is free one phase after its read and gets the piece
+// of the stage after next at once: a load has six phases (3,000 cycles) to
+// land, and every phase issues four loads per wave, reads one piece and ends
+// in one barrier that waits for the loads of six phases before.
+#pragma once
+
+#include "mm_tile.hpp"
+
+namespace m3 {
+
+// A 16 KB piece of an operand: half `H` of the rows of the two wave groups
+// (rows 128 g + 64 H .. + 63; in a gated block's second operand, all 128 rows
+// of the half's own matrix).
+// KC: 128 rows of 128 bytes; chunk c of row r at chunk c ^ fsw(r).
+// Otherwise: 128 / ES rows of k, each 128 elements; bf16: chunk c of row k at
+// c ^ 4 (k mod 4), for the transpose reads.
+template <typename T, bool KC, bool APART>
+struct Piece {
+  static constexpr int ES = io<T>::BYTES;
+  static constexpr int BK = 128 / ES;
+  static constexpr int LPR = KC ? 8 : 8 * ES;  // lanes per row of LDS
+  static constexpr int RPI = 64 / LPR;         // rows per load
+  int voff, kpos, ldb;
+  int at[KC ? 4 : 2];
+
+  __device__ __forceinline__ void init(int64_t ld, int lane, int wave, int group) {
+    ldb = (int)(ld * ES);
+    const int row = wave * RPI + lane / LPR, slot = lane % LPR;
+    if constexpr (KC) {
+      const int c = slot ^ fsw<8>(row);
+      kpos = c * 16;
+      voff = row * ldb + kpos;
+      const int r = group * 64 + (lane & 31);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) at[s] = r * 128 + (((2 * s + (lane >> 5)) ^ fsw<8>(r)) << 4);
+    } else {
+      const int c = ES == 2 ? slot ^ ((row & 3) << 2) : slot;
+      kpos = 0;
+      voff = row * ldb + c / (LPR / 2) * 128 * ES + c % (LPR / 2) * 16;
+      if constexpr (ES == 2) {
+        const int g = lane >> 4, i = lane & 15, q = i >> 2;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          at[t] = (8 * (g >> 1) + q) * 256 +
+                  (((((group * 2 + t) ^ q) * 4) + (g & 1) * 2 + ((i & 3) >> 1)) << 4) + (i & 1) * 8;
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) at[t] = 4 * (lane >> 5) * 512 + (group * 64 + t * 32 + (lane & 31)) * 4;
+      }
+    }
+  }
+  // base: the tile's first element at k = 0 (APART: the half's); rows: rows
+  // of the tile that exist.  What lies past them or past K reads as zero (a
+  // partial last 16 bytes exists in memory and holds zeros past K).
+  template <int H>
+  __device__ __forceinline__ void load(const char* base, int64_t rows, int64_t K, int kb, char* lds, int wave) const {
+    if constexpr (KC) {
+      const int most = APART ? 128 : 256;
+      const int n = rows < most ? (int)rows : most;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)base, 0, (uint32_t)((n - 1) * ldb + (int)((K * ES + 15) & ~(int64_t)15)), 0x00020000);
+      const int vo = kpos < (int)(K * ES) - kb * 128 ? voff : 0x7ff00000;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (lds_void*)(lds + (i * 4 + wave) * 1024), 16, vo,
+            (APART ? i * 32 : (i >> 1) * 128 + H * 64 + (i & 1) * 32) * ldb + kb * 128, 0, 0);
+    } else {
+      const int64_t all = (int64_t)kb * BK, k0 = all < K ? all : K;
+      const int left = K - k0 < BK ? (int)(K - k0) : BK;
+      const int bytes = (left - 1) * ldb + (int)((rows * ES + 15) & ~(int64_t)15);
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(base + k0 * ldb), 0, bytes > 0 ? bytes : 0, 0x00020000);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * 4 + wave) * 1024), 16, voff,
+                                                 i * 4 * RPI * ldb + H * 64 * ES, 0, 0);
+    }
+  }
+  // fragment of tile t (0, 1) of the wave's half, k-step s
+  __device__ __forceinline__ uint4 read(const char* lds, int t, int s) const {
+    if constexpr (KC) {
+      return __builtin_bit_cast(uint4, read16((const u32x4*)(lds + at[s] + t * 4096)));
+    } else if constexpr (ES == 2) {
+      const char* p = lds + at[t] + s * 4096;
+      const uint2 a = read_tr(p), b = read_tr(p + 1024);
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      const char* p = lds + at[t] + s * 4096;
+      return make_uint4(read4((const uint32_t*)p), read4((const uint32_t*)(p + 512)),
+                        read4((const uint32_t*)(p + 1024)), read4((const uint32_t*)(p + 1536)));
+    }
+  }
+};
+
+template <typename T, int LAYOUT, int EPI, int ACT>
+__global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
+  constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
+  constexpr int ES = io<T>::BYTES;
+  constexpr bool G = EPI == MM_GATED;
+  constexpr int BC = G ? 128 : 256;  // columns of out per tile
+  constexpr int PIECE = 16384, BUF = 4 * PIECE;  // P0 P1 Q0 Q1
+  __shared__ __attribute__((aligned(1024))) char smem[2 * BUF];
+
+  const MmWalk walk(pl);
+  int id = blockIdx.x >> 3;
+  if (id >= walk.end) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Piece<T, PK, false> op;
+  Piece<T, QK, G> oq;
+  op.init(a.ldp, lane, wave, wave & 1);
+  oq.init(a.ldq, lane, wave, wave >> 1);
+  const int past = (int)((a.K + op.BK - 1) / op.BK);  // a stage that reads zeros
+
+  auto load_p = [&](auto half, const MmItem& it, int kb, int buf) {
+    constexpr int H = decltype(half)::value;
+    const char* b = (const char*)a.P + (PK ? it.m0 * a.ldp : it.m0) * ES;
+    op.template load<H>(b, a.M - it.m0, a.K, kb, smem + buf * BUF + H * PIECE, wave);
+  };
+  auto load_q = [&](auto half, const MmItem& it, int kb, int buf) {
+    constexpr int H = decltype(half)::value;
+    const int64_t n = it.n0 + (G && H ? a.N : 0);
+    const char* b = (const char*)a.Q + (QK ? n * a.ldq : n) * ES;
+    oq.template load<H>(b, a.N - it.n0, a.K, kb, smem + buf * BUF + (2 + H) * PIECE, wave);
+  };
+  // fragments of the pieces: P0, P1; Q0 and Q1 change places every stage,
+  // since the next Q0 is read while this stage's is in use
+  uint4 p[2][2][4], q[2][2][4];
+  auto read_p = [&](int half, int buf) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) p[half][t][s] = op.read(smem + buf * BUF + half * PIECE, t, s);
+  };
+  auto read_q = [&](int half, int buf, int to) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) q[to][t][s] = oq.read(smem + buf * BUF + (2 + half) * PIECE, t, s);
+  };
+  f32x16 acc[4][4];  // [tile of Q][tile of P]
+  auto multiply = [&](int ph, int qh, int qat, auto fresh) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f32x16& c = acc[qh * 2 + i][ph * 2 + j];
+          if (decltype(fresh)::value && s == 0) c = mma32<T>(q[qat][i][s], p[ph][j][s], f32x16{});
+          else c = mma32<T>(q[qat][i][s], p[ph][j][s], c);
+        }
+  };
+  constexpr int NM = 16 * (ES == 2 ? 1 : 4);
+  constexpr int NP = PK ? 8 : ES == 2 ? 16 : 32, NQ = QK ? 8 : ES == 2 ? 16 : 32;  // LDS reads of a piece
+  // All but the last 24 loads of this wave have landed (the six latest
+  // phases'), its reads are done, and so it is with every wave.
+  auto settle = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x4078);  // vmcnt(24) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+  std::integral_constant<int, 0> c0;
+  std::integral_constant<int, 1> c1;
+  std::integral_constant<bool, true> yes;
+  std::integral_constant<bool, false> no;
+  // Stage in buffer B; n2, k2 and n3, k3: the stages two and three later.
+  auto stage = [&](auto cur, auto fresh, const MmItem& n2, int k2, const MmItem& n3, int k3) {
+    constexpr int B = decltype(cur)::value;
+    read_q(1, B, B ^ 1);
+    load_q(c0, n2, k2, B);
+    multiply(0, 0, B, fresh);
+    mix_k_step<NM, NQ, 4>();
+    settle();
+    read_p(1, B);
+    load_q(c1, n2, k2, B);
+    multiply(0, 1, B ^ 1, fresh);
+    mix_k_step<NM, NP, 4>();
+    settle();
+    read_p(0, B ^ 1);
+    load_p(c1, n2, k2, B);
+    multiply(1, 1, B ^ 1, fresh);
+    mix_k_step<NM, NP, 4>();
+    settle();
+    read_q(0, B ^ 1, B ^ 1);
+    load_p(c0, n3, k3, B ^ 1);
+    multiply(1, 0, B, fresh);
+    mix_k_step<NM, NQ, 4>();
+    settle();
+  };
+
+  MmItem it = walk.item<256, BC>(pl, id);
+  load_p(c0, it, it.kb, 0);
+  load_q(c0, it, it.kb, 0);
+  load_q(c1, it, it.kb, 0);
+  load_p(c1, it, it.kb, 0);
+  load_p(c0, it, it.kb + 1, 1);
+  load_q(c0, it, it.kb + 1, 1);
+  load_q(c1, it, it.kb + 1, 1);
+  load_p(c1, it, it.kb + 1, 1);
+  settle();  // P0 and Q0 are there
+  read_p(0, 0);
+  read_q(0, 0, 0);
+  settle();  // ... and read
+  load_p(c0, it, it.kb + 2, 0);
+  settle();  // Q1 is there
+  for (;;) {
+    id += walk.step;
+    const bool last = id >= walk.end;
+    MmItem nx = walk.item<256, BC>(pl, last ? 0 : id);
+    if (last) nx.kb = past;
+    const int nk = it.part < 0 ? pl.whole : pl.stages;  // even, at least 4
+    stage(c0, yes, it, it.kb + 2, it, it.kb + 3);
+    stage(c1, no, it, it.kb + 3, nk == 4 ? nx : it, nk == 4 ? nx.kb : it.kb + 4);
+    for (int t = 2; t < nk; t += 2) {
+      const bool over = t + 2 >= nk, near = t + 4 >= nk;
+      const int k2 = over ? nx.kb - nk : it.kb, k4 = near ? nx.kb - nk : it.kb;
+      stage(c0, no, over ? nx : it, k2 + t + 2, over ? nx : it, k2 + t + 3);
+      stage(c1, no, over ? nx : it, k2 + t + 3, near ? nx : it, k4 + t + 4);
+    }
+    // opaque, so that the epilogue's addresses are not kept in registers
+    // across the products
+    int el = lane, ew = wave;
+    asm volatile("" : "+v"(el), "+s"(ew));
+    mm_finish<T, EPI, ACT, 256, 256>(a, it, acc, el, ew);
+    if (last) break;
+    it = nx;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last item (zeros) have landed
+}
+
+}  // namespace m3
