@@ -386,6 +386,26 @@ struct MmWalk {
   }
 };
 
+// The values of an accumulator tile.  A 256 x 256 tile's leave the
+// accumulation registers here and not before: left to the compiler, copies of
+// all of them are made at the loop's end, and spilled.  (The caller has waited
+// for the last product: mm_drain.)
+template <bool WIDE>
+__device__ __forceinline__ void acc_values(const f32x16& acc, float* z) {
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    if constexpr (WIDE) asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(z[v]) : "a"(acc[v]));
+    else z[v] = acc[v];
+  }
+}
+// More wait states than any product's latency; the compiler does not know
+// that acc_values reads what a product wrote.
+__device__ __forceinline__ void mm_drain() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // The end of an item: its epilogue, or its part's sums to the workspace.
 template <typename T, int EPI, int ACT, int BM, int BN>
 __device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32x16 (&acc)[BN / 64][BM / 64], int lane,
@@ -399,11 +419,11 @@ __device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        if constexpr (BM == 256) asm volatile("" : "+a"(acc[i][j]));
+        float z[16];
+        acc_values<BM == 256>(acc[i][j], z);
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          part[((i * MT + j) * 4 + v) * 256] =
-              f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+          part[((i * MT + j) * 4 + v) * 256] = f32x4{z[4 * v], z[4 * v + 1], z[4 * v + 2], z[4 * v + 3]};
       }
     return;
   }
@@ -413,16 +433,8 @@ __device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32
     for (int i = 0; i < (G ? NT / 2 : NT); ++i)
       tile_column<T, EPI, ACT, MT, decltype(inner)::value>(
           a, m, it.n0 + wn * (BC / 2) + i * 32, h, [&](int j, float* z, float* u) {
-            // leaves the accumulation registers only now: all at once would not fit
-            if constexpr (BM == 256) {
-              asm volatile("" : "+a"(acc[i][j]));
-              if constexpr (G) asm volatile("" : "+a"(acc[i + NT / 2][j]));
-            }
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              z[v] = acc[i][j][v];
-              u[v] = G ? acc[i + (G ? NT / 2 : 0)][j][v] : 0.0f;
-            }
+            acc_values<BM == 256>(acc[i][j], z);
+            if constexpr (G) acc_values<BM == 256>(acc[i + NT / 2][j], u);
           });
   };
   if (it.m0 + BM <= a.M && it.n0 + BC <= a.N) columns(std::integral_constant<bool, true>{});

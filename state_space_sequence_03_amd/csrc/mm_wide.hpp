@@ -106,6 +106,143 @@ struct Piece {
   }
 };
 
+// 32 rows x 64 columns of bf16 between the accumulators' layout (lane l: row l
+// mod 32, columns 8 q + 4 (l / 32) .. + 3 of each 32) and whole 128-byte rows
+// (lane l: rows l / 8 + 8 k, columns 8 (l mod 8) .. + 7), through 4 KB of LDS
+// of the wave's own: 16-byte chunk c of row r at chunk c ^ (r mod 8).  Stored
+// straight from the accumulators' layout, an output row goes out in pieces of
+// 32 bytes, at half the rate.
+__device__ __forceinline__ void write8(uint2* __restrict p, uint2 v) { *p = v; }
+__device__ __forceinline__ void write16(u32x4* __restrict p, u32x4 v) { *p = v; }
+__device__ __forceinline__ uint2 read8(const uint2* __restrict p) { return *p; }
+struct Rows64 {
+  char* lds;
+  int lane;
+  __device__ __forceinline__ char* piece(int tile, int q) const {
+    const int r = lane & 31;
+    return lds + r * 128 + (((tile * 4 + q) ^ (r & 7)) << 4) + (lane >> 5) * 8;
+  }
+  __device__ __forceinline__ char* line(int k) const {
+    const int r = 8 * k + (lane >> 3);
+    return lds + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+  }
+  // tile t's values in, from the accumulators' layout
+  __device__ __forceinline__ void put(int t, const float (&z)[16]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      write8((uint2*)piece(t, q),
+             make_uint2(pack_bf2(z[4 * q], z[4 * q + 1]), pack_bf2(z[4 * q + 2], z[4 * q + 3])));
+  }
+  // what is there for tile t added to z
+  __device__ __forceinline__ void add(int t, float (&z)[16]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint2 w = read8((const uint2*)piece(t, q));
+      z[4 * q] += bf_lo(w.x);
+      z[4 * q + 1] += bf_hi(w.x);
+      z[4 * q + 2] += bf_lo(w.y);
+      z[4 * q + 3] += bf_hi(w.y);
+    }
+  }
+  // whole rows out to memory (dst: row 0, column 0), and in
+  __device__ __forceinline__ void store(char* dst, int64_t ld) const {
+    asm volatile("" ::: "memory");
+    u32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = read16((const u32x4*)line(k));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *(u32x4_any*)(dst + ((8 * k + (lane >> 3)) * ld + 8 * (lane & 7)) * 2) = v[k];
+    asm volatile("" ::: "memory");
+  }
+  __device__ __forceinline__ void load(const char* src, int64_t ld, u32x4 (&v)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *(const u32x4_any*)(src + ((8 * k + (lane >> 3)) * ld + 8 * (lane & 7)) * 2);
+  }
+  __device__ __forceinline__ void fill(const u32x4 (&v)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) write16((u32x4*)line(k), v[k]);
+    asm volatile("" ::: "memory");
+  }
+};
+
+// The epilogue of a whole tile inside the matrix, bf16 io.  bias: the tile's
+// in LDS (gated: the first half's 128 columns, then the other's).
+template <int EPI, int ACT>
+__device__ __forceinline__ void wide_epilogue(const MmArgs& a, const MmItem& it, f32x16 (&acc)[4][4], char* lds,
+                                              const float* bias, int lane, int wave) {
+  constexpr bool G = EPI == MM_GATED;
+  const int h = lane >> 5;
+  const int64_t m = it.m0 + (wave & 1) * 128;
+  const Rows64 rows{lds, lane};
+  // acc[i][j] (+ bias) of the tile i from column c of the block on
+  auto value = [&](int i, int j, int c, float (&z)[16]) {
+    acc_values<true>(acc[i][j], z);
+    if constexpr (EPI != MM_STORE)
+      if (a.bias) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 b = *(const f32x4*)(bias + c + 8 * q + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[4 * q + e] += b[e];
+        }
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < (G ? 2 : 4); i += 2) {
+    const int c = (wave >> 1) * (G ? 64 : 128) + i * 32;
+    const int64_t n = it.n0 + c;
+    u32x4 res[4];
+    const char* rs = (const char*)a.res + (m * a.ldr + n) * 2;
+    if constexpr (EPI == MM_LINEAR)
+      if (a.res) rows.load(rs, a.ldr, res);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = m + 32 * j;
+      float z[16], u[16];
+      if constexpr (EPI != MM_STORE)
+        if (a.pre) {
+          char* pre = (char*)a.pre + (r * (G ? 2 : 1) * a.N + n) * 2;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            value(i + t, j, c + 32 * t, z);
+            rows.put(t, z);
+          }
+          rows.store(pre, (G ? 2 : 1) * a.N);
+          if constexpr (G) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              value(2 + t, j, 128 + c + 32 * t, u);
+              rows.put(t, u);
+            }
+            rows.store(pre + a.N * 2, 2 * a.N);
+          }
+        }
+      if constexpr (EPI == MM_LINEAR)
+        if (a.res) {
+          rows.fill(res);
+          if (j < 3) rows.load(rs + 32 * (j + 1) * a.ldr * 2, a.ldr, res);
+        }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        value(i + t, j, c + 32 * t, z);
+        if constexpr (EPI != MM_STORE) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) z[v] = act_fwd<ACT, false>(z[v]);
+        }
+        if constexpr (EPI == MM_LINEAR)
+          if (a.res) rows.add(t, z);
+        if constexpr (G) {
+          value(2 + t, j, 128 + c + 32 * t, u);
+#pragma unroll
+          for (int v = 0; v < 16; ++v) z[v] *= u[v];
+        }
+        rows.put(t, z);
+      }
+      rows.store((char*)a.out + (r * a.ldo + n) * 2, a.ldo);
+    }
+  }
+}
+
 template <typename T, int LAYOUT, int EPI, int ACT>
 __global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
   constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
@@ -113,7 +250,12 @@ __global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
   constexpr bool G = EPI == MM_GATED;
   constexpr int BC = G ? 128 : 256;  // columns of out per tile
   constexpr int PIECE = 16384, BUF = 4 * PIECE;  // P0 P1 Q0 Q1
-  __shared__ __attribute__((aligned(1024))) char smem[2 * BUF];
+  // One array for all of it: with several, the compiler tracks which one a
+  // load into LDS still in flight writes, and holds every fragment read back
+  // until all of them have landed.
+  constexpr int ROWS = 2 * BUF, BIAS = ROWS + (ES == 2 ? 4 * 4096 : 0);
+  __shared__ __attribute__((aligned(1024))) char smem[BIAS + (ES == 2 ? 1024 : 0)];
+  float* const bias = (float*)(smem + BIAS);
 
   const MmWalk walk(pl);
   int id = blockIdx.x >> 3;
@@ -226,6 +368,12 @@ __global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
     MmItem nx = walk.item<256, BC>(pl, last ? 0 : id);
     if (last) nx.kb = past;
     const int nk = it.part < 0 ? pl.whole : pl.stages;  // even, at least 4
+    float b = 0.0f;  // of column it.n0 + tid, for the epilogue
+    if constexpr (ES == 2 && EPI != MM_STORE)
+      if (a.bias) {
+        const int64_t n = it.n0 + (threadIdx.x & (BC - 1));
+        b = a.bias[(n < a.N ? n : a.N - 1) + (threadIdx.x >= BC ? a.N : 0)];
+      }
     stage(c0, yes, it, it.kb + 2, it, it.kb + 3);
     stage(c1, no, it, it.kb + 3, nk == 4 ? nx : it, nk == 4 ? nx.kb : it.kb + 4);
     for (int t = 2; t < nk; t += 2) {
@@ -238,7 +386,21 @@ __global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
     // across the products
     int el = lane, ew = wave;
     asm volatile("" : "+v"(el), "+s"(ew));
-    mm_finish<T, EPI, ACT, 256, 256>(a, it, acc, el, ew);
+    mm_drain();
+    bool done = false;
+    if constexpr (ES == 2)
+      if (it.part < 0 && it.m0 + 256 <= a.M && it.n0 + BC <= a.N) {
+        if constexpr (EPI != MM_STORE)
+          if (a.bias) {
+            bias[threadIdx.x] = b;
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+          }
+        wide_epilogue<EPI, ACT>(a, it, acc, smem + ROWS + ew * 4096, bias, el, ew);
+        done = true;
+      }
+    if (!done) mm_finish<T, EPI, ACT, 256, 256>(a, it, acc, el, ew);
     if (last) break;
     it = nx;
   }
