@@ -211,12 +211,10 @@ m3_status linear_bwd(const m3_linear_dims* d, bool gated, const void* x, const v
     e.pre = pre; e.dy = dy; e.ldy = a.ldp;
     e.ldp = padded(n, d->io_dtype);
     e.dp = store_dp ? ws + w.dp : nullptr;
-    e.part = dbias ? (float*)(ws + w.cols) : nullptr;
+    e.dbias = dbias;
+    e.part = (float*)(ws + w.cols);
     e.rows = d->rows; e.cols = d->d_out; e.act = d->act; e.gated = gated;
-    hipError_t err = m3::launch_act_bwd(io, e, s);
-    if (err == hipSuccess && dbias)
-      err = m3::launch_reduce_parts(e.part, m3::act_bwd_parts(d->rows), n, n, dbias, n, nullptr, s);
-    if (err != hipSuccess) return M3_ERR_HIP;
+    if (m3::launch_act_bwd(io, e, s) != hipSuccess) return M3_ERR_HIP;
     if (store_dp) {
       a.P = e.dp;
       a.ldp = e.ldp;
@@ -288,12 +286,12 @@ m3_status mamba3_layer_norm_bwd(const m3_norm_dims* d, const void* x, const floa
   if (!cols && !dx) return M3_OK;
   m3::NormBwdArgs a{};
   a.x = x; a.gain = gain; a.mean = mean; a.rstd = rstd; a.dy = dy; a.dskip = dskip; a.dx = dx;
-  a.part = cols ? (float*)workspace : nullptr;
+  a.dgain = dgain; a.dbias = dbias; a.part = (float*)workspace;
   a.rows = d->rows; a.width = d->width;
   a.x_stride = or_width(d->x_stride, d->width);
   a.y_stride = or_width(d->y_stride, d->width);
   a.skip_stride = or_width(d->skip_stride, d->width);
-  return hip_status(m3::launch_norm_bwd(bf16(d->io_dtype), a, dgain, dbias, s));
+  return hip_status(m3::launch_norm_bwd(bf16(d->io_dtype), a, s));
 }
 
 size_t mamba3_linear_fwd_workspace_size(const m3_linear_dims* d) {

@@ -4,51 +4,66 @@
 
 namespace m3 {
 
+namespace {
+
+// What a product costs with a given tile, in microseconds, fitted to calls of
+// 50 to 32768 rows on one MI355X (bf16 / fp32): a stage of one tile alone on
+// its CU and with as many tiles as fit, the start and end of a tile, and the
+// join of split tiles (a launch, and the parts written and read).
+struct TileCost {
+  int tile;
+  double alone[2], shared[2], ends;
+};
+constexpr TileCost kTiles[] = {{256, {1.05, 7.2}, {1.05, 7.2}, 6.0},
+                               {128, {0.70, 2.1}, {0.60, 2.1}, 1.0},
+                               {64, {0.32, 0.62}, {0.26, 0.61}, 0.5}};
+constexpr double kJoin = 6.0, kJoinBytesPerUs = 1.0e7;
+
+}  // namespace
+
 MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
-  MmPlan p{};
-  if (epi != MM_STORE && M <= MM_FEW_ROWS) return p;
-  const int es = io_bf16 ? 2 : 4;
+  MmPlan best{};
+  if (epi != MM_STORE && M <= MM_FEW_ROWS) return best;
+  const int es = io_bf16 ? 2 : 4, ty = io_bf16 ? 0 : 1;
   const int total = (int)((K * es + 127) / 128);  // stages of 128 bytes
-  auto even = [](int v) { return v + (v & 1); };
-  const int gated = epi == MM_GATED ? 2 : 1;
-  auto cut = [&](int tile) {
-    const int bc = tile / gated;
-    p.tile = tile;
-    p.ntm = (int)((M + tile - 1) / tile);
-    p.ntn = (int)((N + bc - 1) / bc);
-    return (int64_t)p.ntm * p.ntn;
-  };
-  int64_t tiles = cut(256);
-  if (tiles < 192) tiles = cut(128);
-  const int room = mm_room(p.tile);
-  p.whole = even(total);
-  if (p.tile == 256 && p.whole < 4) p.whole = 4;
-  p.stages = p.whole;
-  p.split = 1;
-  // The last, partial round of tiles: split over k so that its parts fill the
-  // chip.  Cost in stages of one block: rounds of parts, plus what writing and
-  // reading a part back takes.
-  const int rest = (int)(tiles % room);
-  p.full = (int)tiles;
-  if (rest > 0) {
-    const int join = p.tile == 256 ? 6 : 4;
-    int best = p.whole;  // one more round of whole tiles
-    for (int s = 2; s <= 64; ++s) {
-      const int st = even((total + s - 1) / s), parts = (total + st - 1) / st;
-      if (parts != s || st < 4) continue;
-      const int cost = (int)(((int64_t)rest * s + room - 1) / room) * (st + join) + join;
-      if (cost < best) {
-        best = cost;
-        p.split = s;
-        p.stages = st;
-      }
+  double least = 0.0;
+  for (const TileCost& c : kTiles) {
+    MmPlan p{};
+    p.tile = c.tile;
+    const int gated = epi == MM_GATED ? 2 : 1;
+    const int64_t bm = c.tile, bn = c.tile == 64 ? 64 * gated : c.tile;
+    p.ntm = (int)((M + bm - 1) / bm);
+    p.ntn = (int)((N * gated + bn - 1) / bn);
+    const int64_t tiles = (int64_t)p.ntm * p.ntn;
+    const int room = mm_room(c.tile), per = mm_blocks(c.tile);
+    // the 256 x 256 tile takes stages in pairs, at least four of them
+    auto stages = [&](int n) { return c.tile != 256 ? n : n < 4 ? 4 : n + (n & 1); };
+    auto time = [&](int64_t items, int st) {  // of one round of items of st stages
+      const int64_t n = (items + 255) / 256;
+      const double wide = c.tile == 64 && gated == 2 ? 1.8 : 1.0;  // 64 x 128 of W's rows there
+      return n == 0 ? 0.0 : (n < per ? st * c.alone[ty] : n * st * c.shared[ty]) * wide + n * c.ends;
+    };
+    p.whole = stages(total);
+    const int64_t rest = tiles % room;
+    const double rounds = time(tiles - rest, p.whole);
+    // the last round's tiles whole, or split over k so that their parts fill
+    // the chip
+    for (int s = 1; s <= 64; ++s) {
+      const int st = s == 1 ? p.whole : stages((total + s - 1) / s);
+      if (s > 1 && (rest == 0 || st < 4 || (total + st - 1) / st != s)) continue;
+      const double bytes = s == 1 ? 0.0 : (double)(rest * s * bm * bn) * 8.0;
+      const double t = rounds + time(rest * s, st) + (s == 1 ? 0.0 : kJoin + bytes / kJoinBytesPerUs);
+      if (best.tile != 0 && t >= least) continue;
+      least = t;
+      p.split = s;
+      p.stages = st;
+      p.full = (int)(s == 1 ? tiles : tiles - rest);
+      p.items = (int)(p.full + (s == 1 ? 0 : rest * s));
+      p.part_bytes = s == 1 ? 0 : (size_t)(rest * s * bm * bn) * 4;
+      best = p;
     }
-    if (p.split > 1) p.full = (int)tiles - rest;
   }
-  const int64_t parts = (tiles - p.full) * p.split;
-  p.items = (int)(p.full + parts);
-  p.part_bytes = (size_t)(parts * p.tile * p.tile) * 4;
-  return p;
+  return best;
 }
 
 hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, const MmPlan& plan,

@@ -165,11 +165,12 @@ struct NormBwdArgs {
   const float *gain, *mean, *rstd;  // gain nullable
   const void *dy, *dskip;           // dskip nullable
   void* dx;                         // nullable; row stride skip_stride
-  float* part;                      // nullable: (norm_bwd_parts(rows), 2, width) partial column sums
+  float *dgain, *dbias;             // nullable
+  float* part;                      // with either: (norm_bwd_parts(rows), 2, width), unused for one part
   int64_t rows, width, x_stride, y_stride, skip_stride;
 };
 int64_t norm_bwd_parts(int64_t rows);
-hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, float* dgain, float* dbias, hipStream_t s);
+hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, hipStream_t s);
 // out[c] = sum over p < np of part[p * stride + c] for c < n; the first n0 go
 // to out0, the rest to out1 (each nullable).
 hipError_t launch_reduce_parts(const float* part, int64_t np, int64_t stride, int64_t n, float* out0, int64_t n0,
@@ -231,7 +232,8 @@ struct ActBwdArgs {
   const void* pre;  // (rows, cols or 2 cols); null when act is none and gated is 0
   const void* dy;   // row stride ldy
   void* dp;         // nullable: as pre, rows ldp apart, padded by zeros
-  float* part;      // nullable: (act_bwd_parts(rows), cols or 2 cols)
+  float* dbias;     // nullable
+  float* part;      // with dbias: (act_bwd_parts(rows), cols or 2 cols), unused for one part
   int64_t rows, cols, ldy, ldp;
   int act, gated;
 };

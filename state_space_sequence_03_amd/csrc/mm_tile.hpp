@@ -44,7 +44,7 @@ __device__ __forceinline__ uint2 read_tr(const void* __restrict p) { return lds_
 // distinct bank groups.
 // Otherwise (rows of memory run along m or n): LDS holds 128 / ES rows of k,
 // each ROWS elements wide.  bf16 fragments come out of the transpose read,
-// chunk c of row k stored at c ^ 4 (k mod 4), so that the four rows a 16-lane
+// chunk c of row k stored at c ^ 4 turn(k), so that the four rows a 16-lane
 // group addresses fall into distinct banks; fp32 fragments are four words.
 template <typename T, bool KC, int ROWS>
 struct Operand {
@@ -55,6 +55,9 @@ struct Operand {
   static constexpr int LPR = KC ? 8 : ROWS * ES / 16;  // lanes per row of LDS
   static constexpr int RPI = 64 / LPR;         // rows per 1 KB load
 
+  // bf16, not KC: chunk c of row k lies at c ^ 4 turn(k)
+  __device__ __forceinline__ static int turn(int k) { return ROWS == 64 ? (k >> 1) & 1 : k & 3; }
+
   int voff;   // lane's byte offset within the tile
   int kpos;   // KC: lane's first byte of k within the stage
   int ldb;
@@ -64,7 +67,7 @@ struct Operand {
     const int row = wave * RPI + lane / LPR, slot = lane % LPR;
     int chunk = slot;
     if constexpr (KC) chunk = slot ^ fsw<8>(row);  // rows 32 apart share it
-    else if constexpr (ES == 2) chunk = slot ^ ((row & 3) << 2);  // rows 4 RPI apart share it
+    else if constexpr (ES == 2) chunk = slot ^ (turn(row) << 2);  // rows 4 RPI apart share it
     kpos = chunk * 16;
     voff = row * ldb + chunk * 16;
   }
@@ -120,7 +123,7 @@ struct Fragments {
       const int row = 8 * (g >> 1) + q, c = (g & 1) * 2 + ((i & 3) >> 1);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        at[t] = row * ROWS * 2 + ((((r0 / 32 + t) ^ q) * 4 + c) << 4) + (i & 1) * 8;
+        at[t] = row * ROWS * 2 + ((((r0 / 32 + t) ^ Operand<T, KC, ROWS>::turn(q)) * 4 + c) << 4) + (i & 1) * 8;
     } else {
       at[0] = (4 * (lane >> 5)) * ROWS * 4 + (r0 + (lane & 31)) * 4;
     }
@@ -326,23 +329,21 @@ __device__ __forceinline__ void mix_k_step() {
 }
 
 // ---------------------------------------------------------------------------
-// The tiled kernel: BM x BN outputs per tile (gated: BN / 2 columns of each
-// half), four waves, each BM / 2 x BN / 2 of them on 32 x 32 products; the
-// 256 x 256 tile runs one wave per SIMD with 256 accumulators each.
+// The smaller tiles, BM x BN outputs (gated: BN / 2 columns of each half) of
+// four waves, each BM / 2 x BN / 2 of them on 32 x 32 products: what has too
+// few 256 x 256 tiles to fill the chip.
 //
-// k advances by 128 bytes per stage through two stages of LDS.  A stage has
+// k advances by 128 bytes per stage through NBUF stages of LDS.  A stage has
 // four k-steps of 32 bytes; a wave reads the fragments of the next k-step
 // while the products of this one run, across the stage's end too: after the
 // third k-step every wave holds the fragments of the fourth in registers, so
-// one barrier there frees this stage's LDS for the loads of the stage after
-// next (which so have a whole stage's products to land in) and publishes the
-// next stage, whose first fragments are read under the fourth k-step's
-// products.
+// one barrier there frees this stage's LDS for the loads of NBUF stages later
+// and publishes the next stage, whose first fragments are read under the
+// fourth k-step's products.
 //
 // Blocks stay: each walks several items (a tile, or a tile's part of k), and
 // the stage after an item's last is the next item's first, so that its loads
-// are in flight during the epilogue.  An item has an even number of stages
-// (one past K reads zeros), so that the two buffers are constants of the loop.
+// are in flight during the epilogue.
 // ---------------------------------------------------------------------------
 struct MmItem {
   int64_t m0, n0;  // first row and column of out
@@ -441,8 +442,8 @@ __device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32
   else columns(std::integral_constant<bool, false>{});
 }
 
-template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN>
-__global__ __launch_bounds__(256, mm_blocks(BM)) void mm_tile_kernel(MmArgs a, MmPlan pl) {
+template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN, int NBUF>
+__global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
   constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
   constexpr int ES = io<T>::BYTES;
   constexpr bool G = EPI == MM_GATED;
@@ -451,18 +452,19 @@ __global__ __launch_bounds__(256, mm_blocks(BM)) void mm_tile_kernel(MmArgs a, M
   typedef Operand<T, PK, BM> OP;
   typedef Operand<T, QK, BN> OQ;
   constexpr int STAGE = OP::BYTES + OQ::BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  static_assert(2 * NBUF * STAGE <= 163840, "two blocks per CU");
+  __shared__ __attribute__((aligned(1024))) char smem[NBUF * STAGE];
 
   const MmWalk walk(pl);
   int id = blockIdx.x >> 3;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (id >= walk.end) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   OP op;
   OQ oq;
   op.init(a.ldp, lane, wave);
   oq.init(a.ldq, lane, wave);
-  const int past = (int)((a.K + OP::BK - 1) / OP::BK);  // a stage that reads zeros
   auto load = [&](const MmItem& it, int kb, int at) {
     char* l = smem + at;
     const char* pb = (const char*)a.P + (PK ? it.m0 * a.ldp : it.m0) * ES;
@@ -494,73 +496,78 @@ __global__ __launch_bounds__(256, mm_blocks(BM)) void mm_tile_kernel(MmArgs a, M
 #pragma unroll
     for (int i = 0; i < NT; ++i) q[to][i] = fq.read(l + OP::BYTES, i, s);
   };
-  auto multiply = [&](int from, auto fresh) {
+  auto multiply = [&](int from) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        if constexpr (decltype(fresh)::value) acc[i][j] = mma32<T>(q[from][i], p[from][j], f32x16{});
-        else acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
-      }
+      for (int j = 0; j < MT; ++j) acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
   };
-  typedef std::integral_constant<bool, false> no;
-  // One stage in buffer B; `next` is loaded into it once it is free.
-  auto stage = [&](auto cur, auto fresh, const MmItem& next, int kb) {
-    constexpr int B = decltype(cur)::value;
-    read(B * STAGE, 1, 1);
-    multiply(0, fresh);
-    mix_k_step<NM, NR, 0>();
-    read(B * STAGE, 2, 0);
-    multiply(1, no{});
-    mix_k_step<NM, NR, 0>();
-    read(B * STAGE, 3, 1);
-    multiply(0, no{});
-    mix_k_step<NM, NR, 0>();
+  // the loads run ahead of the products: the item and stage they are at
+  int lid = id;
+  MmItem lt = walk.item<BM, BC>(pl, id);
+  int lk = 0, ln = lt.part < 0 ? pl.whole : pl.stages;
+  auto load_next = [&](int at) {
+    load(lt, lt.kb + lk, at);
+    if (++lk == ln) {
+      lid += walk.step;
+      if (lid < walk.end) {
+        lt = walk.item<BM, BC>(pl, lid);
+        ln = lt.part < 0 ? pl.whole : pl.stages;
+        lk = 0;
+      } else {  // nothing left: stages past K, which read zeros
+        lt.kb = pl.whole;
+        lk = 0;
+        ln = 0x7fffffff;
+      }
+    }
+  };
+  constexpr int NL = OP::NI + OQ::NI;    // loads of a stage
+  constexpr int AHEAD = (NBUF - 2) * NL;  // in flight past the stage that comes next
+  static_assert(AHEAD + NL < 64, "vmcnt");
+  auto settle = [&](auto n) {
+    constexpr int N = decltype(n)::value;
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-    read((B ^ 1) * STAGE, 0, 0);
-    load(next, kb, B * STAGE);
-    multiply(1, no{});
-    mix_k_step<NM, NR, OP::NI + OQ::NI>();
-    __builtin_amdgcn_sched_barrier(0);
   };
-  std::integral_constant<int, 0> b0;
-  std::integral_constant<int, 1> b1;
-  std::integral_constant<bool, true> yes;
-
-  if (id >= walk.end) return;
-  MmItem it = walk.item<BM, BC>(pl, id);
-  load(it, it.kb, 0);
-  load(it, it.kb + 1, STAGE);
-  constexpr int NL = OP::NI + OQ::NI;  // loads of a stage
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (NL & 15) | (NL >> 4) << 14);  // the first stage has landed
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < NBUF; ++i) load_next(i * STAGE);
+  settle(std::integral_constant<int, AHEAD + NL>{});
   read(0, 0, 0);
-  for (;;) {
-    id += walk.step;
-    const bool last = id >= walk.end;
-    MmItem nx = walk.item<BM, BC>(pl, last ? 0 : id);
-    if (last) nx.kb = past;
+  int at = 0;
+  for (; id < walk.end; id += walk.step) {
+    const MmItem it = walk.item<BM, BC>(pl, id);
     const int nk = it.part < 0 ? pl.whole : pl.stages;
-    const bool two = nk == 2;
-    stage(b0, yes, two ? nx : it, two ? nx.kb : it.kb + 2);
-    stage(b1, no{}, two ? nx : it, two ? nx.kb + 1 : it.kb + 3);
-    for (int t = 2; t < nk; t += 2) {
-      const bool over = t + 2 >= nk;
-      stage(b0, no{}, over ? nx : it, over ? nx.kb : it.kb + t + 2);
-      stage(b1, no{}, over ? nx : it, over ? nx.kb + 1 : it.kb + t + 3);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    for (int kb = 0; kb < nk; ++kb) {
+      const int nxt = at == (NBUF - 1) * STAGE ? 0 : at + STAGE;
+      read(at, 1, 1);
+      multiply(0);
+      mix_k_step<NM, NR, 0>();
+      read(at, 2, 0);
+      multiply(1);
+      mix_k_step<NM, NR, 0>();
+      read(at, 3, 1);
+      multiply(0);
+      mix_k_step<NM, NR, 0>();
+      settle(std::integral_constant<int, AHEAD>{});
+      read(nxt, 0, 0);
+      load_next(at);
+      multiply(1);
+      at = nxt;
     }
     // opaque, so that the epilogue's addresses are not kept in registers
     // across the products
     int el = lane, ew = wave;
     asm volatile("" : "+v"(el), "+s"(ew));
     mm_finish<T, EPI, ACT, BM, BN>(a, it, acc, el, ew);
-    if (last) break;
-    it = nx;
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last item (zeros) have landed
 }

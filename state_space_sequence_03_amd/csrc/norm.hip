@@ -119,13 +119,13 @@ __global__ __launch_bounds__(256) void norm_fwd_wide_kernel(NormArgs a) {
   }
 }
 
-// Rows blockIdx, blockIdx + gridDim, ... (in groups of 256 / TPR); column
-// sums of the block's rows to part[blockIdx][2][D] when part is set.
-template <typename T, int NV, int TPR>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
+// Rows blockIdx, blockIdx + gridDim, ... (in groups of 256 / TPR), and the
+// column sums of the block's rows.
+template <typename T, int NV, int TPR, bool SKIP>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int V = io<T>::VEC;
-  constexpr int RPB = 256 / TPR;
-  __shared__ float sh[2][2][4];
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  __shared__ float sh[2][2][TPR / 64];
   __shared__ float comb[RPB > 1 ? (RPB - 1) * 64 * V : 1];
   const int t = threadIdx.x % TPR, rr = threadIdx.x / TPR;
   const int64_t D = a.width;
@@ -137,20 +137,38 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) sg[i][j] = sb[i][j] = 0.0f;
   }
-  int par = 0;
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB, par ^= 1) {
-    const int64_t row = base + rr;
-    if (RPB > 1 && row >= a.rows) break;  // the wave's last group
+  // the next row is requested while this one is worked on
+  u32x4 nx[NV], nd[NV], ns[NV];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto request = [&](int64_t row) {
     const char* x = (const char*)a.x + row * a.x_stride * io<T>::BYTES;
     const char* dy = (const char*)a.dy + row * a.y_stride * io<T>::BYTES;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    const char* sk = (const char*)a.dskip + row * a.skip_stride * io<T>::BYTES;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * TPR + t) * V;
+      nx[i] = row_raw<T>(x, c, D);
+      nd[i] = row_raw<T>(dy, c, D);
+      if (SKIP) ns[i] = row_raw<T>(sk, c, D);
+    }
+    nmean = a.mean[row];
+    nrstd = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + rr;
+  if (row < a.rows) request(row);
+  for (int par = 0; row < a.rows; row += step, par ^= 1) {  // uniform per wave, and per block where a row is a block's
+    const float mean = nmean, rstd = nrstd;
     float f[NV][V], d[NV][V];
+    u32x4 sk[NV];
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      row_load<T>(x, (int64_t)(i * TPR + t) * V, D, f[i]);
-      row_load<T>(dy, (int64_t)(i * TPR + t) * V, D, d[i]);
+      unpack_raw<T>(nx[i], f[i]);
+      unpack_raw<T>(nd[i], d[i]);
+      if (SKIP) sk[i] = ns[i];
     }
+    if (row + step < a.rows) request(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -166,13 +184,12 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     c1 = row_sum<TPR>(c1, sh[par][0]) / n;
     c2 = row_sum<TPR>(c2, sh[par][1]) / n;
     char* dx = (char*)a.dx + row * a.skip_stride * io<T>::BYTES;
-    const char* sk = a.dskip ? (const char*)a.dskip + row * a.skip_stride * io<T>::BYTES : nullptr;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = (int64_t)(i * TPR + t) * V;
       if (c >= D) break;
       float o[V];
-      if (sk) row_load<T>(sk, c, D, o);
+      if (SKIP) unpack_raw<T>(sk[i], o);
       else
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = 0.0f;
@@ -181,8 +198,12 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
       row_store<T>(dx, c, D, o);
     }
   }
-  if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * D;
+  if (!a.dgain && !a.dbias) return;
+  float* out[2] = {a.dgain, a.dbias};  // a lone block's sums are the result
+  if (gridDim.x > 1) {
+    out[0] = a.part + (int64_t)blockIdx.x * 2 * D;
+    out[1] = out[0] + D;
+  }
   // the block's waves, in order
 #pragma unroll
   for (int which = 0; which < 2; ++which)
@@ -202,10 +223,10 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             for (int w = 0; w < RPB - 1; ++w) s[j] += comb[(w * V + j) * 64 + t];
       }
       const int64_t c = (int64_t)(i * TPR + t) * V;
-      if (rr == 0)
+      if (rr == 0 && out[which])
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          if (c + j < D) part[which * D + c + j] = s[j];
+          if (c + j < D) out[which][c + j] = s[j];
     }
 }
 
@@ -267,31 +288,34 @@ __global__ __launch_bounds__(256) void norm_cols_wide_kernel(NormBwdArgs a) {
       sb[j] += d[j];
     }
   }
-  float* part = a.part + (int64_t)blockIdx.y * 2 * D;
+  float* og = gridDim.y > 1 ? a.part + (int64_t)blockIdx.y * 2 * D : a.dgain;
+  float* ob = gridDim.y > 1 ? og + D : a.dbias;
 #pragma unroll
   for (int j = 0; j < V; ++j)
     if (c + j < D) {
-      part[c + j] = sg[j];
-      part[D + c + j] = sb[j];
+      if (og) og[c + j] = sg[j];
+      if (ob) ob[c + j] = sb[j];
     }
 }
 
 // out[c] = sum over p of part[p * stride + c], c < n0 to out0 and the rest to
 // out1 (each nullable).  64 columns per block, the partial rows split over
-// its 4 waves, which are then added in order.
-__global__ __launch_bounds__(256) void reduce_parts_kernel(const float* part, int64_t np, int64_t stride, int64_t n,
-                                                           float* out0, int64_t n0, float* out1) {
-  __shared__ float sh[4][64];
+// its 16 waves, which are then added in order.
+__global__ __launch_bounds__(1024) void reduce_parts_kernel(const float* part, int64_t np, int64_t stride, int64_t n,
+                                                            float* out0, int64_t n0, float* out1) {
+  __shared__ float sh[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
   if (c < n)
 #pragma unroll 8
-    for (int64_t p = w; p < np; p += 4) s += part[p * stride + c];
+    for (int64_t p = w; p < np; p += 16) s += part[p * stride + c];
   sh[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < n) {
-    s = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += sh[k][lane];
     float* o = c < n0 ? out0 : out1;
     if (o) o[c < n0 ? c : c - n0] = s;
   }
@@ -317,18 +341,18 @@ hipError_t norm_fwd_run(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool SKIP>
 hipError_t norm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
   const int64_t n64 = vectors<T>(a.width, 64), n256 = vectors<T>(a.width, 256);
   const dim3 parts((unsigned)norm_bwd_parts(a.rows)), blk(256);
-  if (n64 == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 64>), parts, blk, 0, s, a);
-  else if (n64 == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, 64>), parts, blk, 0, s, a);
-  else if (n64 <= 4) hipLaunchKernelGGL((norm_bwd_kernel<T, 4, 64>), parts, blk, 0, s, a);
-  else if (n256 <= 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, 256>), parts, blk, 0, s, a);
-  else if (n256 <= 4) hipLaunchKernelGGL((norm_bwd_kernel<T, 4, 256>), parts, blk, 0, s, a);
+  if (n64 == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 64, SKIP>), parts, blk, 0, s, a);
+  else if (n64 == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, 64, SKIP>), parts, blk, 0, s, a);
+  else if (n256 == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 256, SKIP>), parts, blk, 0, s, a);
+  else if (n256 == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, 256, SKIP>), parts, blk, 0, s, a);
+  else if (n256 <= 4) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 1024, SKIP>), parts, dim3(1024), 0, s, a);
   else {
     if (a.dx) hipLaunchKernelGGL((norm_bwd_wide_kernel<T>), dim3((unsigned)a.rows), blk, 0, s, a);
-    if (a.part)
+    if (a.dgain || a.dbias)
       hipLaunchKernelGGL((norm_cols_wide_kernel<T>), dim3((unsigned)n256, parts.x), blk, 0, s, a);
   }
   return hipGetLastError();
@@ -336,14 +360,16 @@ hipError_t norm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// Blocks of the backward: up to four per CU, four rows each at least; up to 8
+// rows one block, which needs no second kernel for its sums.
 int64_t norm_bwd_parts(int64_t rows) {
   const int64_t groups = (rows + 3) / 4;
-  return groups < 512 ? groups : 512;
+  return rows <= 8 ? 1 : groups < 1024 ? groups : 1024;
 }
 
 hipError_t launch_reduce_parts(const float* part, int64_t np, int64_t stride, int64_t n, float* out0, int64_t n0,
                                float* out1, hipStream_t s) {
-  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)((n + 63) / 64)), dim3(256), 0, s, part, np, stride, n, out0,
+  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, s, part, np, stride, n, out0,
                      n0, out1);
   return hipGetLastError();
 }
@@ -352,10 +378,12 @@ hipError_t launch_norm_fwd(int io_bf16, const NormArgs& a, hipStream_t s) {
   return io_bf16 ? norm_fwd_run<bf16_t>(a, s) : norm_fwd_run<float>(a, s);
 }
 
-hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, float* dgain, float* dbias, hipStream_t s) {
-  const hipError_t e = io_bf16 ? norm_bwd_run<bf16_t>(a, s) : norm_bwd_run<float>(a, s);
-  if (e != hipSuccess || !a.part) return e;
-  return launch_reduce_parts(a.part, norm_bwd_parts(a.rows), 2 * a.width, 2 * a.width, dgain, a.width, dbias, s);
+hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, hipStream_t s) {
+  const hipError_t e = io_bf16 ? (a.dskip ? norm_bwd_run<bf16_t, true>(a, s) : norm_bwd_run<bf16_t, false>(a, s))
+                               : (a.dskip ? norm_bwd_run<float, true>(a, s) : norm_bwd_run<float, false>(a, s));
+  const int64_t parts = norm_bwd_parts(a.rows);
+  if (e != hipSuccess || parts == 1 || (!a.dgain && !a.dbias)) return e;
+  return launch_reduce_parts(a.part, parts, 2 * a.width, 2 * a.width, a.dgain, a.width, a.dbias, s);
 }
 
 }  // namespace m3

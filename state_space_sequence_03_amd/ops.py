@@ -129,9 +129,15 @@ def status_string(status: int) -> str:
         return "unknown"
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _io_code(t) -> int:
@@ -399,51 +405,50 @@ def mamba3_bc_prologue(u, W, dt, theta, nheads, rank, dstate, gain=None, bias=No
 # ---------------------------------------------------------------------------
 # the residual block around the core: layer norm, linear, gated feed-forward
 # ---------------------------------------------------------------------------
+# (a call of a few rows is bound by its host side: the checks' passing path is
+# kept short, and the error is worked out only when one fails)
 def _rows(name, t, width, rows, dtype, device):
     """(pointer, row stride in elements; 0: contiguous) of a matrix of rows:
     (..., width) contiguous, or (rows, width) with rows further apart."""
-    if t is None:
-        return None, 0
+    if t.dtype is dtype and t.device == device and t.numel() == rows * width and t.shape[-1] == width:
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= width:
+            return t.data_ptr(), t.stride(0)
+        raise ValueError(f"{name}: must be contiguous, or 2-d with contiguous rows")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.shape[-1] != width or t.numel() != rows * width:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {rows} rows of {width}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= width:
-        return t.data_ptr(), t.stride(0)
-    raise ValueError(f"{name}: must be contiguous, or 2-d with contiguous rows")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {rows} rows of {width}")
 
 
 def _vec(name, t, shape, dtype, device):
     """Pointer of a contiguous operand of the given shape (None: absent)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     _expect(name, t, shape, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
-def _workspace(query, dims, workspace, device):
-    need = query(ctypes.byref(dims))
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        workspace = _torch().empty(need, device=device, dtype=_torch().uint8)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _raw_stream(stream, device):
-    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    current = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    if current is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return current(device.index)
 
 
-def _shape_rows(x):
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (..., width) with a width from 1")
-    return x.numel() // x.shape[-1], x.shape[-1]
+def _rows_of(x):
+    """rows, width, type code of x (..., width)."""
+    shape = x.shape
+    if not shape or shape[-1] == 0:
+        raise ValueError(f"x: shape {tuple(shape)}, expected (..., width) with a width from 1")
+    return x.numel() // shape[-1], shape[-1], _io_code(x)
 
 
 def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=None, rstd=None, want_stats=False,
@@ -451,15 +456,14 @@ def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=Non
     """Layer norm of the rows of x (..., D).  Returns (y, mean, rstd); the
     statistics ((rows) fp32, for the backward) are None unless wanted or given."""
     torch = _torch()
-    rows, D = _shape_rows(x)
+    rows, D, code = _rows_of(x)
     io, dev, f32 = x.dtype, x.device, torch.float32
-    code = _io_code(x)
     px, sx = _rows("x", x, D, rows, io, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=io, device=dev)
+        y = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
     if want_stats or mean is not None or rstd is not None:
         mean = torch.empty(rows, dtype=f32, device=dev) if mean is None else mean
-        rstd = torch.empty(rows, dtype=f32, device=dev) if rstd is None else rstd
+        rstd = torch.empty_like(mean) if rstd is None else rstd
     py, sy = _rows("y", y, D, rows, io, dev)
     st = lib().mamba3_layer_norm_fwd(NormDims(rows, D, sx, sy, 0, code, 0), px, _vec("gain", gain, (D,), f32, dev),
                                      _vec("bias", bias, (D,), f32, dev), eps, py,
@@ -479,19 +483,20 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
     norm, added to dx.  Returns a dict with dx (io dtype), dgain and dbias (fp32),
     as wanted.  dskip and dx have the same row stride."""
     torch = _torch()
-    rows, D = _shape_rows(x)
+    rows, D, code = _rows_of(x)
     io, dev, f32 = x.dtype, x.device, torch.float32
-    code = _io_code(x)
     px, sx = _rows("x", x, D, rows, io, dev)
     pdy, sdy = _rows("dy", dy, D, rows, io, dev)
-    psk, ssk = _rows("dskip", dskip, D, rows, io, dev)
+    psk, ssk = (None, 0) if dskip is None else _rows("dskip", dskip, D, rows, io, dev)
     out = {}
     pdx = pg = pb = pws = None
     nws = 0
     if want_dx or dx is not None:
         if dx is None:
-            dx = torch.empty(x.shape, dtype=io, device=dev) if ssk == 0 else torch.empty_strided(
-                (rows, D), (ssk, 1), dtype=io, device=dev)
+            if ssk:
+                dx = torch.empty_strided((rows, D), (ssk, 1), dtype=io, device=dev)
+            else:
+                dx = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
         pdx, sdx = _rows("dx", dx, D, rows, io, dev)
         if dskip is not None and (sdx or D) != (ssk or D):
             raise ValueError("dx and dskip must have the same row stride")
@@ -504,11 +509,12 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
         out["dbias"] = dbias = torch.empty(D, dtype=f32, device=dev) if dbias is None else dbias
         pb = _vec("dbias", dbias, (D,), f32, dev)
     dims = NormDims(rows, D, sx, sdy, ssk, code, 0)
+    L = lib()
     if pg or pb:
-        workspace, pws, nws = _workspace(lib().mamba3_layer_norm_bwd_workspace_size, dims, workspace, dev)
-    st = lib().mamba3_layer_norm_bwd(dims, px, _vec("gain", gain, (D,), f32, dev),
-                                     _vec("mean", mean, (rows,), f32, dev), _vec("rstd", rstd, (rows,), f32, dev),
-                                     pdy, psk, pdx, pg, pb, pws, nws, _raw_stream(stream, dev))
+        workspace, pws, nws = _workspace(L.mamba3_layer_norm_bwd_workspace_size, dims, workspace, dev)
+    st = L.mamba3_layer_norm_bwd(dims, px, _vec("gain", gain, (D,), f32, dev), _vec("mean", mean, (rows,), f32, dev),
+                                 _vec("rstd", rstd, (rows,), f32, dev), pdy, psk, pdx, pg, pb, pws, nws,
+                                 _raw_stream(stream, dev))
     _check(st, "mamba3_layer_norm_bwd")
     return out
 
@@ -529,71 +535,90 @@ def gated_ffn_bwd_workspace_size(dims: LinearDims) -> int:
     return int(lib().mamba3_gated_ffn_bwd_workspace_size(ctypes.byref(dims)))
 
 
-def _weight_shape(x, W, gated):
+def _workspace(query, dims, workspace, device):
+    """(tensor, pointer, bytes) of the workspace a call needs (None, None, 0: none)."""
+    need = query(dims)
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _torch().empty(need, device=device, dtype=_torch().uint8)
+        return workspace, workspace.data_ptr(), need
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _weight_rows(W, gated):
+    """Rows of W and the width of the operator's result."""
     if W.dim() != 2:
         raise ValueError(f"W: shape {tuple(W.shape)}, expected (rows of W, d_in)")
-    if gated and W.shape[0] % 2:
-        raise ValueError(f"W: {W.shape[0]} rows, expected the gate's and as many more")
-    rows, K = _shape_rows(x)
-    return rows, K, W.shape[0], W.shape[0] // 2 if gated else W.shape[0]
+    n = W.shape[0]
+    if not gated:
+        return n, n
+    if n % 2:
+        raise ValueError(f"W: {n} rows, expected the gate's and as many more")
+    return n, n // 2
 
 
 def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, workspace, stream):
     torch = _torch()
-    rows, K, wrows, N = _weight_shape(x, W, gated)
+    rows, K, code = _rows_of(x)
+    wrows, N = _weight_rows(W, gated)
     io, dev, L = x.dtype, x.device, lib()
-    code = _io_code(x)
     px, sx = _rows("x", x, K, rows, io, dev)
     lead = x.shape[:-1]
     if y is None:
         y = torch.empty(lead + (N,), dtype=io, device=dev)
     py, sy = _rows("y", y, N, rows, io, dev)
-    pr, sr = _rows("residual", residual, N, rows, io, dev)
+    pr, sr = (None, 0) if residual is None else _rows("residual", residual, N, rows, io, dev)
     if pre is None and want_pre:
         pre = torch.empty(lead + (wrows,), dtype=io, device=dev)
     ppre = _vec("pre", pre, lead + (wrows,), io, dev)
     pW = _vec("W", W, (wrows, K), io, dev)
-    dims = LinearDims(rows, K, N, sx, sy, sr, code, act, M3_FLAG_UNALIGNED if (px | pW) & 15 else 0, 0)
-    query = L.mamba3_gated_ffn_fwd_workspace_size if gated else L.mamba3_linear_fwd_workspace_size
-    workspace, pws, nws = _workspace(query, dims, workspace, dev)
     pb = _vec("bias", bias, (wrows,), torch.float32, dev)
+    dims = LinearDims(rows, K, N, sx, sy, sr, code, act, M3_FLAG_UNALIGNED if (px | pW) & 15 else 0, 0)
     s = _raw_stream(stream, dev)
-    st = (L.mamba3_gated_ffn_fwd(dims, px, pW, pb, py, ppre, pws, nws, s) if gated else
-          L.mamba3_linear_fwd(dims, px, pW, pb, pr, py, ppre, pws, nws, s))
+    if gated:
+        workspace, pws, nws = _workspace(L.mamba3_gated_ffn_fwd_workspace_size, dims, workspace, dev)
+        st = L.mamba3_gated_ffn_fwd(dims, px, pW, pb, py, ppre, pws, nws, s)
+    else:
+        workspace, pws, nws = _workspace(L.mamba3_linear_fwd_workspace_size, dims, workspace, dev)
+        st = L.mamba3_linear_fwd(dims, px, pW, pb, pr, py, ppre, pws, nws, s)
     _check(st, name)
     return y, pre
 
 
 def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, dx, dW, dbias, workspace, stream):
     torch = _torch()
-    rows, K, wrows, N = _weight_shape(x, W, gated)
+    rows, K, code = _rows_of(x)
+    wrows, N = _weight_rows(W, gated)
     io, dev, L = x.dtype, x.device, lib()
-    code = _io_code(x)
     px, sx = _rows("x", x, K, rows, io, dev)
     pdy, sdy = _rows("dy", dy, N, rows, io, dev)
-    if pre is None and (gated or act != M3_ACT_NONE):
+    ppre = None
+    if pre is not None:
+        ppre, spre = _rows("pre", pre, wrows, rows, io, dev)
+        if spre:
+            raise ValueError("pre: must be contiguous")
+    elif gated or act != M3_ACT_NONE:
         raise ValueError("pre is required (the forward's want_pre)")
-    ppre = _rows("pre", pre, wrows, rows, io, dev)
-    if ppre[1]:
-        raise ValueError("pre: must be contiguous")
+    pW = _vec("W", W, (wrows, K), io, dev)
     out = {}
     pdx = pdW = pb = None
     if want_dx or dx is not None:
-        out["dx"] = dx = torch.empty(x.shape, dtype=io, device=dev) if dx is None else dx
+        if dx is None:
+            dx = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
+        out["dx"] = dx
         pdx = _vec("dx", dx, x.shape, io, dev)
     if want_dW or dW is not None:
-        out["dW"] = dW = torch.empty((wrows, K), dtype=io, device=dev) if dW is None else dW
+        out["dW"] = dW = torch.empty_like(W) if dW is None else dW
         pdW = _vec("dW", dW, (wrows, K), io, dev)
     if want_dbias or dbias is not None:
         out["dbias"] = dbias = torch.empty(wrows, dtype=torch.float32, device=dev) if dbias is None else dbias
         pb = _vec("dbias", dbias, (wrows,), torch.float32, dev)
-    pW = _vec("W", W, (wrows, K), io, dev)
     dims = LinearDims(rows, K, N, sx, sdy, 0, code, act, M3_FLAG_UNALIGNED if (px | pW | pdy) & 15 else 0, 0)
-    query = L.mamba3_gated_ffn_bwd_workspace_size if gated else L.mamba3_linear_bwd_workspace_size
+    query, call = ((L.mamba3_gated_ffn_bwd_workspace_size, L.mamba3_gated_ffn_bwd) if gated else
+                   (L.mamba3_linear_bwd_workspace_size, L.mamba3_linear_bwd))
     workspace, pws, nws = _workspace(query, dims, workspace, dev)
-    call = L.mamba3_gated_ffn_bwd if gated else L.mamba3_linear_bwd
-    st = call(dims, px, pW, ppre[0], pdy, pdx, pdW, pb, pws, nws,
-              _raw_stream(stream, dev))
+    st = call(dims, px, pW, ppre, pdy, pdx, pdW, pb, pws, nws, _raw_stream(stream, dev))
     _check(st, name)
     return out
 
