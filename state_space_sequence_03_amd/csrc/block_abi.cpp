@@ -226,17 +226,15 @@ m3_status linear_bwd(const m3_linear_dims* d, bool gated, const void* x, const v
   if (w.pack_w && dx) pk.add(a.Q, a.ldq, n, d->d_in, w.w);
   if (m3::launch_pack(io, pk.args, s) != hipSuccess) return M3_ERR_HIP;
   b.P = a.P; b.ldp = a.ldp;
-  if (dx) {
-    a.M = d->rows; a.N = d->d_in; a.K = n;
-    a.out = dx; a.ldo = d->d_in;
-    if (m3::launch_mm(io, m3::MM_P_K, m3::MM_STORE, a, w.dx, s) != hipSuccess) return M3_ERR_HIP;
-  }
-  if (dW) {
-    b.M = n; b.N = d->d_in; b.K = d->rows;
-    b.out = dW; b.ldo = d->d_in;
-    if (m3::launch_mm(io, m3::MM_NONE_K, m3::MM_STORE, b, w.dw, s) != hipSuccess) return M3_ERR_HIP;
-  }
-  return M3_OK;
+  a.M = d->rows; a.N = d->d_in; a.K = n;
+  a.out = dx; a.ldo = d->d_in;
+  b.M = n; b.N = d->d_in; b.K = d->rows;
+  b.out = dW; b.ldo = d->d_in;
+  hipError_t e = hipSuccess;
+  if (dx && dW) e = m3::launch_mm_pair(io, a, w.dx, b, w.dw, s);
+  else if (dx) e = m3::launch_mm(io, m3::MM_P_K, m3::MM_STORE, a, w.dx, s);
+  else if (dW) e = m3::launch_mm(io, m3::MM_NONE_K, m3::MM_STORE, b, w.dw, s);
+  return hip_status(e);
 }
 
 }  // namespace

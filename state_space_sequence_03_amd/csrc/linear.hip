@@ -15,22 +15,27 @@ struct TileCost {
   double alone[2], shared[2], ends;
 };
 constexpr TileCost kTiles[] = {{256, {1.05, 7.2}, {1.05, 7.2}, 6.0},
-                               {128, {0.70, 2.1}, {0.60, 2.1}, 1.0},
+                               {128, {0.60, 2.1}, {0.50, 2.1}, 2.0},
                                {64, {0.32, 0.62}, {0.26, 0.61}, 0.5}};
-constexpr double kJoin = 6.0, kJoinBytesPerUs = 1.0e7;
+constexpr double kJoin = 6.0;
+// parts that the caches hold are joined twice as fast
+inline double join_time(double bytes) { return kJoin + bytes / (bytes < 4.0e7 ? 1.0e7 : 5.0e6); }
 
 }  // namespace
 
 MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
   MmPlan best{};
-  if (epi != MM_STORE && M <= MM_FEW_ROWS) return best;
   const int es = io_bf16 ? 2 : 4, ty = io_bf16 ? 0 : 1;
+  const int gated = epi == MM_GATED ? 2 : 1;
+  // the few-row kernel: every block reads all of P, so that more rows pay only
+  // where Q is small too (64 rows through 256 -> 512: 3.7 us against 4.8
+  // tiled; through 2048 -> 2 x 5632: 26.7 against 16.2)
+  if (epi != MM_STORE && (M <= 32 || (M <= 64 && N * gated * K * es <= (int64_t(4) << 20)))) return best;
   const int total = (int)((K * es + 127) / 128);  // stages of 128 bytes
   double least = 0.0;
   for (const TileCost& c : kTiles) {
     MmPlan p{};
     p.tile = c.tile;
-    const int gated = epi == MM_GATED ? 2 : 1;
     const int64_t bm = c.tile, bn = c.tile == 64 ? 64 * gated : c.tile;
     p.ntm = (int)((M + bm - 1) / bm);
     p.ntn = (int)((N * gated + bn - 1) / bn);
@@ -52,7 +57,7 @@ MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
       const int st = s == 1 ? p.whole : stages((total + s - 1) / s);
       if (s > 1 && (rest == 0 || st < 4 || (total + st - 1) / st != s)) continue;
       const double bytes = s == 1 ? 0.0 : (double)(rest * s * bm * bn) * 8.0;
-      const double t = rounds + time(rest * s, st) + (s == 1 ? 0.0 : kJoin + bytes / kJoinBytesPerUs);
+      const double t = rounds + time(rest * s, st) + (s == 1 ? 0.0 : join_time(bytes));
       if (best.tile != 0 && t >= least) continue;
       least = t;
       p.split = s;
@@ -72,6 +77,14 @@ hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs&
   if (layout != MM_PQ_K) return hipErrorInvalidValue;
   if (epi == MM_LINEAR) return io_bf16 ? mm_linear_bf16(a, plan, s) : mm_linear_f32(a, plan, s);
   return io_bf16 ? mm_gated_bf16(a, plan, s) : mm_gated_f32(a, plan, s);
+}
+
+hipError_t launch_mm_pair(int io_bf16, const MmArgs& dx, const MmPlan& px, const MmArgs& dw, const MmPlan& pw,
+                          hipStream_t s) {
+  if (px.tile == 64 && pw.tile == 64 && px.split == 1 && pw.split == 1 && px.items + pw.items <= mm_room(64) - 8)
+    return io_bf16 ? mm_pair_bf16(dx, px, dw, pw, s) : mm_pair_f32(dx, px, dw, pw, s);
+  const hipError_t e = launch_mm(io_bf16, MM_P_K, MM_STORE, dx, px, s);
+  return e != hipSuccess ? e : launch_mm(io_bf16, MM_NONE_K, MM_STORE, dw, pw, s);
 }
 
 }  // namespace m3

@@ -200,7 +200,7 @@ struct MmArgs {
 // kernel), the first `full` of them whole, the others split over k into
 // `split` parts of `stages` stages of 128 bytes, which a second kernel joins.
 struct MmPlan {
-  int tile, ntm, ntn, full, split;
+  int tile, ntm, ntn, full, split;  // tile 0 takes rows of any alignment
   int stages, whole;  // stages of a part and of a whole tile (both even)
   int items;          // full + split parts
   size_t part_bytes;
@@ -211,8 +211,10 @@ MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K);
 // The tiled kernels need rows of P and Q that start on 16 bytes; a row along
 // k whose last 16 bytes are partial must be backed by zeros up to there.
 hipError_t launch_mm(int io_bf16, MmLayout layout, MmEpilogue epi, const MmArgs& a, const MmPlan& plan, hipStream_t s);
-// The few-row kernel (rows of P and Q along k) takes any alignment.
-constexpr int MM_FEW_ROWS = 64;
+// dx (P along k) and dW (neither along k) of one backward: in one launch
+// where both are of whole 64 x 64 tiles that fit the chip at once, else in two.
+hipError_t launch_mm_pair(int io_bf16, const MmArgs& dx, const MmPlan& px, const MmArgs& dw, const MmPlan& pw,
+                          hipStream_t s);
 
 // Copies of up to three matrices with rows padded by zeros to `ld` elements
 // (a multiple of 16 bytes).

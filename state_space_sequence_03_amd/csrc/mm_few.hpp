@@ -1,11 +1,15 @@
 // Products of few rows (generation steps): bound by reading Q once.
 //
 // A block owns 16 rows of Q (gated: 16 of each half) and its eight waves
-// split k: step s of wave w covers the 64 bytes of k at (8 s + w) * 64, one
-// 16-byte load per lane and operand straight into the fragment layout of the
-// 16 x 16 products (lane l: row l mod 16, 16 bytes l / 16), no LDS on the way.
-// U steps' loads are issued before their products, so that a wave has U KB
-// (gated 2U) of Q in flight.  The waves' sums are joined in LDS in order.
+// split k in runs of U steps of 64 bytes: one 16-byte load per lane and
+// operand straight into the fragment layout of the 16 x 16 products (lane l:
+// row l mod 16, 16 bytes l / 16), no LDS on the way.  A run's loads are issued
+// before its products, so that a wave has U KB (gated 2U) of Q in flight.  The
+// waves' sums are joined in LDS in order.  One row through 2048 -> 2 x 5632
+// takes 10.2 us (46 MB: 4.5 TB/s), 16 rows 13.1: every block reads all of P,
+// from its L2.
+// (Sixteen waves, for calls with fewer blocks than CUs, measured the same: 7.1
+// us for one row of 4096 -> 2048.)
 // Rows of P past the last and rows of Q past N repeat the last row; their
 // outputs are not written.
 #pragma once
@@ -45,8 +49,8 @@ template <typename T, int EPI, int ACT, int MT>
 __global__ __launch_bounds__(512) void mm_few_kernel(MmArgs a) {
   constexpr int ES = io<T>::BYTES;
   constexpr bool G = EPI == MM_GATED;
-  constexpr int QT = G ? 2 : 1, U = MT == 1 ? 8 : 4;
-  __shared__ f32x4 sh[8][QT * MT][64];
+  constexpr int NW = 8, QT = G ? 2 : 1, U = MT == 1 ? 8 : 4;
+  __shared__ f32x4 sh[NW][QT * MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int r = lane & 15, c16 = (lane >> 4) * 16;
@@ -68,17 +72,19 @@ __global__ __launch_bounds__(512) void mm_few_kernel(MmArgs a) {
   for (int i = 0; i < QT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  int b = wave * 64 + c16;
-  // whole 64-byte steps, U at a time
-  for (; b - c16 + (U - 1) * 512 + 64 <= bytes; b += U * 512) {
+  // whole runs of U steps per wave
+  int k0 = 0;
+  for (; k0 + NW * U * 64 <= bytes; k0 += NW * U * 64) {
+    const int b = k0 + wave * U * 64 + c16;
     u32x4 fq[U][QT], fp[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int i = 0; i < QT; ++i) fq[u][i] = *(const u32x4_any*)(q[i] + b + u * 512);
+      for (int i = 0; i < QT; ++i) fq[u][i] = *(const u32x4_any*)(q[i] + b + u * 64);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) fp[u][j] = *(const u32x4_any*)(p[j] + b + u * 512);
+      for (int j = 0; j < MT; ++j) fp[u][j] = *(const u32x4_any*)(p[j] + b + u * 64);
     }
+    __builtin_amdgcn_sched_barrier(0);  // all of them before the first product
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -86,7 +92,7 @@ __global__ __launch_bounds__(512) void mm_few_kernel(MmArgs a) {
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = mma16<T>(fq[u][i], fp[u][j], acc[i][j]);
   }
-  for (; b - c16 < bytes; b += 512) {
+  for (int b = k0 + wave * 64 + c16; b - c16 < bytes; b += NW * 64) {
     u32x4 fq[QT], fp[MT];
 #pragma unroll
     for (int i = 0; i < QT; ++i) fq[i] = few_load<T>(q[i], b, bytes);
@@ -105,13 +111,13 @@ __global__ __launch_bounds__(512) void mm_few_kernel(MmArgs a) {
   // thread e: column e mod 16 of row e / 16; its sum sits in lane
   // row + 16 (column / 4), word column mod 4
   constexpr bool FINE = ES == 4;
-  for (int e = threadIdx.x; e < MT * 256; e += 512) {
+  for (int e = threadIdx.x; e < MT * 256; e += 64 * NW) {
     const int j = e >> 8, row = (e >> 4) & 15, col = e & 15, l = row + 16 * (col >> 2), w = col & 3;
     const int64_t m = j * 16 + row, n = n0 + col;
     if (m >= a.M || n >= a.N) continue;
     float z = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < NW; ++k) {
       z += sh[k][j][l][w];
       if constexpr (G) u += sh[k][MT + j][l][w];
     }

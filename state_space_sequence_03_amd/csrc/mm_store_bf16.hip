@@ -10,4 +10,8 @@ hipError_t mm_store_bf16(MmLayout layout, const MmArgs& a, const MmPlan& plan, h
   return hipErrorInvalidValue;
 }
 
+hipError_t mm_pair_bf16(const MmArgs& a, const MmPlan& pa, const MmArgs& b, const MmPlan& pb, hipStream_t s) {
+  return mm_pair_run<bf16_t>(a, pa, b, pb, s);
+}
+
 }  // namespace m3

@@ -10,4 +10,8 @@ hipError_t mm_store_f32(MmLayout layout, const MmArgs& a, const MmPlan& plan, hi
   return hipErrorInvalidValue;
 }
 
+hipError_t mm_pair_f32(const MmArgs& a, const MmPlan& pa, const MmArgs& b, const MmPlan& pb, hipStream_t s) {
+  return mm_pair_run<float>(a, pa, b, pb, s);
+}
+
 }  // namespace m3

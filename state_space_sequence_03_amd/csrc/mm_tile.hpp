@@ -334,16 +334,19 @@ __device__ __forceinline__ void mix_k_step() {
 // few 256 x 256 tiles to fill the chip.
 //
 // k advances by 128 bytes per stage through NBUF stages of LDS.  A stage has
-// four k-steps of 32 bytes; a wave reads the fragments of the next k-step
-// while the products of this one run, across the stage's end too: after the
-// third k-step every wave holds the fragments of the fourth in registers, so
-// one barrier there frees this stage's LDS for the loads of NBUF stages later
-// and publishes the next stage, whose first fragments are read under the
-// fourth k-step's products.
+// four k-steps of 32 bytes; a wave reads the fragments of the next two k-steps
+// while the products of these two run, across the stage's end too: half way through, every wave holds the second half's
+// fragments in registers, so one barrier there frees this stage's LDS for the
+// loads of NBUF stages later and publishes the next stage, whose first
+// fragments are read under the second half's products.
 //
 // Blocks stay: each walks several items (a tile, or a tile's part of k), and
 // the stage after an item's last is the next item's first, so that its loads
 // are in flight during the epilogue.
+//
+// PER blocks share a CU: two where there are more items than CUs; where a
+// block is alone on its CU, nobody covers its waits, and it takes all of the
+// LDS for a pipeline twice as deep.
 // ---------------------------------------------------------------------------
 struct MmItem {
   int64_t m0, n0;  // first row and column of out
@@ -370,12 +373,14 @@ __device__ __forceinline__ MmItem mm_item(const MmPlan& pl, int id) {
 // whole tiles and one of the parts, so that its blocks in flight share operand
 // tiles in its L2.
 struct MmWalk {
-  int step, f0, nf, p0, end;  // the block's items: blockIdx / 8, + step, ... below end
-  __device__ __forceinline__ explicit MmWalk(const MmPlan& pl) {
-    const int xcd = blockIdx.x & 7;
+  int id, step, f0, nf, p0, end;  // the block's items: id, id + step, ... below end
+  // block of blocks; block 0 is on the first XCD of its eight
+  __device__ __forceinline__ MmWalk(const MmPlan& pl, int block, int blocks) {
+    const int xcd = block & 7;
+    id = block >> 3;
     auto first = [&](int n) { return xcd * (n >> 3) + (xcd < (n & 7) ? xcd : (n & 7)); };
     auto count = [&](int n) { return (n >> 3) + (xcd < (n & 7) ? 1 : 0); };
-    step = (gridDim.x + 7 - xcd) >> 3;  // blocks of this XCD
+    step = (blocks + 7 - xcd) >> 3;  // blocks of this XCD
     f0 = first(pl.full);
     nf = count(pl.full);
     p0 = pl.full + first(pl.items - pl.full);
@@ -443,7 +448,7 @@ __device__ __forceinline__ void mm_finish(const MmArgs& a, const MmItem& it, f32
 }
 
 template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN, int NBUF>
-__global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
+__device__ __forceinline__ void mm_tile_walk(const MmArgs& a, const MmPlan& pl, char* smem, int block, int blocks) {
   constexpr bool PK = LAYOUT != MM_NONE_K, QK = LAYOUT == MM_PQ_K;
   constexpr int ES = io<T>::BYTES;
   constexpr bool G = EPI == MM_GATED;
@@ -452,11 +457,9 @@ __global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
   typedef Operand<T, PK, BM> OP;
   typedef Operand<T, QK, BN> OQ;
   constexpr int STAGE = OP::BYTES + OQ::BYTES;
-  static_assert(2 * NBUF * STAGE <= 163840, "two blocks per CU");
-  __shared__ __attribute__((aligned(1024))) char smem[NBUF * STAGE];
 
-  const MmWalk walk(pl);
-  int id = blockIdx.x >> 3;
+  const MmWalk walk(pl, block, blocks);
+  int id = walk.id;
   if (id >= walk.end) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -485,40 +488,42 @@ __global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
   fq.init(G ? wn * (BN / 4) : wn * (BN / 2), lane);
 
   f32x16 acc[NT][MT];
-  // of one k-step: matrix instructions and LDS reads
-  constexpr int NM = MT * NT * (ES == 2 ? 1 : 4);
-  constexpr int NR = MT * (PK ? 1 : ES == 2 ? 2 : 4) + NT * (QK ? 1 : ES == 2 ? 2 : 4);
-  uint4 p[2][MT], q[2][NT];
-  auto read = [&](int at, int s, int to) {
+  // of two k-steps: matrix instructions and LDS reads
+  constexpr int NM = 2 * MT * NT * (ES == 2 ? 1 : 4);
+  constexpr int NR = 2 * (MT * (PK ? 1 : ES == 2 ? 2 : 4) + NT * (QK ? 1 : ES == 2 ? 2 : 4));
+  uint4 p[2][2][MT], q[2][2][NT];
+  auto read = [&](int at, int half) {  // k-steps 2 half, 2 half + 1
     const char* l = smem + at;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) p[to][j] = fp.read(l, j, s);
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) q[to][i] = fq.read(l + OP::BYTES, i, s);
+      for (int j = 0; j < MT; ++j) p[half][s][j] = fp.read(l, j, 2 * half + s);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) q[half][s][i] = fq.read(l + OP::BYTES, i, 2 * half + s);
+    }
   };
-  auto multiply = [&](int from) {
+  auto multiply = [&](int half) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = mma32<T>(q[from][i], p[from][j], acc[i][j]);
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = mma32<T>(q[half][s][i], p[half][s][j], acc[i][j]);
   };
   // the loads run ahead of the products: the item and stage they are at
   int lid = id;
   MmItem lt = walk.item<BM, BC>(pl, id);
   int lk = 0, ln = lt.part < 0 ? pl.whole : pl.stages;
-  auto load_next = [&](int at) {
-    load(lt, lt.kb + lk, at);
-    if (++lk == ln) {
-      lid += walk.step;
-      if (lid < walk.end) {
-        lt = walk.item<BM, BC>(pl, lid);
-        ln = lt.part < 0 ? pl.whole : pl.stages;
-        lk = 0;
-      } else {  // nothing left: stages past K, which read zeros
-        lt.kb = pl.whole;
-        lk = 0;
-        ln = 0x7fffffff;
-      }
+  auto advance = [&] {
+    if (++lk < ln) return;
+    lk = 0;
+    lid += walk.step;
+    if (lid < walk.end) {
+      lt = walk.item<BM, BC>(pl, lid);
+      ln = lt.part < 0 ? pl.whole : pl.stages;
+    } else {  // nothing left: stages past K, which read zeros
+      lt.kb = pl.whole;
+      ln = 0x7fffffff;
     }
   };
   constexpr int NL = OP::NI + OQ::NI;    // loads of a stage
@@ -533,9 +538,12 @@ __global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
     asm volatile("" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < NBUF; ++i) load_next(i * STAGE);
+  for (int i = 0; i < NBUF; ++i) {
+    load(lt, lt.kb + lk, i * STAGE);
+    advance();
+  }
   settle(std::integral_constant<int, AHEAD + NL>{});
-  read(0, 0, 0);
+  read(0, 0);
   int at = 0;
   for (; id < walk.end; id += walk.step) {
     const MmItem it = walk.item<BM, BC>(pl, id);
@@ -548,19 +556,16 @@ __global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     for (int kb = 0; kb < nk; ++kb) {
       const int nxt = at == (NBUF - 1) * STAGE ? 0 : at + STAGE;
-      read(at, 1, 1);
-      multiply(0);
-      mix_k_step<NM, NR, 0>();
-      read(at, 2, 0);
-      multiply(1);
-      mix_k_step<NM, NR, 0>();
-      read(at, 3, 1);
+      read(at, 1);
       multiply(0);
       mix_k_step<NM, NR, 0>();
       settle(std::integral_constant<int, AHEAD>{});
-      read(nxt, 0, 0);
-      load_next(at);
+      read(nxt, 0);
+      load(lt, lt.kb + lk, at);
       multiply(1);
+      mix_k_step<NM, NR, NL>();
+      __builtin_amdgcn_sched_barrier(0);
+      advance();
       at = nxt;
     }
     // opaque, so that the epilogue's addresses are not kept in registers
@@ -570,6 +575,23 @@ __global__ __launch_bounds__(256, 2) void mm_tile_kernel(MmArgs a, MmPlan pl) {
     mm_finish<T, EPI, ACT, BM, BN>(a, it, acc, el, ew);
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the loads past the last item (zeros) have landed
+}
+
+template <typename T, int LAYOUT, int EPI, int ACT, int BM, int BN, int NBUF, int PER>
+__global__ __launch_bounds__(256, PER) void mm_tile_kernel(MmArgs a, MmPlan pl) {
+  static_assert(PER * NBUF * (BM + BN) * 128 <= 163840, "blocks per CU");
+  __shared__ __attribute__((aligned(1024))) char smem[NBUF * (BM + BN) * 128];
+  mm_tile_walk<T, LAYOUT, EPI, ACT, BM, BN, NBUF>(a, pl, smem, blockIdx.x, gridDim.x);
+}
+
+// Both products of a small backward in one launch (each launch costs the host
+// as long as such a product takes): the first `na` blocks do dx, the others
+// dW.
+template <typename T>
+__global__ __launch_bounds__(256, 2) void mm_pair_kernel(MmArgs a, MmPlan pa, MmArgs b, MmPlan pb, int na) {
+  __shared__ __attribute__((aligned(1024))) char smem[4 * 128 * 128];
+  if ((int)blockIdx.x < na) mm_tile_walk<T, MM_P_K, MM_STORE, ACT_NONE, 64, 64, 4>(a, pa, smem, blockIdx.x, na);
+  else mm_tile_walk<T, MM_NONE_K, MM_STORE, ACT_NONE, 64, 64, 4>(b, pb, smem, blockIdx.x - na, gridDim.x - na);
 }
 
 // Adds the parts of the split tiles in order and applies the epilogue: one

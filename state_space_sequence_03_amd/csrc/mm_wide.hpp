@@ -257,8 +257,8 @@ __global__ __launch_bounds__(256, 1) void mm_wide_kernel(MmArgs a, MmPlan pl) {
   __shared__ __attribute__((aligned(1024))) char smem[BIAS + (ES == 2 ? 1024 : 0)];
   float* const bias = (float*)(smem + BIAS);
 
-  const MmWalk walk(pl);
-  int id = blockIdx.x >> 3;
+  const MmWalk walk(pl, blockIdx.x, gridDim.x);
+  int id = walk.id;
   if (id >= walk.end) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
