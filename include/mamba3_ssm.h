@@ -340,7 +340,7 @@ size_t mamba3_bc_prologue_workspace_size(const m3_dims* d);
  * unless flags holds M3_FLAG_UNALIGNED, which makes the call copy them (the
  * workspace queries count it in); every other pointer its element's size,
  * the workspaces 16.  Limits
- * (M3_ERR_UNSUPPORTED): widths and strides at most 2^20, rows at most 2^24,
+ * (M3_ERR_UNSUPPORTED): widths and strides at most 2^20, rows at most 2^24 - 1,
  * and at most 2^24 - 1 tiles of 64 x 64 outputs in any product of a call.
  * With rows = 0 nothing is read and no row written; gradients summed over the
  * rows (dW, dgain, dbias) are written as zeros.

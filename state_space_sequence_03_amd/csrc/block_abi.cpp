@@ -10,7 +10,7 @@
 namespace {
 
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
-constexpr int64_t kMaxRows = int64_t(1) << 24;
+constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;  // a block of 256 threads each stays under 2^32
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

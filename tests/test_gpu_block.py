@@ -184,7 +184,7 @@ def check_bwd(ops, io, name, x, W, dy, pre, is_gated):
     code = getattr(ops, "M3_ACT_" + name.upper())
     call = ops.gated_ffn_bwd if is_gated else ops.linear_bwd
     out = call(x, W, dy, pre, act=code)
-    hp, hd = host(pre), host(dy)
+    hp, hd = None if pre is None else host(pre), host(dy)
     dp = block.dp_gated(hp, hd, name) if is_gated else block.dp_linear(hp, hd, name)
     u_dp = unit(io) if is_gated or name != "none" else 0.0
     bounds = block.products_bound(dp, block.dp_eval(hp, hd, name, is_gated), host(x), host(W), unit(io), u_dp)
@@ -237,6 +237,81 @@ def test_larger_products(ops, io, M, K, N, name):
         res = None if is_gated else draw(r, (M, N), io)
         pre = check_fwd(ops, io, name, x, W, bias, res, is_gated)
         check_bwd(ops, io, name, x, W, dy, pre, is_gated)
+
+
+# the widest tiles: more of them than CUs, so that some are whole and the last
+# ones split over k, with ragged edges (M, N) or none (4096), K short, odd or
+# off the tile's stages
+WIDE = [(4100, 520, 4000, "silu"), (4096, 200, 4352, "gelu"), (8200, 65, 2304, "none"), (4097, 1031, 4103, "relu")]
+
+
+@pytest.mark.parametrize("M,K,N,name", WIDE)
+def test_wide_tiles(ops, M, K, N, name):
+    r = np.random.default_rng(M + K)
+    for is_gated in (False, True):
+        n = N // 2 if is_gated else N
+        say(f"{'gated' if is_gated else 'linear'} {M} x {K} x {n} {name}")
+        x, W, bias, dy = product_inputs(r, "bf16", M, K, n, is_gated)
+        res = None if is_gated else draw(r, (M, n), "bf16")
+        pre = check_fwd(ops, "bf16", name, x, W, bias, res, is_gated)
+        check_fwd(ops, "bf16", name, x, W, None, None, is_gated)
+        check_bwd(ops, "bf16", name, x, W, dy, pre, is_gated)
+
+
+def test_wide_tiles_f32(ops):
+    r = np.random.default_rng(77)
+    for is_gated in (False, True):
+        n = 2000 if is_gated else 4000
+        x, W, bias, dy = product_inputs(r, "f32", 4100, 132, n, is_gated)
+        pre = check_fwd(ops, "f32", "silu", x, W, bias, None, is_gated)
+        check_bwd(ops, "f32", "silu", x, W, dy, pre, is_gated)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,N", [(5, 64, 48), (70, 64, 72), (300, 512, 256)])
+def test_pointers_off_16_bytes(ops, io, M, K, N):
+    # rows of whole 16 bytes that start off them: every operand a view one element into its buffer
+    r = np.random.default_rng(M + K + N)
+
+    def off(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    for is_gated in (False, True):
+        x, W, bias, dy = product_inputs(r, io, M, K, N, is_gated)
+        pre = check_fwd(ops, io, "silu", off(x), off(W), off(bias), None, is_gated)
+        check_bwd(ops, io, "silu", off(x), off(W), off(dy), off(pre), is_gated)
+        if not is_gated:
+            check_bwd(ops, io, "none", x, W, off(dy), None, False)
+
+
+def test_graph_replays(ops):
+    # a block's forward and backward captured once; every replay equals the eager call
+    r = np.random.default_rng(55)
+    x, W, bias, dy = product_inputs(r, "bf16", 1000, 264, 520, True)
+    gain = draw(r, 264, "f32")
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def block_step():
+        n, mean, rstd = ops.layer_norm_fwd(x, gain, want_stats=True)
+        h, pre = ops.gated_ffn_fwd(n, W, bias, want_pre=True, workspace=ws)
+        g = ops.gated_ffn_bwd(n, W, dy, pre, workspace=ws)
+        b = ops.layer_norm_bwd(x, mean, rstd, g["dx"], gain, workspace=ws)
+        return [h, g["dW"], g["dbias"], b["dx"], b["dgain"], b["dbias"]]
+
+    block_step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block_step()
+    for k in range(4):
+        x.copy_(draw(r, (1000, 264), "bf16"))
+        want = [t.clone() for t in block_step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), k
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
