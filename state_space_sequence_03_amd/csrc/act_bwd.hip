@@ -129,9 +129,11 @@ hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Slabs of rows: eight rows each until there are 64; up to 64 rows one slab,
+// which needs no second kernel for its sums.
 int64_t act_bwd_parts(int64_t rows) {
-  const int64_t p = (rows + 63) / 64;
-  return p < 64 ? p : 64;
+  const int64_t p = (rows + 7) / 8;
+  return rows <= 64 ? 1 : p < 64 ? p : 64;
 }
 
 hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s) {

@@ -12,11 +12,11 @@ namespace {
 // join of split tiles (a launch, and the parts written and read).
 struct TileCost {
   int tile;
-  double alone[2], shared[2], ends;
+  double alone[2], shared[2], ends[2];
 };
-constexpr TileCost kTiles[] = {{256, {1.05, 7.2}, {1.05, 7.2}, 6.0},
-                               {128, {0.60, 2.1}, {0.50, 2.1}, 2.0},
-                               {64, {0.32, 0.62}, {0.26, 0.61}, 0.5}};
+constexpr TileCost kTiles[] = {{256, {1.05, 7.2}, {1.05, 7.2}, {6.0, 6.0}},
+                               {128, {0.60, 2.1}, {0.50, 2.1}, {2.0, 6.0}},
+                               {64, {0.32, 0.62}, {0.26, 0.61}, {0.5, 0.5}}};
 constexpr double kJoin = 6.0;
 // parts that the caches hold are joined twice as fast
 inline double join_time(double bytes) { return kJoin + bytes / (bytes < 4.0e7 ? 1.0e7 : 5.0e6); }
@@ -46,7 +46,7 @@ MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
     auto time = [&](int64_t items, int st) {  // of one round of items of st stages
       const int64_t n = (items + 255) / 256;
       const double wide = c.tile == 64 && gated == 2 ? 1.8 : 1.0;  // 64 x 128 of W's rows there
-      return n == 0 ? 0.0 : (n < per ? st * c.alone[ty] : n * st * c.shared[ty]) * wide + n * c.ends;
+      return n == 0 ? 0.0 : (n < per ? st * c.alone[ty] : n * st * c.shared[ty]) * wide + n * c.ends[ty];
     };
     p.whole = stages(total);
     const int64_t rest = tiles % room;
@@ -55,7 +55,8 @@ MmPlan mm_plan(int io_bf16, MmEpilogue epi, int64_t M, int64_t N, int64_t K) {
     // the chip
     for (int s = 1; s <= 64; ++s) {
       const int st = s == 1 ? p.whole : stages((total + s - 1) / s);
-      if (s > 1 && (rest == 0 || st < 4 || (total + st - 1) / st != s)) continue;
+      if (s > 1 && (rest == 0 || st < 4 || rest * s > 4 * room)) break;
+      if (s > 1 && (total + st - 1) / st != s) continue;
       const double bytes = s == 1 ? 0.0 : (double)(rest * s * bm * bn) * 8.0;
       const double t = rounds + time(rest * s, st) + (s == 1 ? 0.0 : join_time(bytes));
       if (best.tile != 0 && t >= least) continue;

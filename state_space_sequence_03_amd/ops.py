@@ -566,11 +566,11 @@ def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, works
     px, sx = _rows("x", x, K, rows, io, dev)
     lead = x.shape[:-1]
     if y is None:
-        y = torch.empty(lead + (N,), dtype=io, device=dev)
+        y = x.new_empty(lead + (N,))
     py, sy = _rows("y", y, N, rows, io, dev)
     pr, sr = (None, 0) if residual is None else _rows("residual", residual, N, rows, io, dev)
     if pre is None and want_pre:
-        pre = torch.empty(lead + (wrows,), dtype=io, device=dev)
+        pre = x.new_empty(lead + (wrows,))
     ppre = _vec("pre", pre, lead + (wrows,), io, dev)
     pW = _vec("W", W, (wrows, K), io, dev)
     pb = _vec("bias", bias, (wrows,), torch.float32, dev)
