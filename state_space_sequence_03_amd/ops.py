@@ -460,11 +460,13 @@ def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=Non
     io, dev, f32 = x.dtype, x.device, torch.float32
     px, sx = _rows("x", x, D, rows, io, dev)
     if y is None:
-        y = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
+        y = torch.empty_like(x) if sx == 0 else x.new_empty(x.shape)
+        py, sy = y.data_ptr(), 0
+    else:
+        py, sy = _rows("y", y, D, rows, io, dev)
     if want_stats or mean is not None or rstd is not None:
         mean = torch.empty(rows, dtype=f32, device=dev) if mean is None else mean
         rstd = torch.empty_like(mean) if rstd is None else rstd
-    py, sy = _rows("y", y, D, rows, io, dev)
     st = lib().mamba3_layer_norm_fwd(NormDims(rows, D, sx, sy, 0, code, 0), px, _vec("gain", gain, (D,), f32, dev),
                                      _vec("bias", bias, (D,), f32, dev), eps, py,
                                      _vec("mean", mean, (rows,), f32, dev), _vec("rstd", rstd, (rows,), f32, dev),
@@ -496,18 +498,24 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
             if ssk:
                 dx = torch.empty_strided((rows, D), (ssk, 1), dtype=io, device=dev)
             else:
-                dx = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
-        pdx, sdx = _rows("dx", dx, D, rows, io, dev)
-        if dskip is not None and (sdx or D) != (ssk or D):
-            raise ValueError("dx and dskip must have the same row stride")
-        ssk = sdx
+                dx = torch.empty_like(x) if sx == 0 else x.new_empty(x.shape)
+            pdx = dx.data_ptr()
+        else:
+            pdx, sdx = _rows("dx", dx, D, rows, io, dev)
+            if dskip is not None and (sdx or D) != (ssk or D):
+                raise ValueError("dx and dskip must have the same row stride")
+            ssk = sdx
         out["dx"] = dx
-    if want_dgain or dgain is not None:
-        out["dgain"] = dgain = torch.empty(D, dtype=f32, device=dev) if dgain is None else dgain
-        pg = _vec("dgain", dgain, (D,), f32, dev)
-    if want_dbias or dbias is not None:
-        out["dbias"] = dbias = torch.empty(D, dtype=f32, device=dev) if dbias is None else dbias
-        pb = _vec("dbias", dbias, (D,), f32, dev)
+    if dgain is not None:
+        out["dgain"], pg = dgain, _vec("dgain", dgain, (D,), f32, dev)
+    elif want_dgain:
+        out["dgain"] = dgain = torch.empty(D, dtype=f32, device=dev)
+        pg = dgain.data_ptr()
+    if dbias is not None:
+        out["dbias"], pb = dbias, _vec("dbias", dbias, (D,), f32, dev)
+    elif want_dbias:
+        out["dbias"] = dbias = torch.empty(D, dtype=f32, device=dev)
+        pb = dbias.data_ptr()
     dims = NormDims(rows, D, sx, sdy, ssk, code, 0)
     L = lib()
     if pg or pb:
@@ -564,14 +572,18 @@ def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, works
     wrows, N = _weight_rows(W, gated)
     io, dev, L = x.dtype, x.device, lib()
     px, sx = _rows("x", x, K, rows, io, dev)
-    lead = x.shape[:-1]
     if y is None:
-        y = x.new_empty(lead + (N,))
-    py, sy = _rows("y", y, N, rows, io, dev)
+        y = x.new_empty(x.shape[:-1] + (N,))
+        py, sy = y.data_ptr(), 0
+    else:
+        py, sy = _rows("y", y, N, rows, io, dev)
     pr, sr = (None, 0) if residual is None else _rows("residual", residual, N, rows, io, dev)
-    if pre is None and want_pre:
-        pre = x.new_empty(lead + (wrows,))
-    ppre = _vec("pre", pre, lead + (wrows,), io, dev)
+    ppre = None
+    if pre is not None:
+        ppre = _vec("pre", pre, x.shape[:-1] + (wrows,), io, dev)
+    elif want_pre:
+        pre = x.new_empty(x.shape[:-1] + (wrows,))
+        ppre = pre.data_ptr()
     pW = _vec("W", W, (wrows, K), io, dev)
     pb = _vec("bias", bias, (wrows,), torch.float32, dev)
     dims = LinearDims(rows, K, N, sx, sy, sr, code, act, M3_FLAG_UNALIGNED if (px | pW) & 15 else 0, 0)
@@ -603,17 +615,21 @@ def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, 
     pW = _vec("W", W, (wrows, K), io, dev)
     out = {}
     pdx = pdW = pb = None
-    if want_dx or dx is not None:
-        if dx is None:
-            dx = torch.empty_like(x) if sx == 0 else torch.empty(x.shape, dtype=io, device=dev)
-        out["dx"] = dx
-        pdx = _vec("dx", dx, x.shape, io, dev)
-    if want_dW or dW is not None:
-        out["dW"] = dW = torch.empty_like(W) if dW is None else dW
-        pdW = _vec("dW", dW, (wrows, K), io, dev)
-    if want_dbias or dbias is not None:
-        out["dbias"] = dbias = torch.empty(wrows, dtype=torch.float32, device=dev) if dbias is None else dbias
-        pb = _vec("dbias", dbias, (wrows,), torch.float32, dev)
+    if dx is not None:
+        out["dx"], pdx = dx, _vec("dx", dx, x.shape, io, dev)
+    elif want_dx:
+        out["dx"] = dx = torch.empty_like(x) if sx == 0 else x.new_empty(x.shape)
+        pdx = dx.data_ptr()
+    if dW is not None:
+        out["dW"], pdW = dW, _vec("dW", dW, (wrows, K), io, dev)
+    elif want_dW:
+        out["dW"] = dW = torch.empty_like(W)
+        pdW = dW.data_ptr()
+    if dbias is not None:
+        out["dbias"], pb = dbias, _vec("dbias", dbias, (wrows,), torch.float32, dev)
+    elif want_dbias:
+        out["dbias"] = dbias = torch.empty(wrows, dtype=torch.float32, device=dev)
+        pb = dbias.data_ptr()
     dims = LinearDims(rows, K, N, sx, sdy, 0, code, act, M3_FLAG_UNALIGNED if (px | pW | pdy) & 15 else 0, 0)
     query, call = ((L.mamba3_gated_ffn_bwd_workspace_size, L.mamba3_gated_ffn_bwd) if gated else
                    (L.mamba3_linear_bwd_workspace_size, L.mamba3_linear_bwd))
