@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int64_t slab
 
 template <typename T>
 hipError_t act_bwd_run(const ActBwdArgs& a, hipStream_t s) {
-  const int64_t parts = act_bwd_parts(a.rows), per = 32 * io<T>::VEC;
+  const int64_t parts = act_bwd_parts(a.rows, a.cols), per = 32 * io<T>::VEC;
   const int64_t slab = (a.rows + parts - 1) / parts;
   const dim3 grid((unsigned)((a.cols + per - 1) / per), (unsigned)parts), blk(256);
   with_act(a.act, [&](auto act) {
@@ -129,16 +129,18 @@ hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Slabs of rows: eight rows each until there are 64; up to 64 rows one slab,
-// which needs no second kernel for its sums.
-int64_t act_bwd_parts(int64_t rows) {
-  const int64_t p = (rows + 7) / 8;
-  return rows <= 64 ? 1 : p < 64 ? p : 64;
+// Slabs of rows: eight rows each until there are 64, or as many as make 1024
+// blocks where the columns are few (26255 rows of 128: 63 -> 9 us); up to 64
+// rows one slab, which needs no second kernel for its sums.
+int64_t act_bwd_parts(int64_t rows, int64_t cols) {
+  const int64_t p = (rows + 7) / 8, across = (cols + 255) / 256;
+  const int64_t most = across >= 16 ? 64 : 1024 / across;
+  return rows <= 64 ? 1 : p < most ? p : most;
 }
 
 hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s) {
   const hipError_t e = io_bf16 ? act_bwd_run<bf16_t>(a, s) : act_bwd_run<float>(a, s);
-  const int64_t parts = act_bwd_parts(a.rows), n = a.gated ? 2 * a.cols : a.cols;
+  const int64_t parts = act_bwd_parts(a.rows, a.cols), n = a.gated ? 2 * a.cols : a.cols;
   if (e != hipSuccess || !a.dbias || parts == 1) return e;
   return launch_reduce_parts(a.part, parts, n, n, a.dbias, n, nullptr, s);
 }

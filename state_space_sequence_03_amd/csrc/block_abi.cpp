@@ -171,7 +171,7 @@ BwdWs bwd_ws(const m3_linear_dims* d, bool gated) {
   w.x = w.has_dp || w.pack_dy ? up256(d->rows * padded(n, d->io_dtype) * es) : 0;
   w.w = w.x + (w.pack_x ? up256(d->rows * padded(K, d->io_dtype) * es) : 0);
   w.cols = w.w + (w.pack_w ? up256(n * padded(K, d->io_dtype) * es) : 0);
-  w.part = w.cols + up256(4 * n * (size_t)m3::act_bwd_parts(d->rows));
+  w.part = w.cols + up256(4 * n * (size_t)m3::act_bwd_parts(d->rows, d->d_out));
   w.bytes = w.part + (w.dx.part_bytes > w.dw.part_bytes ? w.dx.part_bytes : w.dw.part_bytes);
   return w;
 }
@@ -260,7 +260,7 @@ m3_status mamba3_layer_norm_fwd(const m3_norm_dims* d, const void* x, const floa
 
 size_t mamba3_layer_norm_bwd_workspace_size(const m3_norm_dims* d) {
   if (check_norm(d) != M3_OK) return 0;
-  return sizeof(float) * 2 * (size_t)d->width * (size_t)m3::norm_bwd_parts(d->rows);
+  return sizeof(float) * 2 * (size_t)d->width * (size_t)m3::norm_bwd_parts(bf16(d->io_dtype), d->rows, d->width);
 }
 
 m3_status mamba3_layer_norm_bwd(const m3_norm_dims* d, const void* x, const float* gain, const float* mean,

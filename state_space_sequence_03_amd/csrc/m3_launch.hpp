@@ -166,10 +166,10 @@ struct NormBwdArgs {
   const void *dy, *dskip;           // dskip nullable
   void* dx;                         // nullable; row stride skip_stride
   float *dgain, *dbias;             // nullable
-  float* part;                      // with either: (norm_bwd_parts(rows), 2, width), unused for one part
+  float* part;                      // with either: (norm_bwd_parts, 2, width), unused for one part
   int64_t rows, width, x_stride, y_stride, skip_stride;
 };
-int64_t norm_bwd_parts(int64_t rows);
+int64_t norm_bwd_parts(int io_bf16, int64_t rows, int64_t width);
 hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, hipStream_t s);
 // out[c] = sum over p < np of part[p * stride + c] for c < n; the first n0 go
 // to out0, the rest to out1 (each nullable).
@@ -235,11 +235,11 @@ struct ActBwdArgs {
   const void* dy;   // row stride ldy
   void* dp;         // nullable: as pre, rows ldp apart, padded by zeros
   float* dbias;     // nullable
-  float* part;      // with dbias: (act_bwd_parts(rows), cols or 2 cols), unused for one part
+  float* part;      // with dbias: (act_bwd_parts(rows, cols), cols or 2 cols), unused for one part
   int64_t rows, cols, ldy, ldp;
   int act, gated;
 };
-int64_t act_bwd_parts(int64_t rows);
+int64_t act_bwd_parts(int64_t rows, int64_t cols);
 hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s);
 // Zeros to `bytes` bytes of dst (2-byte aligned, an even count).
 hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s);

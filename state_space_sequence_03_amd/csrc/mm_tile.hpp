@@ -607,7 +607,7 @@ __global__ __launch_bounds__(256) void mm_join_kernel(MmArgs a, MmPlan pl) {
   float z[16], u[16];
 #pragma unroll
   for (int v = 0; v < 16; ++v) z[v] = u[v] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8  // loads of several parts in flight: up to 64 parts of few tiles
   for (int s = 0; s < pl.split; ++s) {
     const f32x4* part = (const f32x4*)a.part + ((int64_t)s * cut + r) * (BM * BN / 4) + tid;
 #pragma unroll

@@ -344,7 +344,7 @@ hipError_t norm_fwd_run(const NormArgs& a, hipStream_t s) {
 template <typename T, bool SKIP>
 hipError_t norm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
   const int64_t n64 = vectors<T>(a.width, 64), n256 = vectors<T>(a.width, 256);
-  const dim3 parts((unsigned)norm_bwd_parts(a.rows)), blk(256);
+  const dim3 parts((unsigned)norm_bwd_parts(io<T>::BYTES == 2, a.rows, a.width)), blk(256);
   if (n64 == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 64, SKIP>), parts, blk, 0, s, a);
   else if (n64 == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, 64, SKIP>), parts, blk, 0, s, a);
   else if (n256 == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, 256, SKIP>), parts, blk, 0, s, a);
@@ -360,10 +360,12 @@ hipError_t norm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Blocks of the backward: up to four per CU, four rows each at least; up to 8
-// rows one block, which needs no second kernel for its sums.
-int64_t norm_bwd_parts(int64_t rows) {
-  const int64_t groups = (rows + 3) / 4;
+// Blocks of the backward: up to four per CU, each with one pass over four rows
+// (a wave each) at least, or with two rows of a block each; up to 8 rows one
+// block, which needs no second kernel for its sums.
+int64_t norm_bwd_parts(int io_bf16, int64_t rows, int64_t width) {
+  const bool wave = (io_bf16 ? vectors<bf16_t>(width, 64) : vectors<float>(width, 64)) <= 2;
+  const int64_t groups = wave ? (rows + 3) / 4 : (rows + 1) / 2;
   return rows <= 8 ? 1 : groups < 1024 ? groups : 1024;
 }
 
@@ -381,7 +383,7 @@ hipError_t launch_norm_fwd(int io_bf16, const NormArgs& a, hipStream_t s) {
 hipError_t launch_norm_bwd(int io_bf16, const NormBwdArgs& a, hipStream_t s) {
   const hipError_t e = io_bf16 ? (a.dskip ? norm_bwd_run<bf16_t, true>(a, s) : norm_bwd_run<bf16_t, false>(a, s))
                                : (a.dskip ? norm_bwd_run<float, true>(a, s) : norm_bwd_run<float, false>(a, s));
-  const int64_t parts = norm_bwd_parts(a.rows);
+  const int64_t parts = norm_bwd_parts(io_bf16, a.rows, a.width);
   if (e != hipSuccess || parts == 1 || (!a.dgain && !a.dbias)) return e;
   return launch_reduce_parts(a.part, parts, 2 * a.width, 2 * a.width, a.dgain, a.width, a.dbias, s);
 }
