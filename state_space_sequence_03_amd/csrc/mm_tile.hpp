@@ -623,14 +623,18 @@ __global__ __launch_bounds__(256) void mm_join_kernel(MmArgs a, MmPlan pl) {
     }
   }
   const int64_t m = it.m0 + (wave & 1) * (BM / 2) + j * 32 + (lane & 31);
-  tile_column<T, EPI, ACT, 1, false>(a, m, it.n0 + (wave >> 1) * (BC / 2) + i * 32, lane >> 5,
-                                     [&](int, float* zz, float* uu) {
+  auto finish = [&](auto inner) {
+    tile_column<T, EPI, ACT, 1, decltype(inner)::value>(a, m, it.n0 + (wave >> 1) * (BC / 2) + i * 32, lane >> 5,
+                                                        [&](int, float* zz, float* uu) {
 #pragma unroll
-                                       for (int v = 0; v < 16; ++v) {
-                                         zz[v] = z[v];
-                                         uu[v] = u[v];
-                                       }
-                                     });
+                                                          for (int v = 0; v < 16; ++v) {
+                                                            zz[v] = z[v];
+                                                            uu[v] = u[v];
+                                                          }
+                                                        });
+  };
+  if (it.m0 + BM <= a.M && it.n0 + BC <= a.N) finish(std::integral_constant<bool, true>{});
+  else finish(std::integral_constant<bool, false>{});
 }
 
 }  // namespace m3
