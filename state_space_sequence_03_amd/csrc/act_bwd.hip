@@ -3,11 +3,12 @@
 //   linear: dP = dy act'(pre);   gated: dP = [dy u act'(g), dy act(g)],
 // rounded once to the io type (the products that follow take their operands
 // in it), and the column sums of the unrounded dP (the bias' gradient).
-// Bound by HBM: 3 reads and 2 writes of rows x cols run at 5.0 TB/s (32768 x
-// 5632 bf16, 0.37 ms), one row per thread at a time: unrolled by 2 or 4 the
-// loop holds fewer waves and takes 0.44 and 0.41 ms.  A block owns 32 vectors
-// of columns and a slab of rows, eight rows at a time; each thread sums its columns over its rows, the eight row
-// groups are added in LDS and the slabs by launch_reduce_parts, all in a
+// Bound by HBM: 3 reads and 2 writes of rows x cols run at 5.1 TB/s (32768 x
+// 5632 bf16, 0.36 ms), one row per thread at a time: unrolled by 2 or 4 the
+// loop holds fewer waves, and a call of it and a short product takes 616 and
+// 583 us against 545.  A block owns 32 vectors of columns and a slab of rows,
+// eight rows at a time; each thread sums its columns over its rows, the eight
+// row groups are added in LDS and the slabs by launch_reduce_parts, all in a
 // fixed order.
 #include "act.hpp"
 #include "m3_launch.hpp"

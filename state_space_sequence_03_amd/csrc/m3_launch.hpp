@@ -201,7 +201,7 @@ struct MmArgs {
 // `split` parts of `stages` stages of 128 bytes, which a second kernel joins.
 struct MmPlan {
   int tile, ntm, ntn, full, split;  // tile 0 takes rows of any alignment
-  int stages, whole;  // stages of a part and of a whole tile (both even)
+  int stages, whole;  // stages of a part and of a whole tile (even for tile 256)
   int items;          // full + split parts
   size_t part_bytes;
 };

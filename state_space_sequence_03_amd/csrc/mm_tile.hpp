@@ -346,7 +346,10 @@ __device__ __forceinline__ void mix_k_step() {
 //
 // PER blocks share a CU: two where there are more items than CUs; where a
 // block is alone on its CU, nobody covers its waits, and it takes all of the
-// LDS for a pipeline twice as deep.
+// LDS for a pipeline twice as deep (dx and dW of 4096 x 1024 -> 4096, 128 x 128
+// tiles, one per CU: 61 and 51 -> 41 us each, 0.83 PFLOP/s).  The matrix cores
+// work about a third of the time there; the tiles' 537 MB of operands come in,
+// mostly from the caches, at 13 TB/s.
 // ---------------------------------------------------------------------------
 struct MmItem {
   int64_t m0, n0;  // first row and column of out
@@ -595,7 +598,8 @@ __global__ __launch_bounds__(256, 2) void mm_pair_kernel(MmArgs a, MmPlan pa, Mm
 }
 
 // Adds the parts of the split tiles in order and applies the epilogue: one
-// block per tile and 32 x 32 piece of each wave.
+// block per tile and 32 x 32 piece of each wave.  Bound by the parts' traffic: 96
+// tiles of 256 x 256 in 23 us, 312 fp32 tiles of 64 x 64 and less in 10.
 template <typename T, int EPI, int ACT, int BM, int BN>
 __global__ __launch_bounds__(256) void mm_join_kernel(MmArgs a, MmPlan pl) {
   constexpr bool G = EPI == MM_GATED;

@@ -15,6 +15,11 @@
 // of the stage after next at once: a load has six phases (3,000 cycles) to
 // land, and every phase issues four loads per wave, reads one piece and ends
 // in one barrier that waits for the loads of six phases before.
+// 32768 x 11264 -> 2048 bf16 (dx): 1.10 ms, 1.37 PFLOP/s, the matrix cores busy
+// in 80 % of the cycles at 1.64 GHz; two whole stages in LDS with all loads in
+// a stage's last quarter took 1.36 ms, 52-55 % busy.  The epilogue goes through
+// LDS so that rows leave in 128 bytes: 32768 x 2048 -> 2 x 5632 with stored
+// pre-activations 1.31 -> 1.23 ms.
 #pragma once
 
 #include "mm_tile.hpp"

@@ -7,12 +7,15 @@
 // Both are bound by HBM: every row is read once into registers, the row sums
 // are taken there (the variance about the mean, not as a difference of
 // moments), and the result is written once.  A row belongs to one wave (TPR =
-// 64) or one block (TPR = 256); NV is the number of 16-byte vectors a thread
-// holds of each operand.  Rows too wide for that are re-read from the caches
-// (the *_wide kernels).  The backward walks many rows per block and keeps the
-// column sums of its rows in registers; one partial row per block and a
-// second kernel that adds the partial rows in order give dgain and dbias
-// (no atomics: the result does not depend on timing).
+// 64) or one block (TPR = 256, 1024); NV is the number of 16-byte vectors a
+// thread holds of each operand.  32768 x 2048 bf16: forward with statistics
+// 45 us from a warm cache, 59 (4.6 TB/s) cold; backward with dskip 108 us (5.0
+// TB/s) and 5 for the column sums, a block per row: a wave per row spilled (227).
+// Rows too wide for that are re-read from the caches (the *_wide kernels).  The
+// backward walks many rows per block and keeps the column sums of its rows in
+// registers; one partial row per block and a second kernel that adds the partial
+// rows in order give dgain and dbias (no atomics: the result does not depend on
+// timing).
 #include "m3_lanes.hpp"
 #include "m3_launch.hpp"
 #include "m3_rows.hpp"
