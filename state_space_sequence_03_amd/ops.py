@@ -433,9 +433,26 @@ def _vec(name, t, shape, dtype, device):
     raise ValueError(f"{name}: must be contiguous")
 
 
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
+def _on_stream(stream, x, call, *args, **kw):
+    """The call made under torch.cuda.stream(stream): what it allocates belongs
+    to that stream, so that the allocator neither hands a workspace dropped at
+    return to another stream's work while the kernels still use it, nor takes
+    for it memory that such work still writes.  Outputs are recorded for the
+    caller's stream too, which reads them next."""
+    torch = _torch()
+    if stream.device != x.device:
+        raise ValueError(f"stream: on {stream.device}, expected {x.device}")
+    here = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in out.values() if isinstance(out, dict) else out:
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
+def _raw_stream(device):
+    """Handle of the device's current stream."""
     torch = _torch()
     current = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
     if current is None or device.index is None:
@@ -455,6 +472,9 @@ def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=Non
                           stream=None):
     """Layer norm of the rows of x (..., D).  Returns (y, mean, rstd); the
     statistics ((rows) fp32, for the backward) are None unless wanted or given."""
+    if stream is not None:
+        return _on_stream(stream, x, mamba3_layer_norm_fwd, x, gain, bias, eps, y=y, mean=mean, rstd=rstd,
+                          want_stats=want_stats)
     torch = _torch()
     rows, D, code = _rows_of(x)
     io, dev, f32 = x.dtype, x.device, torch.float32
@@ -470,7 +490,7 @@ def mamba3_layer_norm_fwd(x, gain=None, bias=None, eps=1e-5, *, y=None, mean=Non
     st = lib().mamba3_layer_norm_fwd(NormDims(rows, D, sx, sy, 0, code, 0), px, _vec("gain", gain, (D,), f32, dev),
                                      _vec("bias", bias, (D,), f32, dev), eps, py,
                                      _vec("mean", mean, (rows,), f32, dev), _vec("rstd", rstd, (rows,), f32, dev),
-                                     _raw_stream(stream, dev))
+                                     _raw_stream(dev))
     _check(st, "mamba3_layer_norm_fwd")
     return y, mean, rstd
 
@@ -484,6 +504,10 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
     """Backward of layer_norm_fwd.  dskip: a gradient that reaches x past the
     norm, added to dx.  Returns a dict with dx (io dtype), dgain and dbias (fp32),
     as wanted.  dskip and dx have the same row stride."""
+    if stream is not None:
+        return _on_stream(stream, x, mamba3_layer_norm_bwd, x, mean, rstd, dy, gain, dskip, want_dx=want_dx,
+                          want_dgain=want_dgain, want_dbias=want_dbias, dx=dx, dgain=dgain, dbias=dbias,
+                          workspace=workspace)
     torch = _torch()
     rows, D, code = _rows_of(x)
     io, dev, f32 = x.dtype, x.device, torch.float32
@@ -522,7 +546,7 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
         workspace, pws, nws = _workspace(L.mamba3_layer_norm_bwd_workspace_size, dims, workspace, dev)
     st = L.mamba3_layer_norm_bwd(dims, px, _vec("gain", gain, (D,), f32, dev), _vec("mean", mean, (rows,), f32, dev),
                                  _vec("rstd", rstd, (rows,), f32, dev), pdy, psk, pdx, pg, pb, pws, nws,
-                                 _raw_stream(stream, dev))
+                                 _raw_stream(dev))
     _check(st, "mamba3_layer_norm_bwd")
     return out
 
@@ -567,6 +591,9 @@ def _weight_rows(W, gated):
 
 
 def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, workspace, stream):
+    if stream is not None:
+        return _on_stream(stream, x, _product_fwd, name, gated, x, W, bias, residual, act, y, pre, want_pre,
+                          workspace, None)
     torch = _torch()
     rows, K, code = _rows_of(x)
     wrows, N = _weight_rows(W, gated)
@@ -587,7 +614,7 @@ def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, works
     pW = _vec("W", W, (wrows, K), io, dev)
     pb = _vec("bias", bias, (wrows,), torch.float32, dev)
     dims = LinearDims(rows, K, N, sx, sy, sr, code, act, M3_FLAG_UNALIGNED if (px | pW) & 15 else 0, 0)
-    s = _raw_stream(stream, dev)
+    s = _raw_stream(dev)
     if gated:
         workspace, pws, nws = _workspace(L.mamba3_gated_ffn_fwd_workspace_size, dims, workspace, dev)
         st = L.mamba3_gated_ffn_fwd(dims, px, pW, pb, py, ppre, pws, nws, s)
@@ -599,6 +626,9 @@ def _product_fwd(name, gated, x, W, bias, residual, act, y, pre, want_pre, works
 
 
 def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, dx, dW, dbias, workspace, stream):
+    if stream is not None:
+        return _on_stream(stream, x, _product_bwd, name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias,
+                          dx, dW, dbias, workspace, None)
     torch = _torch()
     rows, K, code = _rows_of(x)
     wrows, N = _weight_rows(W, gated)
@@ -634,7 +664,7 @@ def _product_bwd(name, gated, x, W, dy, pre, act, want_dx, want_dW, want_dbias, 
     query, call = ((L.mamba3_gated_ffn_bwd_workspace_size, L.mamba3_gated_ffn_bwd) if gated else
                    (L.mamba3_linear_bwd_workspace_size, L.mamba3_linear_bwd))
     workspace, pws, nws = _workspace(query, dims, workspace, dev)
-    st = call(dims, px, pW, ppre, pdy, pdx, pdW, pb, pws, nws, _raw_stream(stream, dev))
+    st = call(dims, px, pW, ppre, pdy, pdx, pdW, pb, pws, nws, _raw_stream(dev))
     _check(st, name)
     return out
 
