@@ -177,6 +177,24 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(stream, x, call, *args, **kw):
+    """The call made under torch.cuda.stream(stream): what it allocates belongs
+    to that stream, so that the allocator neither hands a workspace dropped at
+    return to another stream's work while the kernels still use it, nor takes
+    for it memory that such work still writes.  Outputs are recorded for the
+    caller's stream too, which reads them next."""
+    torch = _torch()
+    if stream.device != x.device:
+        raise ValueError(f"stream: on {stream.device}, expected {x.device}")
+    here = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def _check(status: int, what: str):
     if status != M3_OK:
         raise Mamba3Error(status, what)
@@ -215,6 +233,10 @@ def mamba3_ssm_chunked_fwd(x, B, C, dt, A, lam, theta, h0=None, prev_B=None, pre
     """Whole-sequence forward.  Returns (y, h_final) (h_final None if not wanted).
     chunk_walk / token_path force one of the two paths for short calls (the
     library picks one by default)."""
+    if stream is not None:
+        return _on_stream(stream, x, mamba3_ssm_chunked_fwd, x, B, C, dt, A, lam, theta, h0, prev_B, prev_x,
+                          chunk=chunk, segments=segments, chunk_walk=chunk_walk, token_path=token_path, y=y,
+                          h_final=h_final, want_final=want_final, workspace=workspace)
     torch = _torch()
     b, L, H, R, P = x.shape
     N = B.shape[-1]
@@ -272,6 +294,9 @@ def mamba3_ssm_chunked_bwd(x, B, C, dt, A, lam, theta, dy, h0=None, prev_B=None,
     dprev_B and dprev_x (io dtype).  segments: 0 = the library's choice, else
     the number of sequence segments walked in parallel (flags' low 16 bits).
     out: optional dict of preallocated outputs (any of the keys above)."""
+    if stream is not None:
+        return _on_stream(stream, x, mamba3_ssm_chunked_bwd, x, B, C, dt, A, lam, theta, dy, h0, prev_B, prev_x,
+                          dh_final, chunk=chunk, segments=segments, want_dh0=want_dh0, workspace=workspace, out=out)
     torch = _torch()
     b, L, H, R, P = x.shape
     N = B.shape[-1]
@@ -310,6 +335,8 @@ def mamba3_ssm_chunked_bwd(x, B, C, dt, A, lam, theta, dy, h0=None, prev_B=None,
 def mamba3_ssm_decode_step(state, x, B, C, dt, A, lam, theta, prev_B=None, prev_x=None, *, y=None, stream=None):
     """One token, state updated in place.  Shapes: state (b,H,N,P) fp32, x (b,H,R,P),
     B/C (b,H,R,N), dt/A/lam (b,H), theta (b,H,N/2).  Returns y (b,H,R,P)."""
+    if stream is not None:
+        return _on_stream(stream, x, mamba3_ssm_decode_step, state, x, B, C, dt, A, lam, theta, prev_B, prev_x, y=y)
     torch = _torch()
     b, H, R, P = x.shape
     N = B.shape[-1]
@@ -335,6 +362,9 @@ def mamba3_ssm_decode_step(state, x, B, C, dt, A, lam, theta, prev_B=None, prev_
 def mamba3_rope_bc(B, C, dt, theta, angle0=None, *, B_rot=None, C_rot=None, angle_final=None,
                    want_final=True, workspace=None, stream=None):
     """Cumulative-angle rotation.  Returns (B_rot, C_rot, angle_final)."""
+    if stream is not None:
+        return _on_stream(stream, B, mamba3_rope_bc, B, C, dt, theta, angle0, B_rot=B_rot, C_rot=C_rot,
+                          angle_final=angle_final, want_final=want_final, workspace=workspace)
     torch = _torch()
     b, L, H, R, N = B.shape
     io, f32, dev = B.dtype, torch.float32, B.device
@@ -371,6 +401,10 @@ def mamba3_bc_prologue(u, W, dt, theta, nheads, rank, dstate, gain=None, bias=No
     """Projection of u (B, L, D) by W (2*H*R*N, D) to B and C, RMS-normalised
     per (token, head, rank) vector with gain and bias, and rotated by the
     cumulative angle.  Returns (B_rot, C_rot, angle_final)."""
+    if stream is not None:
+        return _on_stream(stream, u, mamba3_bc_prologue, u, W, dt, theta, nheads, rank, dstate, gain, bias, eps, angle0,
+                          B_rot=B_rot, C_rot=C_rot, angle_final=angle_final, want_final=want_final,
+                          workspace=workspace)
     torch = _torch()
     b, L, D = u.shape
     H, R, N = nheads, rank, dstate
@@ -431,24 +465,6 @@ def _vec(name, t, shape, dtype, device):
         return t.data_ptr()
     _expect(name, t, shape, dtype, device)
     raise ValueError(f"{name}: must be contiguous")
-
-
-def _on_stream(stream, x, call, *args, **kw):
-    """The call made under torch.cuda.stream(stream): what it allocates belongs
-    to that stream, so that the allocator neither hands a workspace dropped at
-    return to another stream's work while the kernels still use it, nor takes
-    for it memory that such work still writes.  Outputs are recorded for the
-    caller's stream too, which reads them next."""
-    torch = _torch()
-    if stream.device != x.device:
-        raise ValueError(f"stream: on {stream.device}, expected {x.device}")
-    here = torch.cuda.current_stream(x.device)
-    with torch.cuda.stream(stream):
-        out = call(*args, **kw)
-    for t in out.values() if isinstance(out, dict) else out:
-        if t is not None:
-            t.record_stream(here)
-    return out
 
 
 def _raw_stream(device):

@@ -1,5 +1,5 @@
-"""The residual block's binding on the host: where its allocations go, what it
-refuses, the shapes it returns.  No GPU and no launch: the library is a
+"""The binding on the host: where its allocations go, what the residual block's
+calls refuse and the shapes they return.  No GPU and no launch: the library is a
 stand-in that takes every call, and operands lie in host memory.
 """
 import contextlib
@@ -66,11 +66,26 @@ def block_calls():
 BLOCK = [name for name, _, _ in block_calls()]
 
 
-@pytest.mark.parametrize("which", range(len(BLOCK)), ids=BLOCK)
-def test_allocations_belong_to_the_given_stream(fake, which):
+def core_calls():
+    """The same for the layer core's entry points that allocate."""
+    b, L, H, R, P, N = 1, 3, 2, 1, 16, 16
+    x, B, s, th = torch.ones(b, L, H, R, P), torch.ones(b, L, H, R, N), torch.ones(b, L, H), torch.ones(b, L, H, N // 2)
+    h, token = torch.ones(b, H, N, P), [t[:, 0].contiguous() for t in (x, B, B, s, s, s, th)]
+    u, W = torch.ones(b, L, 8), torch.ones(2 * H * R * N, 8)
+    yield "ssm_chunked_fwd", lambda **k: ops.chunked_fwd(x, B, B, s, s, s, th, **k), 2, 1
+    yield "ssm_chunked_bwd", lambda **k: ops.chunked_bwd(x, B, B, s, s, s, th, x, **k), 8, 1
+    yield "ssm_decode_step", lambda **k: ops.decode_step(h, *token, **k), 1, 0
+    yield "rope_bc", lambda **k: ops.rope_bc(B, B, s, th, **k), 3, 1
+    yield "bc_prologue", lambda **k: ops.bc_prologue(u, W, s, th, H, R, N, **k), 3, 1
+
+
+ALL = [c if len(c) == 4 else c + (0 if c[0] == "layer_norm_fwd" else 1,) for c in (*block_calls(), *core_calls())]
+
+
+@pytest.mark.parametrize("name,call,outputs,workspace", ALL, ids=[c[0] for c in ALL])
+def test_allocations_belong_to_the_given_stream(fake, name, call, outputs, workspace):
     # a workspace that the call drops at return must not go back to another
     # stream's pool while the kernels on the given stream still use it
-    name, call, outputs = list(block_calls())[which]
     seen = []
 
     class Allocations(TorchDispatchMode):
@@ -82,24 +97,25 @@ def test_allocations_belong_to_the_given_stream(fake, which):
     side = Stream()
     with Allocations():
         out = call(stream=side)
-    workspace = 0 if name == "layer_norm_fwd" else 1
     assert len(seen) == outputs + workspace and all(s is side for s in seen)
     assert [c[0] for c in fake.calls] == ["mamba3_" + name]
-    assert fake.calls[0][1][-1] == side.cuda_stream  # ... and the kernels go there
+    handle = fake.calls[0][1][-1]  # ... and the kernels go there
+    assert getattr(handle, "value", handle) == side.cuda_stream
     # the outputs are read on the caller's stream next
-    mine = [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
+    out = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
+    mine = [t for t in out if t is not None]
     assert len(mine) == outputs and len(fake.recorded) == outputs
     assert all(a is b for a, b in zip(mine, fake.recorded))
     assert fake.inside is None
 
 
-@pytest.mark.parametrize("which", range(len(BLOCK)), ids=BLOCK)
-def test_a_stream_of_another_device_is_refused(fake, which):
+@pytest.mark.parametrize("call", [c[1] for c in ALL], ids=[c[0] for c in ALL])
+def test_a_stream_of_another_device_is_refused(fake, call):
     class Other(Stream):
         device = torch.device("meta")
 
     with pytest.raises(ValueError, match="stream"):
-        list(block_calls())[which][1](stream=Other())
+        call(stream=Other())
     assert not fake.calls
 
 
