@@ -591,6 +591,10 @@ def _workspace(query, dims, workspace, device):
             return None, None, 0
         workspace = _torch().empty(need, device=device, dtype=_torch().uint8)
         return workspace, workspace.data_ptr(), need
+    if workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous():  # its bytes are counted from its entries
+        raise ValueError("workspace: must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

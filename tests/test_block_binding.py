@@ -124,3 +124,18 @@ def test_without_a_stream_the_current_one_is_used(fake, which):
     name, call, _ = list(block_calls())[which]
     call()
     assert fake.calls[0][0] == "mamba3_" + name and fake.calls[0][1][-1] == 0 and not fake.recorded
+
+
+@pytest.mark.parametrize("which", range(1, len(BLOCK)), ids=BLOCK[1:])
+def test_workspaces_that_are_refused(fake, which):
+    # entries on top of each other (4096 counted, one there), every second byte, another device
+    call = list(block_calls())[which][1]
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(8192, dtype=torch.uint8)[::2],
+                torch.empty(4096, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=bad)
+    assert not fake.calls
+    # of any type, its size in bytes
+    call(workspace=torch.zeros(1024))
+    args = [getattr(a, "value", a) for a in fake.calls[0][1]]
+    assert args[-2] == 4096
