@@ -519,7 +519,8 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
                           want_dbias=True, dx=None, dgain=None, dbias=None, workspace=None, stream=None):
     """Backward of layer_norm_fwd.  dskip: a gradient that reaches x past the
     norm, added to dx.  Returns a dict with dx (io dtype), dgain and dbias (fp32),
-    as wanted.  dskip and dx have the same row stride."""
+    as wanted.  dskip and dx have the same row stride: a dx made here has x's
+    shape, and dskip's row stride where dskip is a column slice."""
     if stream is not None:
         return _on_stream(stream, x, mamba3_layer_norm_bwd, x, mean, rstd, dy, gain, dskip, want_dx=want_dx,
                           want_dgain=want_dgain, want_dbias=want_dbias, dx=dx, dgain=dgain, dbias=dbias,
@@ -536,7 +537,7 @@ def mamba3_layer_norm_bwd(x, mean, rstd, dy, gain=None, dskip=None, *, want_dx=T
     if want_dx or dx is not None:
         if dx is None:
             if ssk:
-                dx = torch.empty_strided((rows, D), (ssk, 1), dtype=io, device=dev)
+                dx = torch.empty_strided((rows, D), (ssk, 1), dtype=io, device=dev).view(x.shape)
             else:
                 dx = torch.empty_like(x) if sx == 0 else x.new_empty(x.shape)
             pdx = dx.data_ptr()

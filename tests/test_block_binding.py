@@ -139,3 +139,16 @@ def test_workspaces_that_are_refused(fake, which):
     call(workspace=torch.zeros(1024))
     args = [getattr(a, "value", a) for a in fake.calls[0][1]]
     assert args[-2] == 4096
+
+
+@pytest.mark.parametrize("shape", [(4, 16), (2, 2, 16), (4, 1, 16), (2, 1, 2, 16)])
+def test_layer_norm_dx_has_the_shape_of_x(fake, shape):
+    x, m = torch.ones(shape), torch.ones(4)
+    wide = torch.zeros(4, 24)
+    for skip, stride in ((None, 16), (x, 16), (x.view(4, 16), 16), (wide[:, 3:19], 24)):
+        dx = ops.layer_norm_bwd(x, m, m, x, dskip=skip)["dx"]
+        assert dx.shape == x.shape and dx.dtype == x.dtype
+        # its rows lie where the kernel, which knows one stride, puts them
+        assert dx.view(4, 16).stride() == (stride, 1)
+        assert (fake.calls[-1][1][0].skip_stride or 16) == stride
+        assert fake.calls[-1][1][7] == dx.data_ptr()
