@@ -189,7 +189,8 @@ m3_status linear_bwd(const m3_linear_dims* d, bool gated, const void* x, const v
   if (d->rows > 0 && ((dx && !base_ok(W, w.pack_w)) || (dW && !base_ok(x, w.pack_x)) ||
                       ((dx || dW) && !has_dp && !base_ok(dy, w.pack_dy))))
     return M3_ERR_ALIGN;
-  if (any && w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return M3_ERR_WORKSPACE;
+  if (!any) return M3_OK;
+  if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return M3_ERR_WORKSPACE;
   const hipStream_t s = (hipStream_t)stream;
   const int64_t n = gated ? 2 * d->d_out : d->d_out;
   const int io = bf16(d->io_dtype);
