@@ -89,3 +89,14 @@ hipError_t launch_mm_pair(int io_bf16, const MmArgs& dx, const MmPlan& px, const
 }
 
 }  // namespace m3
+
+// How a product is cut, for the tests that mean to run a certain form: tile,
+// tiles in all, whole ones of them, parts of each of the others (1: none).
+// epilogue: an MmEpilogue.
+extern "C" void m3_product_plan(int io_bf16, int epilogue, int64_t M, int64_t N, int64_t K, int64_t* out) {
+  const m3::MmPlan p = m3::mm_plan(io_bf16, (m3::MmEpilogue)epilogue, M, N, K);
+  out[0] = p.tile;
+  out[1] = (int64_t)p.ntm * p.ntn;
+  out[2] = p.full;
+  out[3] = p.split;
+}

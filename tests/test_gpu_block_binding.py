@@ -1,5 +1,6 @@
-"""The residual block's operators with stream=: what a call allocates stays its
-own until its kernels are done.  Needs an MI355X."""
+"""What the residual block's calls allocate themselves: with stream= it stays
+theirs until their kernels are done; an output has its operand's shape.  Needs
+an MI355X."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -51,3 +52,16 @@ def test_workspaces_outlive_their_call(ops, dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
         del fill
+
+
+def test_norm_of_three_dimensions_with_a_strided_skip(ops):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g)
+    x, dy, wide = rand(3, 5, 64), rand(3, 5, 64), rand(15, 100)
+    skip = wide[:, 7:71]
+    _, mean, rstd = ops.layer_norm_fwd(x, want_stats=True)
+    want = ops.layer_norm_bwd(x, mean, rstd, dy, dskip=skip.contiguous())
+    got = ops.layer_norm_bwd(x, mean, rstd, dy, dskip=skip)
+    assert got["dx"].shape == x.shape and torch.equal(got["dx"], want["dx"])
+    assert torch.equal(got["dgain"], want["dgain"])
