@@ -80,8 +80,10 @@ __device__ __forceinline__ void act_both(float z, float& f, float& df) {
     df = p + c * p * (1.0f - p) * 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
     df = z == z ? df : z;
   } else if constexpr (ACT == ACT_SIGMOID) {
-    f = sigmoid<FINE>(z);
-    df = f * (1.0f - f);
+    // from exp(-|z|), so that neither tail is a difference of near-equal terms
+    const float e = exp_neg<FINE>(fabsf(z)), r = recip<FINE>(1.0f + e);
+    f = z < 0.0f ? e * r : r;
+    df = e * r * r;
   } else {
     f = z;
     df = 1.0f;
