@@ -365,11 +365,15 @@ hipError_t norm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
 
 // Blocks of the backward: up to four per CU, each with one pass over four rows
 // (a wave each) at least, or with two rows of a block each; up to 8 rows one
-// block, which needs no second kernel for its sums.
+// block, which needs no second kernel for its sums.  Where rows are re-read, a
+// slab of rows is a row of blocks already, and as many slabs are taken as make
+// 1024 blocks: their partial rows are 16 MB at most, whatever the width.
 int64_t norm_bwd_parts(int io_bf16, int64_t rows, int64_t width) {
   const bool wave = (io_bf16 ? vectors<bf16_t>(width, 64) : vectors<float>(width, 64)) <= 2;
+  const int64_t n256 = io_bf16 ? vectors<bf16_t>(width, 256) : vectors<float>(width, 256);
   const int64_t groups = wave ? (rows + 3) / 4 : (rows + 1) / 2;
-  return rows <= 8 ? 1 : groups < 1024 ? groups : 1024;
+  const int64_t most = n256 <= 4 ? 1024 : n256 < 1024 ? 1024 / n256 : 1;
+  return rows <= 8 ? 1 : groups < most ? groups : most;
 }
 
 hipError_t launch_reduce_parts(const float* part, int64_t np, int64_t stride, int64_t n, float* out0, int64_t n0,

@@ -35,3 +35,16 @@ def test_largest_sizes(L):
                 for fn in ("linear", "gated_ffn"):
                     assert getattr(L, fn + "_fwd_workspace_size")(d) >= copies
                     getattr(L, fn + "_bwd_workspace_size")(d)
+
+
+@pytest.mark.parametrize("io", ["M3_BF16", "M3_F32"])
+def test_norm_workspace_is_bounded(L, io):
+    # partial column sums: 1024 rows of the widest row that a block holds, and 16
+    # MB where rows are wider than that
+    held = 8192 if io == "M3_BF16" else 4096
+    for rows in (1, 9, 300, 2048, 100_000, (1 << 24) - 1):
+        for width in (1, 64, 1021, 2048, held, held + 1, 9001, 20000, 65536, 1 << 20):
+            need = L.layer_norm_bwd_workspace_size(norm(L, rows=rows, width=width, io_dtype=getattr(L, io)))
+            assert need > 0 and need % (8 * width) == 0
+            assert rows > 8 or need == 8 * width
+            assert need <= (1024 * 8 * held if width <= held else 1 << 24)
