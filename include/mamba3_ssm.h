@@ -419,7 +419,8 @@ size_t mamba3_linear_fwd_workspace_size(const m3_linear_dims* d);
  * pre: required unless act is M3_ACT_NONE (then ignored).  dx (M, K), dW
  * (N, K), dbias (N): nullable, each by itself; x is needed for dW, W for dx.
  * workspace: at least mamba3_linear_bwd_workspace_size(d) bytes (dP, copies,
- * partial sums), whichever gradients are asked for. */
+ * partial sums), whichever gradients are asked for; a call that asks for none
+ * returns after its checks and needs none. */
 m3_status mamba3_linear_bwd(const m3_linear_dims* d, const void* x, const void* W, const void* pre, const void* dy,
                             void* dx, void* dW, float* dbias, void* workspace, size_t workspace_bytes,
                             void* stream);

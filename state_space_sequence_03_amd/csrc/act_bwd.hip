@@ -1,10 +1,13 @@
 // The elementwise part of the backward of the linear and gated feed-forward
 // operators, in one pass over dy and the stored pre-activations:
 //   linear: dP = dy act'(pre);   gated: dP = [dy u act'(g), dy act(g)],
-// rounded once to the io type (the products that follow take their operands
-// in it), and the column sums of the unrounded dP (the bias' gradient).
-// Bound by HBM: 3 reads and 2 writes of rows x cols run at 5.1 TB/s (32768 x
-// 5632 bf16, 0.36 ms), one row per thread at a time: unrolled by 2 or 4 the
+// rounded once to the io type, and the column sums of the unrounded dP (the
+// bias' gradient).  The products that follow take their operands in the io
+// type, and the bf16 matrix cores nothing wider: for bf16 io that rounding and
+// the output's, 1.7e-3 relative each, leave dx and dW 2.3e-3 off; dP as a sum
+// of two bf16 operands would double the products' time.  fp32 io keeps it whole.
+// Bound by HBM: 3 reads and 2 writes of rows x cols run at 5.1-5.5 TB/s (32768 x
+// 5632 bf16, 0.34-0.36 ms), one row per thread at a time: unrolled by 2 or 4 the
 // loop holds fewer waves, and a call of it and a short product takes 616 and
 // 583 us against 545.  A block owns 32 vectors of columns and a slab of rows,
 // eight rows at a time; each thread sums its columns over its rows, the eight
@@ -131,8 +134,9 @@ hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s) {
 }
 
 // Slabs of rows: eight rows each until there are 64, or as many as make 1024
-// blocks where the columns are few (26255 rows of 128: 63 -> 9 us); up to 64
-// rows one slab, which needs no second kernel for its sums.
+// blocks where the columns are few (32768 rows bf16, with the sums of the
+// slabs: of 128 columns 40 us with 64 slabs, 15 so; of 1024 columns 62 and 24);
+// up to 64 rows one slab, which needs no second kernel for its sums.
 int64_t act_bwd_parts(int64_t rows, int64_t cols) {
   const int64_t p = (rows + 7) / 8, across = (cols + 255) / 256;
   const int64_t most = across >= 16 ? 64 : 1024 / across;
