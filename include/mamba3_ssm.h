@@ -1,8 +1,9 @@
 /*
  * mamba3_ssm.h -- C ABI of the MI355X (gfx950) Mamba-3 SSM layer core.
  *
- * Five operations of the layer core and three of the residual block around
- * it, all asynchronous on a caller-given HIP stream:
+ * Five operations of the layer core, three of the residual block around it
+ * and three of an attention layer beside it, all asynchronous on a caller-given
+ * HIP stream:
  *
  *   mamba3_ssm_chunked_fwd   whole-sequence forward (prefill / training
  *                            forward) by the chunked parallel form;
@@ -17,7 +18,12 @@
  *   mamba3_gated_ffn_*       both projections of a gated feed-forward, its
  *                            activation and product (each of the three with
  *                            its backward; their own conventions stand with
- *                            them, at the end of this file).
+ *                            them, below the core's);
+ *   mamba3_qk_norm_rope_*    norms of queries and keys for each head and their
+ *                            rotation by position;
+ *   mamba3_window_attn_*     causal attention over a sliding window with first
+ *                            tokens that stay visible, its backward, and the
+ *                            same for new tokens over a cache (at the end).
  *
  * What the core computes (pages cited by title and section):
  *
@@ -441,6 +447,150 @@ m3_status mamba3_gated_ffn_bwd(const m3_linear_dims* d, const void* x, const voi
                                const void* dh, void* dx, void* dW, float* dbias, void* workspace,
                                size_t workspace_bytes, void* stream);
 size_t mamba3_gated_ffn_bwd_workspace_size(const m3_linear_dims* d);
+
+/* ---------------------------------------------------------------------------
+ * An attention layer beside the core: norms of queries and keys with their
+ * rotation, windowed attention with sinks, and that over a cache.
+ *
+ * A row is one token: its heads side by side, head_dim entries each (queries
+ * q_heads of them, keys and values kv_heads).  The stride fields count elements
+ * from token to token, so that queries, keys and values may be slices of one
+ * projection's rows; 0 stands for contiguous rows, and a stride below a row's
+ * width is M3_ERR_SHAPE.  io operands are fp32 or bf16, all of one call the
+ * same type.  Sums, softmax statistics and angles' reductions are held in fp32
+ * (angles in fp64) and outputs rounded once (nearest even); for bf16 io the
+ * softmax weights p and the scores' gradients ds are rounded to bf16 as
+ * operands of the products that take them, one rounding each as the outputs'.
+ *
+ * Limits (M3_ERR_UNSUPPORTED beyond them): strides and rows' widths at most
+ * 2^20, tokens of a call at most 2^24 - 1.  Outputs must not alias inputs
+ * unless stated.  Results do not depend on the launch's timing. */
+#define M3_FLAG_ROPE_HALVES 0x80000  /* qk_norm_rope: pairs (j, j + rope_dim/2) rather than (2j, 2j + 1) */
+#define M3_FLAG_PACKED 0x100000      /* window_attn: sequences of any lengths, given by starts */
+
+typedef struct {
+  int64_t rows;          /* tokens */
+  int64_t seqlen;        /* without pos, row r stands at position r mod seqlen (0: r) */
+  int64_t q_heads, k_heads;  /* either may be 0: its pointers are ignored */
+  int64_t head_dim;      /* D, 1 to 256 */
+  int64_t rope_dim;      /* the first entries, which are rotated: even, 0 to D */
+  int64_t q_stride, k_stride;          /* of q and k */
+  int64_t q_out_stride, k_out_stride;  /* of q_out and k_out (forward), of their gradients (backward) */
+  int64_t dq_stride, dk_stride;        /* of dq and dk (backward) */
+  int32_t io_dtype;
+  int32_t flags;         /* 0 or M3_FLAG_ROPE_HALVES */
+} m3_norm_rope_dims;
+
+/* For every head x of q and k: z = x / sqrt(mean x^2 + eps) gain, then every
+ * pair (a, b) of z's first rope_dim entries turned by the angle w = pos
+ * theta[pair]: (a cos w - b sin w, a sin w + b cos w).
+ * gain_q, gain_k: nullable (D) (NULL: 1).  eps: >= 0 and finite.
+ * theta: (rope_dim/2) fp32 angle rates, required unless rope_dim is 0.
+ * pos: nullable (rows) positions, any sign.  Angles are taken in fp64.
+ * q_out and k_out may be q and k themselves (same strides).
+ * Alignment: an element's size (pos 8). */
+m3_status mamba3_qk_norm_rope_fwd(const m3_norm_rope_dims* d, const void* q, const void* k, const float* gain_q,
+                                  const float* gain_k, float eps, const float* theta, const int64_t* pos,
+                                  void* q_out, void* k_out, void* stream);
+
+/* Its backward from q, k and the gradients dq_out, dk_out of the results: with
+ * r = 1 / sqrt(mean x^2 + eps), xh = x r, dz the incoming gradient turned back
+ * and a = dz gain,
+ *   dx = r (a - xh mean(a xh)),  dgain = sum over tokens and heads of dz xh.
+ * dq, dk: written (may be dq_out, dk_out themselves with the same strides).
+ * dgain_q, dgain_k: nullable (D) fp32, each by itself; zeros where its heads
+ * or the rows are 0.
+ * workspace: at least mamba3_qk_norm_rope_bwd_workspace_size(d) bytes (partial
+ * sums), needed when dgain_q or dgain_k is given. */
+m3_status mamba3_qk_norm_rope_bwd(const m3_norm_rope_dims* d, const void* q, const void* k, const void* dq_out,
+                                  const void* dk_out, const float* gain_q, const float* gain_k, float eps,
+                                  const float* theta, const int64_t* pos, void* dq, void* dk, float* dgain_q,
+                                  float* dgain_k, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba3_qk_norm_rope_bwd_workspace_size(const m3_norm_rope_dims* d);
+
+typedef struct {
+  int64_t batch;           /* sequences */
+  int64_t q_len, kv_len;   /* of each sequence; ignored when packed */
+  int64_t rows;            /* packed: tokens in all; else ignored */
+  int64_t kv_rows;         /* rows of k and v from sequence to sequence (0: kv_len; at least that), e.g. a
+                              cache's capacity; ignored when packed */
+  int64_t q_heads, kv_heads;  /* kv_heads divides q_heads: head i of q uses head i / (q_heads / kv_heads) */
+  int64_t head_dim;        /* D: a multiple of 8, 8 to 128 */
+  int64_t window;          /* 0: none */
+  int64_t sinks;           /* first tokens that stay visible behind the window */
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  int64_t do_stride, dq_stride, dk_stride, dv_stride;  /* backward */
+  float scale;             /* of the scores: > 0 and finite */
+  int32_t io_dtype;
+  int32_t flags;           /* 0 or M3_FLAG_PACKED */
+  int32_t reserved;        /* must be 0 */
+} m3_attn_dims;
+
+/* Query i of a sequence stands at position p = kv_len - q_len + i and sees key
+ * j (at position j) if j <= p and, with a window, p - j < window or j < sinks:
+ *   s_j = scale q k_j over what is seen,  lse = log sum exp s,
+ *   o = sum_j exp(s_j - lse) v_j.
+ * A query that sees nothing (p < 0) gets o = 0 and lse = -inf.  What a query
+ * does not see may hold anything finite; rows of other sequences, and rows of
+ * k and v past kv_len, anything at all.
+ * Without M3_FLAG_PACKED: q and o are (batch, q_len) rows, k and v (batch,
+ * kv_rows) rows of which the first kv_len are keys; starts is ignored.  With it:
+ * q, k, v and o have `rows` rows, sequence b those from starts[b] to
+ * starts[b + 1] - 1 (batch + 1 entries, rising, on the device; queries and keys
+ * have the same); rows of no sequence are neither read nor written.
+ * lse: nullable (tokens, q_heads) fp32, written when given (the backward takes
+ * it).
+ * Alignment: io pointers, and rows (strides), 16 bytes; starts 8.  batch times
+ * q_heads times 128-query tiles is at most 2^24 - 1. */
+m3_status mamba3_window_attn_fwd(const m3_attn_dims* d, const void* q, const void* k, const void* v,
+                                 const int64_t* starts, void* o, float* lse, void* stream);
+
+/* Its backward: with p = exp(s - lse), dp = do v^T and delta = sum over D of
+ * do o (o and lse as the forward gave them),
+ *   ds = p (dp - delta),  dq = scale ds k,  dk = scale ds^T q,  dv = p^T do,
+ * dk and dv summed over the query heads that share a head.  dq, dk, dv:
+ * nullable, each by itself.  Keys that no query sees get zeros.
+ * workspace: at least mamba3_window_attn_bwd_workspace_size(d) bytes (per query
+ * and head two fp32 statistics, and partial sums of the sinks' keys, which
+ * whole sequences see: those are summed in pieces side by side).  16-byte
+ * aligned, as every io pointer. */
+m3_status mamba3_window_attn_bwd(const m3_attn_dims* d, const void* q, const void* k, const void* v, const void* o,
+                                 const float* lse, const void* dout, const int64_t* starts, void* dq, void* dk,
+                                 void* dv, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba3_window_attn_bwd_workspace_size(const m3_attn_dims* d);
+
+typedef struct {
+  int64_t batch;
+  int64_t tokens;          /* T new tokens of each sequence, 1 to 16 (several: drafted tokens to verify) */
+  int64_t capacity;        /* slots of each sequence's cache, at most 2^30 */
+  int64_t q_heads, kv_heads, head_dim, window, sinks;  /* as above */
+  int64_t q_stride, k_stride, v_stride, o_stride;      /* of the new tokens */
+  int64_t k_cache_stride, v_cache_stride;              /* from slot to slot */
+  float scale;
+  int32_t io_dtype;
+  int32_t flags;           /* must be 0 */
+  int32_t reserved;        /* must be 0 */
+} m3_attn_decode_dims;
+
+/* The same for T new tokens of each sequence over a cache that it writes them
+ * to first.  The token at position p lies in slot p if p < sinks, and in slot
+ * sinks + (p - sinks) mod (capacity - sinks) otherwise: the sinks stay, the
+ * rest is a ring (a cache longer than the sequence never wraps).
+ * q, o: (batch, T) rows; k, v: (batch, T) rows of the new tokens, rotated
+ * already; k_cache, v_cache: (batch, capacity) rows, updated in place.
+ * lens: (batch) tokens in the cache before the call, on the device; a negative
+ * one marks an idle sequence: its cache is left alone and its o set to 0.
+ * Slots that hold no token yet may hold anything.
+ * With a window, capacity - sinks is at least window + T - 1 (M3_ERR_SHAPE
+ * otherwise); without one, at least T, and every token sees all earlier ones
+ * that the cache holds after the write.
+ * workspace: at least mamba3_window_attn_decode_workspace_size(d) bytes
+ * (results of parts of a long cache; may be 0).
+ * Alignment: io pointers, strides and the workspace 16 bytes, lens 8. */
+m3_status mamba3_window_attn_decode(const m3_attn_decode_dims* d, const void* q, const void* k, const void* v,
+                                    void* k_cache, void* v_cache, const int64_t* lens, void* o, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+size_t mamba3_window_attn_decode_workspace_size(const m3_attn_decode_dims* d);
 
 const char* mamba3_status_string(m3_status s);
 int mamba3_abi_version(void);

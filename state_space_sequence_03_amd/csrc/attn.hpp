@@ -1,0 +1,293 @@
+// What the kernels of windowed attention share: which keys a query sees, the
+// order of the work, and tiles of rows in LDS read as matrix operands both ways.
+//
+// All products are 32 x 32 tiles (mma32 of mm_tile.hpp).  A product's result
+// has its columns over the lanes (lane l: column l mod 32) and its rows in
+// registers (v[4 q + j]: row 8 q + 4 (l / 32) + j).  The first product is laid
+// so that what the softmax runs over, and what the second product sums over,
+// are the rows: the second product's operand is then the lane's own registers,
+// without any exchange, when the other operand's rows come in that order too
+// (Tile::col).
+#pragma once
+
+#include "m3_lanes.hpp"
+#include "mm_tile.hpp"
+
+namespace m3 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFar = 0x7ff00000;  // an offset past every buffer: reads as zero
+
+// A sequence's rows.
+struct AttnSeq {
+  int64_t q0, k0;  // first row of its queries and keys
+  int nq, nk;
+  int64_t id;
+  // position of its query r: past() + r; its keys' are 0 .. nk - 1
+  __device__ __forceinline__ int past() const { return nk - nq; }
+};
+
+__device__ __forceinline__ int64_t start_of(const AttnArgs& a, int64_t i) {
+  const int64_t s = a.starts[i];
+  return s < 0 ? 0 : s > a.rows ? a.rows : s;
+}
+
+// Item `flat` of all sequences' tiles of `tile` rows, longer than `over` rows
+// (queries, or keys with KEYS): the sequence and the tile within it.  false:
+// there are fewer.  Every lane of a wave calls it with the same arguments.
+template <bool KEYS>
+__device__ __forceinline__ bool attn_item(const AttnArgs& a, int64_t flat, int tile, int over, AttnSeq& s, int& t) {
+  if (!a.starts) {
+    const int n = KEYS ? a.kv_len : a.q_len;
+    const int per = n > over ? (n + tile - 1) / tile : 0;
+    if (per == 0) return false;
+    s.id = flat / per;
+    if (s.id >= a.batch) return false;
+    t = (int)(flat - s.id * per);
+    s.q0 = s.id * a.q_len;
+    s.k0 = s.id * a.kv_rows;
+    s.nq = a.q_len;
+    s.nk = a.kv_len;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = 0; b < a.batch; b += 64) {
+    int64_t lo = 0, n = 0;
+    if (b + lane < a.batch) {
+      lo = start_of(a, b + lane);
+      n = start_of(a, b + lane + 1) - lo;
+    }
+    const int mine = n > over ? (int)((n + tile - 1) / tile) : 0;
+    int sum = mine;  // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int x = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += x;
+    }
+    const uint64_t beyond = __ballot(flat < sum);
+    if (beyond) {
+      const int w = __builtin_ctzll(beyond);
+      s.id = b + w;
+      s.q0 = s.k0 = ((int64_t)__builtin_amdgcn_readlane((int)(lo >> 32), w) << 32) |
+                    (uint32_t)__builtin_amdgcn_readlane((int)lo, w);
+      s.nq = s.nk = __builtin_amdgcn_readlane((int)n, w);
+      t = (int)flat - (__builtin_amdgcn_readlane(sum, w) - __builtin_amdgcn_readlane(mine, w));
+      return true;
+    }
+    flat -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+// At most as many items there are.
+inline int64_t attn_items(const AttnArgs& a, bool keys, int tile) {
+  if (!a.starts) return a.batch * (((keys ? a.kv_len : a.q_len) + tile - 1) / tile);
+  return a.rows / tile + (a.batch < a.rows ? a.batch : a.rows);
+}
+
+// Pieces of the sequences that are longer than one, at most.
+inline int64_t attn_pieces(const AttnArgs& a) {
+  if (a.sinks == 0 || a.window >= kNoWindow) return 0;
+  if (!a.starts) return a.q_len > a.piece ? a.batch * ((a.q_len + a.piece - 1) / a.piece) : 0;
+  return a.rows / a.piece * 2;  // a sequence of more than a piece has fewer pieces than twice its whole ones
+}
+
+// Blocks go to the 8 XCDs in turn, each with an L2 of its own: XCD x gets the
+// x-th contiguous eighth of the work, whose neighbours share keys and values.
+__device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
+  const int64_t x = i & 7, per = n >> 3, rem = n & 7;
+  return x * per + (x < rem ? x : rem) + (i >> 3);
+}
+
+// Whether key j is seen from position p.
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
+  return j <= p && (p - j < window || j < sinks);
+}
+// ... every key of [j0, j1] from every position of [p0, p1]
+__device__ __forceinline__ bool sees_all(int p0, int p1, int j0, int j1, int window, int sinks) {
+  return j1 <= p0 && (p1 - j0 < window || j1 < sinks);
+}
+// ... none
+__device__ __forceinline__ bool sees_none(int p0, int p1, int j0, int j1, int window, int sinks) {
+  return j0 > p1 || (p0 - j1 >= window && j0 >= sinks);
+}
+
+// ROWS rows of DP entries in LDS, 16-byte chunk c of row r at chunk c ^ f(r):
+// f spreads the 16 rows of a row read over all banks, and the 4 rows of a
+// transposed read over the quarters of them.  Filled straight from memory by
+// NW waves; entries past the width and rows past the last read as zero.
+template <typename T, int DP, int ROWS, int NW>
+struct Tile {
+  static constexpr int ES = io<T>::BYTES;
+  static constexpr int ROWB = DP * ES;
+  static constexpr int BYTES = ROWS * ROWB;
+  static constexpr int LPR = ROWB / 16;           // lanes per row
+  static constexpr int RPI = 64 / LPR;            // rows per 1 KB load
+  static constexpr int NI = BYTES / 1024 / NW;    // loads per wave
+  static constexpr int KS = ROWB / 32;            // steps of a product over a row
+  static constexpr int CT = DP / 32;              // tiles of a product whose result's rows are the columns
+  static constexpr int CK = ES == 2 ? 16 : 8;     // rows a step of such a product takes
+  static constexpr int NV = RPI * NW % 16 == 0 ? 1 : 16 / (RPI * NW);  // loads until f repeats
+  static_assert(BYTES % (1024 * NW) == 0 && LPR <= 64, "whole loads");
+
+  __device__ __forceinline__ static int f(int r) {
+    if constexpr (ES == 4) return (r & 7) << 1;
+    else if constexpr (LPR == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    else return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+
+  int voff[NV];
+  int ldb;
+  int row_at, col_at[ES == 2 ? 2 : 4];
+  int fx;
+
+  // ld: entries from row to row in memory; width: entries a row has
+  __device__ __forceinline__ void init(int64_t ld, int width, int lane, int wave) {
+    ldb = (int)(ld * ES);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int row = (i * NW + wave) * RPI + lane / LPR, c = (lane % LPR) ^ f(row);
+      voff[i] = c * 16 < width * ES ? (wave * RPI + lane / LPR) * ldb + c * 16 : kFar;
+    }
+    const int r = lane & 31, h = lane >> 5;
+    row_at = r * ROWB + ((h ^ f(r)) << 4);  // step s: the chunk's other bits are flipped by 2 s
+    if constexpr (ES == 2) {
+      const int q = (lane & 15) >> 2, c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + 4 * h + q;
+        col_at[i] = row * ROWB + ((c ^ f(row)) << 4) + (lane & 1) * 8;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * h + i;
+        col_at[i] = row * ROWB + (((r >> 2) ^ f(row)) << 4) + (r & 3) * 4;
+      }
+    }
+  }
+  // base: the first row; rows: that exist, from 1.  Device code only: a second
+  // kernel that calls this loses its host stub, without an error, where the
+  // host's pass meets the builtins.
+  __device__ __forceinline__ void load(const char* base, int rows, int width, char* lds, int wave) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int n = rows < ROWS ? rows : ROWS;
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (uint32_t)((n - 1) * ldb + width * ES), 0x00020000);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * NW + wave) * 1024), 16, voff[i % NV],
+                                               i * NW * RPI * ldb, 0, 0);
+#endif
+  }
+  // rows [32 t, 32 t + 32) as an operand whose sum runs over the columns, step s
+  __device__ __forceinline__ uint4 row(const char* lds, int t, int s) const {
+    return __builtin_bit_cast(uint4, read16((const u32x4*)(lds + ((row_at ^ (s << 5)) + t * 32 * ROWB))));
+  }
+  // columns [32 t, 32 t + 32) as an operand whose sum runs over the rows, step
+  // ks: rows CK ks .. + CK - 1 in the order in which a product's result holds
+  // its rows
+  __device__ __forceinline__ uint4 col(const char* lds, int t, int ks) const {
+    const char* p = lds + ks * CK * ROWB;
+    if constexpr (ES == 2) {
+      const uint2 a = read_tr(p + (col_at[0] ^ (t << 6))), b = read_tr(p + (col_at[1] ^ (t << 6)));
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      return make_uint4(read4((const uint32_t*)(p + (col_at[0] ^ (t << 7)))),
+                        read4((const uint32_t*)(p + (col_at[1] ^ (t << 7)))),
+                        read4((const uint32_t*)(p + (col_at[2] ^ (t << 7)))),
+                        read4((const uint32_t*)(p + (col_at[3] ^ (t << 7)))));
+    }
+  }
+};
+
+// 32 rows from memory as the other operand of a product over their columns:
+// lane l holds row l mod 32.  in: that row exists.
+template <typename T, int DP>
+struct RowRegs {
+  static constexpr int KS = DP * io<T>::BYTES / 32;
+  uint4 v[KS];
+  __device__ __forceinline__ void load(const char* row, bool in, int width, int h) {
+    constexpr int V = io<T>::VEC;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      v[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && (2 * s + h) * V < width) v[s] = *(const uint4*)(row + (2 * s + h) * 16);
+    }
+  }
+};
+
+// Step ks of a result (its rows 16 ks .. or 8 ks ..) as the operand that goes
+// with Tile::col.
+template <typename T>
+__device__ __forceinline__ uint4 result_step(const float* v, int ks) {
+  if constexpr (io<T>::BYTES == 2) {
+    const float* p = v + 8 * ks;
+    return make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
+  } else {
+    const float* p = v + 4 * ks;
+    return make_uint4(__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]), __float_as_uint(p[3]));
+  }
+}
+
+// Larger of lane l's and lane l ^ 32's.
+__device__ __forceinline__ float max_halves(float v) {
+  uint32_t a = __float_as_uint(v), b = a;
+  asm volatile("" : "+v"(b));
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = s[0];
+  b = s[1];
+  asm volatile("" : "+v"(a), "+v"(b));
+  return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+
+// This wave's loads into LDS have landed and its reads are done, and so it is
+// with every wave of the block.
+__device__ __forceinline__ void attn_settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// The softmax of 32 columns over rows that come in pieces: running maximum
+// and sum, and the result's columns scaled along.
+//
+// The maximum is let behind by up to kSlack powers of two before what was
+// summed is scaled anew: p stays below 2^kSlack, where fp32 sums and bf16
+// roundings are as exact as below 1.
+constexpr float kSlack = 8.0f;
+template <int CT>
+struct Softmax {
+  float m, l;  // m of both halves of the wave, l of the lane's own rows
+  __device__ __forceinline__ void init() {
+    m = -INFINITY;
+    l = 0.0f;
+  }
+  // s: NS scores of the lane's column (-inf: not seen), turned into weights
+  template <int NS>
+  __device__ __forceinline__ void step(float* s, float c, f32x16 (&acc)[CT]) {
+    float t = s[0];
+#pragma unroll
+    for (int i = 1; i < NS; ++i) t = fmaxf(t, s[i]);
+    t = max_halves(t);
+    if (__any((t - m) * c > kSlack || (m == -INFINITY && t > m))) {
+      const float n = fmaxf(m, t);
+      const float scale = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - n) * c);
+      m = n;
+      l *= scale;
+#pragma unroll
+      for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] *= scale;
+    }
+    const float mc = m == -INFINITY ? 0.0f : m * c;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+      l += s[i];
+    }
+  }
+};
+
+}  // namespace m3

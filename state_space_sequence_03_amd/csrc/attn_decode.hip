@@ -1,0 +1,39 @@
+// Windowed attention over a cache, both types, and the plans of the launches
+// that the workspaces depend on.
+#include "attn_decode.hpp"
+
+namespace m3 {
+
+template hipError_t launch_attn_decode<bf16_t>(const AttnDecodeArgs&, hipStream_t);
+template hipError_t launch_attn_decode<float>(const AttnDecodeArgs&, hipStream_t);
+
+// Enough blocks for every CU, each wave with two tiles of 32 slots at least.
+int attn_decode_splits(int io_bf16, const AttnDecodeArgs& a) {
+  const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
+  const int64_t blocks = a.batch * a.kv_heads * groups, waves = !io_bf16 && a.dim > 64 ? 2 : 4;
+  int64_t slots = a.capacity;
+  if (a.window < kNoWindow && slots > (int64_t)a.sinks + a.window + a.tokens - 1)
+    slots = (int64_t)a.sinks + a.window + a.tokens - 1;
+  const int64_t most = (slots + 31) / 32 / (2 * waves), want = blocks > 0 ? (256 + blocks - 1) / blocks : 1;
+  const int64_t n = want < most ? want : most;
+  return n < 1 ? 1 : (int)n;
+}
+size_t attn_decode_part_bytes(const AttnDecodeArgs& a) {
+  return a.splits == 1 ? 0 : (size_t)a.batch * a.tokens * a.q_heads * a.splits * (a.dim + 2) * 4;
+}
+
+// Queries of a piece of a sinks' tile: about as many as see a tile behind the
+// sinks, and so many that there are 2048 pieces at most.
+int attn_bwd_piece(const AttnArgs& a) {
+  int64_t n = (a.window < (1 << 24) ? a.window : 1 << 24) + 128;
+  const int64_t work = a.rows * ((a.sinks + 127) / 128) * a.kv_heads;
+  if (n < 1024) n = 1024;
+  if (n < work / 1024) n = work / 1024;
+  n = (n + 127) / 128 * 128;
+  return (int)(n < (1 << 25) ? n : 1 << 25);
+}
+size_t attn_bwd_part_bytes(const AttnArgs& a) {
+  return (size_t)attn_pieces(a) * ((a.sinks + 127) / 128) * a.kv_heads * 2 * 128 * a.dim * 4;
+}
+
+}  // namespace m3

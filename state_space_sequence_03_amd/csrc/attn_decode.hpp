@@ -1,0 +1,266 @@
+// Windowed attention with sinks of new tokens over a cache that wraps.
+#pragma once
+
+#include "attn.hpp"
+
+namespace m3 {
+
+// The slots of a sequence's cache that its new tokens see, as two runs, and
+// the position that each holds.  Positions are taken relative to the first new
+// token's, n: those that matter lie within the cache's length of it.
+struct CacheView {
+  int end0, from1, end1;  // slots [0, end0) and [from1, end1)
+  int slot_n;             // of the first new token; the others' follow, and go on behind the sinks at the cache's end
+  int n;                  // tokens before the call, or 2^30 for more
+  int ring, sinks, rem, newer;
+  __device__ __forceinline__ void init(int64_t len, int tokens, int capacity, int sinks_, int window) {
+    sinks = sinks_;
+    ring = capacity - sinks;
+    n = len < (1 << 30) ? (int)len : 1 << 30;
+    const int64_t last = len + tokens - 1;
+    slot_n = (int)(len < sinks ? len : sinks + (len - sinks) % ring);
+    from1 = end1 = 0;
+    rem = -1;
+    newer = 0;
+    if (last < sinks) {
+      end0 = (int)(last + 1);
+      return;
+    }
+    const int64_t turns = (last - sinks) / ring;
+    rem = (int)(last - sinks - turns * ring);
+    newer = (int)(sinks + turns * ring - len);
+    int64_t lo = len - window + 1;
+    if (lo < last - ring + 1) lo = last - ring + 1;
+    if (lo < sinks) lo = sinks;
+    const int count = (int)(last - lo + 1), at = (int)((lo - sinks) % ring);
+    if (at + count <= ring) {
+      end0 = sinks;
+      from1 = sinks + at;
+      end1 = from1 + count;
+    } else {
+      end0 = sinks + at + count - ring;
+      from1 = sinks + at;
+      end1 = capacity;
+    }
+    if (from1 == end0) {
+      end0 = end1;
+      from1 = end1 = 0;
+    }
+  }
+  __device__ __forceinline__ int tiles0() const { return (end0 + 31) >> 5; }
+  __device__ __forceinline__ int tiles() const { return tiles0() + ((end1 - from1 + 31) >> 5); }
+  // slots [x, e) of tile i, 32 at most
+  __device__ __forceinline__ void tile(int i, int& x, int& e) const {
+    const int n0 = tiles0();
+    x = i < n0 ? i * 32 : from1 + (i - n0) * 32;
+    e = i < n0 ? end0 : end1;
+    if (e > x + 32) e = x + 32;
+  }
+  // whether new token t sees what slot x holds
+  __device__ __forceinline__ bool seen(int x, int t, int window) const {
+    if (x < sinks) return x - n <= t;
+    const int r = x - sinks, rel = r <= rem ? newer + r : newer + r - ring;
+    return rel <= t && t - rel < window;
+  }
+};
+
+// A block takes the heads and tokens that share a head's keys, 32 at a time,
+// as the columns of its products, and a share of the slots they see; each wave
+// walks 32 slots at a time of its own, straight from memory into its part of
+// LDS, the next ones' while this one's products run, and needs no other wave
+// until the end, when the waves' results are joined.  The new tokens' keys and
+// values are written to the cache by the wave that then reads their slots.
+//
+// Bound by HBM: the slots seen are read once per 32 columns.
+template <typename T, int DP, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs a) {
+  using KV = Tile<T, DP, 32, 1>;
+  constexpr int ES = io<T>::BYTES, STEPS = 32 / KV::CK, LD = DP + 4;
+  static_assert(32 * LD * 4 <= 4 * KV::BYTES, "a wave's result fits its part");
+  __shared__ __attribute__((aligned(1024))) char smem[NW * 4 * KV::BYTES];
+  __shared__ float stat[NW][2][32];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, col = lane & 31;
+  const int G = a.q_heads / a.kv_heads, cols = G * a.tokens;
+  const int groups = (cols + 31) / 32;
+  int64_t id = xcd_order(blockIdx.x, gridDim.x);
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  const int group = (int)(id % groups);
+  id /= groups;
+  const int64_t hk = id % a.kv_heads, b = id / a.kv_heads;
+  const int c0 = group * 32;
+  const bool in = c0 + col < cols;
+  const int tok = in ? (c0 + col) / G : 0;
+  const int64_t hq = hk * G + (in ? (c0 + col) - tok * G : 0);
+  RowRegs<T, DP> q;
+  q.load((const char*)a.q + ((b * a.tokens + tok) * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
+
+  CacheView view;
+  const int64_t len = a.lens[b];
+  int begin = 0, end = 0;
+  if (len >= 0) {
+    view.init(len, a.tokens, (int)a.capacity, a.sinks, a.window);
+    const int share = NW * a.splits, per = (view.tiles() + share - 1) / share;
+    begin = (split * NW + wave) * per;
+    end = begin + per < view.tiles() ? begin + per : view.tiles();
+  }
+  KV kt, vt;
+  kt.init(a.kc_stride, a.dim, lane, 0);
+  vt.init(a.vc_stride, a.dim, lane, 0);
+  char* kc = (char*)a.k_cache + (b * a.capacity * a.kc_stride + hk * a.dim) * ES;
+  char* vc = (char*)a.v_cache + (b * a.capacity * a.vc_stride + hk * a.dim) * ES;
+  char* mine = smem + wave * 4 * KV::BYTES;
+  auto load = [&](int i, int buf) {
+    int x, e;
+    view.tile(i, x, e);
+    // new tokens that fall into the tile
+    int at = view.slot_n + lane;
+    if (at >= a.capacity) at -= view.ring;
+    uint64_t fresh = __ballot(lane < a.tokens && at >= x && at < e);
+    if (fresh) {
+      while (fresh) {
+        const int t = __builtin_ctzll(fresh);
+        fresh &= fresh - 1;
+        const int64_t slot = __builtin_amdgcn_readlane(at, t), row = b * a.tokens + t;
+        const char* src = h ? (const char*)a.v + (row * a.v_stride + hk * a.dim) * ES
+                            : (const char*)a.k + (row * a.k_stride + hk * a.dim) * ES;
+        char* dst = h ? vc + slot * a.vc_stride * ES : kc + slot * a.kc_stride * ES;
+        if (col * 16 < a.dim * ES) *(uint4*)(dst + col * 16) = *(const uint4*)(src + col * 16);
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores are done
+      asm volatile("" ::: "memory");
+    }
+    kt.load(kc + (int64_t)x * a.kc_stride * ES, e - x, a.dim, mine + buf * 2 * KV::BYTES, 0);
+    vt.load(vc + (int64_t)x * a.vc_stride * ES, e - x, a.dim, mine + (buf * 2 + 1) * KV::BYTES, 0);
+  };
+  f32x16 acc[KV::CT];
+#pragma unroll
+  for (int i = 0; i < KV::CT; ++i) acc[i] = f32x16{};
+  Softmax<KV::CT> soft;
+  soft.init();
+  const float c = a.scale * kLog2e;
+  if (begin < end) load(begin, 0);
+  for (int i = begin; i < end; ++i) {
+    const int buf = (i - begin) & 1;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    if (i + 1 < end) load(i + 1, buf ^ 1);
+    const char* kl = mine + buf * 2 * KV::BYTES;
+    int x, e;
+    view.tile(i, x, e);
+    f32x16 sc = f32x16{};
+#pragma unroll
+    for (int st = 0; st < KV::KS; ++st) sc = mma32<T>(kt.row(kl, 0, st), q.v[st], sc);
+    float z[16];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int j = x + v / 4 * 8 + 4 * h + v % 4;
+      z[v] = j < e && view.seen(j, tok, a.window) ? sc[v] : -INFINITY;
+    }
+    soft.template step<16>(z, c, acc);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const uint4 w = result_step<T>(z, k);
+#pragma unroll
+      for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(vt.col(kl + KV::BYTES, d, k), w, acc[d]);
+    }
+  }
+  // the waves' results: maximum, sum and unscaled output of each column
+  const float l = swap_sum32(soft.l);
+  float* res = (float*)mine;
+  __syncthreads();
+  if (h == 0) {
+    stat[wave][0][col] = soft.m;
+    stat[wave][1][col] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < KV::CT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *(f32x4*)(res + col * LD + d * 32 + 8 * i + 4 * h) =
+          f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+  __syncthreads();
+  const int width = a.dim / 4, valid = cols - c0 < 32 ? cols - c0 : 32;
+  for (int e = threadIdx.x; e < valid * width; e += 64 * NW) {
+    const int k = e / width, d = (e - k * width) * 4, t = (c0 + k) / G;
+    float m = stat[0][0][k];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) m = fmaxf(m, stat[w][0][k]);
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[w][0][k] - m) * c);
+      sum += f * stat[w][1][k];
+      const f32x4 x = *(const f32x4*)((const float*)(smem + w * 4 * KV::BYTES) + k * LD + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] += f * x[j];
+    }
+    const int64_t row = b * a.tokens + t, head = hk * G + (c0 + k - t * G);
+    if (a.splits == 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float f[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+      io<T>::store4(a.o, row * a.o_stride + head * a.dim + d, f);
+    } else {
+      // (row, head, split): output, then maximum and sum of all of them
+      const int64_t at = (row * a.q_heads + head) * a.splits + split;
+      *(f32x4*)(a.part + at * a.dim + d) = o;
+      if (d == 0) {
+        float* s = a.part + a.batch * a.tokens * a.q_heads * a.splits * a.dim + 2 * at;
+        s[0] = m;
+        s[1] = sum;
+      }
+    }
+  }
+}
+
+// The splits joined in order: a wave per row and head.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnDecodeArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t all = a.batch * a.tokens * a.q_heads, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= all) return;
+  const float* stat = a.part + all * a.splits * a.dim + 2 * id * a.splits;
+  const float c = a.scale * kLog2e;
+  float m = -INFINITY;
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, stat[2 * i]);
+  float o[2] = {0.0f, 0.0f}, sum = 0.0f;
+  const float* part = a.part + id * a.splits * a.dim;
+  const int d0 = lane < a.dim ? lane : 0, d1 = lane + 64 < a.dim ? lane + 64 : 0;
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) {
+    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[2 * i] - m) * c);
+    sum += f * stat[2 * i + 1];
+    o[0] += f * part[i * a.dim + d0];
+    o[1] += f * part[i * a.dim + d1];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t row = id / a.q_heads, at = row * a.o_stride + (id - row * a.q_heads) * a.dim;
+  if (lane < a.dim) io<T>::store1(a.o, at + lane, o[0] * inv);
+  if (lane + 64 < a.dim) io<T>::store1(a.o, at + lane + 64, o[1] * inv);
+}
+
+template <typename T, int DP, int NW>
+void attn_decode_run(const AttnDecodeArgs& a, hipStream_t s) {
+  const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
+  hipLaunchKernelGGL((attn_decode_kernel<T, DP, NW>), dim3((unsigned)(a.batch * a.kv_heads * groups * a.splits)),
+                     dim3(64 * NW), 0, s, a);
+}
+
+template <typename T>
+hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s) {
+  if (a.dim <= 64) attn_decode_run<T, 64, 4>(a, s);
+  else attn_decode_run<T, 128, io<T>::BYTES == 2 ? 4 : 2>(a, s);
+  if (a.splits > 1) {
+    const int64_t rows = a.batch * a.tokens * a.q_heads;
+    hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace m3

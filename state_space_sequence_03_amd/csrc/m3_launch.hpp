@@ -244,6 +244,80 @@ hipError_t launch_act_bwd(int io_bf16, const ActBwdArgs& a, hipStream_t s);
 // Zeros to `bytes` bytes of dst (2-byte aligned, an even count).
 hipError_t launch_zero(void* dst, int64_t bytes, hipStream_t s);
 
+// Norms of queries and keys for each head with their rotation: forward (q, k
+// -> q_out, k_out) or backward (dq_out, dk_out -> q_out, k_out, which then
+// hold the gradients of q and k).  Row strides in elements.
+struct NormRopeArgs {
+  const void *q, *k;            // either null where its heads are 0
+  const void *dq_out, *dk_out;  // backward; strides q_out_stride, k_out_stride
+  void *q_out, *k_out;          // backward: strides dq_stride, dk_stride
+  const float *gain_q, *gain_k;  // nullable
+  const float* theta;            // (rope / 2)
+  const int64_t* pos;            // (rows), nullable: the row's place among its `seqlen`
+  float* part;                   // nullable: (norm_rope_parts, 2, dim)
+  float *dgain_q, *dgain_k;      // with part, each nullable
+  float eps;
+  int64_t rows, q_stride, k_stride, q_out_stride, k_out_stride, dq_stride, dk_stride;
+  int seqlen;  // 0: rows are counted through
+  int q_heads, k_heads, dim, rope, halves;
+  int tokens;  // per block, set by the launch
+};
+int64_t norm_rope_parts(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int64_t rope);
+hipError_t launch_norm_rope(int io_bf16, bool bwd, NormRopeArgs a, hipStream_t s);
+
+// Causal attention over a window with sinks.  Rows are tokens, strides in
+// elements from token to token, the heads of a token adjacent.
+constexpr int kNoWindow = 1 << 30;
+struct AttnArgs {
+  const void *q, *k, *v;
+  void* o;
+  float* lse;             // (rows, q_heads), nullable
+  const int64_t* starts;  // (batch + 1), nullable: packed sequences, the same rows for queries and keys
+  int64_t batch;
+  int64_t rows;     // of q in all
+  int64_t kv_rows;  // of k from sequence to sequence (no starts)
+  int q_len, kv_len;      // no starts
+  int q_heads, kv_heads, dim;
+  int window;  // kNoWindow: none
+  int sinks;
+  float scale;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  // backward
+  const void* dout;
+  void *dq, *dk, *dv;  // each nullable
+  int64_t do_stride, dq_stride, dk_stride, dv_stride;
+  float *lse2, *delta;  // workspace: (q_heads, rows): lse in powers of two (+inf for a row that sees nothing), rowsum(do o)
+  float* part;          // workspace of the sinks' tiles
+  int piece;            // queries of a piece of a sinks' tile
+};
+size_t attn_bwd_part_bytes(const AttnArgs& a);
+int attn_bwd_piece(const AttnArgs& a);
+template <typename T>
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
+template <typename T>
+hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s);
+
+// The same for new tokens over a cache of `capacity` slots: token p lies in
+// slot p < sinks, or sinks + (p - sinks) mod (capacity - sinks).
+struct AttnDecodeArgs {
+  const void *q, *k, *v;  // (batch, tokens, heads, dim), strides from token to token
+  void *k_cache, *v_cache;
+  const int64_t* lens;  // (batch): tokens before the call; negative: an idle sequence
+  void* o;
+  int64_t batch, capacity;
+  int tokens, q_heads, kv_heads, dim;
+  int window;  // kNoWindow: none
+  int sinks;
+  float scale;
+  int64_t q_stride, k_stride, v_stride, o_stride, kc_stride, vc_stride;  // from token (slot) to token
+  float* part;
+  int splits;
+};
+int attn_decode_splits(int io_bf16, const AttnDecodeArgs& a);
+size_t attn_decode_part_bytes(const AttnDecodeArgs& a);
+template <typename T>
+hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s);
+
 // Fill n floats of dst with src (or zeros when src is NULL).
 hipError_t launch_copy_f32(float* dst, const float* src, int64_t n, hipStream_t s);
 

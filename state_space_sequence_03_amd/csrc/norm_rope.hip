@@ -1,0 +1,266 @@
+// Norms of queries and keys for each head, with the position rotation in the
+// same pass.
+//   forward:  r = 1 / sqrt(sum x^2 / D + eps), z = x r gain, and the pairs of
+//             z's first R entries turned by pos theta[pair];
+//   backward: dz = dy turned back, a = dz gain, xh = x r,
+//             dx = r (a - xh mean_D(a xh)), dgain = sum over vectors of dz xh.
+// Both are bound by HBM: a vector (one head of one token) belongs to LPV lanes
+// that hold it in registers, is read once and its result written once, queries
+// and keys in one launch.  The cosines and sines are taken once per token and
+// pair, shared by the token's heads through LDS; the angle is a product in 64
+// bits reduced to a fraction of a turn there, so that far positions lose
+// nothing.
+#include "m3_lanes.hpp"
+#include "m3_launch.hpp"
+#include "m3_rows.hpp"
+
+namespace m3 {
+
+namespace {
+
+constexpr int kTable = 2048;  // (token, pair) entries a block holds
+
+// Cosine and sine of each pair's angle for tokens [t0, t0 + n).
+__device__ __forceinline__ void fill_table(const NormRopeArgs& a, int64_t t0, int n, float2* tab) {
+  const int pairs = a.rope / 2;
+  for (int i = threadIdx.x; i < n * pairs; i += 256) {
+    const int t = i / pairs;
+    const int64_t row = t0 + t;
+    const int64_t pos = a.pos ? a.pos[row] : a.seqlen ? (int64_t)((uint32_t)row % (uint32_t)a.seqlen) : row;
+    const double turn = (double)pos * (double)a.theta[i - t * pairs] * 0.15915494309189533577;
+    float s, c;
+    sincospif(2.0f * (float)(turn - rint(turn)), &s, &c);
+    tab[i] = make_float2(c, s);
+  }
+}
+
+// The lane's entries [c, c + V) of a vector turned by its token's angles (DIR
+// = 1) or back (-1).  xs: LDS of the vector's own, for pairs half apart.
+template <int V, bool HALVES, int DIR>
+__device__ __forceinline__ void turn(const NormRopeArgs& a, const float2* tab, float* xs, int c, float* f) {
+  const int R = a.rope;
+  if constexpr (HALVES) {
+    const int h = R / 2;
+    // the lanes of a vector are of one wave: its LDS accesses go in order
+#pragma unroll
+    for (int j = 0; j < V; j += 4) *(f32x4*)(xs + c + j) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+    asm volatile("" ::: "memory");
+    if (h % V == 0) {  // the lane's partners are one lane's
+      if (c < R) {
+        const bool low = c < h;
+        const int p = low ? c + h : c - h;
+        const float sign = (low ? -1.0f : 1.0f) * DIR;
+        const float2* t = tab + (low ? c : p);
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          const f32x4 o = *(const f32x4*)(xs + p + j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 cs = t[j + e];
+            f[j + e] = f[j + e] * cs.x + sign * o[e] * cs.y;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (c + j < R) {
+          const bool low = c + j < h;
+          const int p = low ? c + j + h : c + j - h;
+          const float2 cs = tab[low ? c + j : p];
+          f[j] = f[j] * cs.x + (low ? -1.0f : 1.0f) * DIR * xs[p] * cs.y;
+        }
+    }
+    asm volatile("" ::: "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+      if (c + j < R) {
+        const float2 cs = tab[(c + j) / 2];
+        const float x = f[j], y = f[j + 1];
+        f[j] = x * cs.x - DIR * y * cs.y;
+        f[j + 1] = y * cs.x + DIR * x * cs.y;
+      }
+  }
+}
+
+// Vector u of the tokens from t0 on: which operand, and its place in a matrix
+// of the two operands' row strides.
+struct Place {
+  bool key;
+  int token;
+  int64_t row;
+  int head;
+  __device__ __forceinline__ Place(const NormRopeArgs& a, int64_t t0, int u) {
+    const int H = a.q_heads + a.k_heads;
+    token = u / H;
+    row = t0 + token;
+    head = u - token * H;
+    key = head >= a.q_heads;
+    if (key) head -= a.q_heads;
+  }
+  template <typename T>
+  __device__ __forceinline__ char* at(const NormRopeArgs& a, const void* q, const void* k, int64_t sq,
+                                      int64_t sk) const {
+    return (char*)(key ? k : q) + (row * (key ? sk : sq) + (int64_t)head * a.dim) * io<T>::BYTES;
+  }
+};
+
+// 1 / sqrt(mean x^2 + eps) of a vector held by LPV lanes (entries past its
+// width are 0).
+template <int V, int LPV>
+__device__ __forceinline__ float rms(const float* f, int dim, float eps) {
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) s += f[j] * f[j];
+  return 1.0f / sqrtf(lane_sum<1, LPV>(s) / (float)dim + eps);
+}
+
+template <typename T, int LPV, bool HALVES>
+__global__ __launch_bounds__(256) void norm_rope_fwd_kernel(NormRopeArgs a) {
+  constexpr int V = io<T>::VEC, VPB = 256 / LPV;
+  __shared__ float2 tab[kTable];
+  __shared__ __attribute__((aligned(16))) float xs[HALVES ? 256 * V : 4];
+  const int lane = threadIdx.x % LPV, slot = threadIdx.x / LPV, c = lane * V;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int n = a.rows - t0 < a.tokens ? (int)(a.rows - t0) : a.tokens;
+  const int vectors = n * (a.q_heads + a.k_heads);
+  u32x4 raw = {0u, 0u, 0u, 0u};
+  int u = slot;
+  if (u < vectors) raw = row_raw<T>(Place(a, t0, u).at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
+  float g[2][V];
+  col_load<V>(a.gain_q, c, a.dim, 1.0f, g[0]);
+  col_load<V>(a.gain_k, c, a.dim, 1.0f, g[1]);
+  fill_table(a, t0, n, tab);
+  __syncthreads();
+  while (u < vectors) {
+    const Place at(a, t0, u);
+    float f[V];
+    unpack_raw<T>(raw, f);
+    u += VPB;
+    if (u < vectors) raw = row_raw<T>(Place(a, t0, u).at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
+    const float r = rms<V, LPV>(f, a.dim, a.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] *= r * (at.key ? g[1][j] : g[0][j]);
+    turn<V, HALVES, 1>(a, tab + at.token * (a.rope / 2), xs + (HALVES ? slot * LPV * V : 0), c, f);
+    row_store<T>(at.at<T>(a, a.q_out, a.k_out, a.q_out_stride, a.k_out_stride), c, a.dim, f);
+  }
+}
+
+// Token groups blockIdx, blockIdx + gridDim, ..., and the sums over them that
+// the gains' gradients take from a block.
+template <typename T, int LPV, bool HALVES>
+__global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormRopeArgs a) {
+  constexpr int V = io<T>::VEC, VPB = 256 / LPV;
+  __shared__ float2 tab[kTable];
+  __shared__ __attribute__((aligned(16))) float xs[256 * V];
+  const int lane = threadIdx.x % LPV, slot = threadIdx.x / LPV, c = lane * V;
+  float g[2][V], sum[2][V];
+  col_load<V>(a.gain_q, c, a.dim, 1.0f, g[0]);
+  col_load<V>(a.gain_k, c, a.dim, 1.0f, g[1]);
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[0][j] = sum[1][j] = 0.0f;
+  for (int64_t t0 = (int64_t)blockIdx.x * a.tokens; t0 < a.rows; t0 += (int64_t)gridDim.x * a.tokens) {
+    const int n = a.rows - t0 < a.tokens ? (int)(a.rows - t0) : a.tokens;
+    const int vectors = n * (a.q_heads + a.k_heads);
+    u32x4 rx = {0u, 0u, 0u, 0u}, ry = rx;
+    int u = slot;
+    auto load = [&] {
+      const Place at(a, t0, u);
+      rx = row_raw<T>(at.at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
+      ry = row_raw<T>(at.at<T>(a, a.dq_out, a.dk_out, a.q_out_stride, a.k_out_stride), c, a.dim);
+    };
+    if (u < vectors) load();
+    fill_table(a, t0, n, tab);
+    __syncthreads();
+    while (u < vectors) {
+      const Place at(a, t0, u);
+      float x[V], d[V];
+      unpack_raw<T>(rx, x);
+      unpack_raw<T>(ry, d);
+      u += VPB;
+      if (u < vectors) load();
+      const float r = rms<V, LPV>(x, a.dim, a.eps);
+      turn<V, HALVES, -1>(a, tab + at.token * (a.rope / 2), xs + slot * LPV * V, c, d);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[j] *= r;
+        const float w = d[j] * x[j];
+        if (at.key) sum[1][j] += w;
+        else sum[0][j] += w;
+        d[j] *= at.key ? g[1][j] : g[0][j];
+        s += d[j] * x[j];
+      }
+      s = lane_sum<1, LPV>(s) / (float)a.dim;
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = r * (d[j] - x[j] * s);
+      row_store<T>(at.at<T>(a, a.q_out, a.k_out, a.dq_stride, a.dk_stride), c, a.dim, d);
+    }
+    __syncthreads();  // the table is read
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) xs[slot * LPV * V + c + j] = sum[o][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.dim; e += 256) {
+      float s = 0.0f;
+      for (int i = 0; i < VPB; ++i) s += xs[i * LPV * V + e];
+      a.part[((int64_t)blockIdx.x * 2 + o) * a.dim + e] = s;
+    }
+  }
+}
+
+template <typename T, int LPV, bool HALVES>
+void launch(bool bwd, const NormRopeArgs& a, unsigned blocks, hipStream_t s) {
+  if (bwd) hipLaunchKernelGGL((norm_rope_bwd_kernel<T, LPV, HALVES>), dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((norm_rope_fwd_kernel<T, LPV, HALVES>), dim3(blocks), dim3(256), 0, s, a);
+}
+template <typename T, bool HALVES>
+void launch_lanes(bool bwd, const NormRopeArgs& a, unsigned blocks, hipStream_t s) {
+  const int lanes = (a.dim + io<T>::VEC - 1) / io<T>::VEC;
+  if (lanes <= 4) launch<T, 4, HALVES>(bwd, a, blocks, s);
+  else if (lanes <= 8) launch<T, 8, HALVES>(bwd, a, blocks, s);
+  else if (lanes <= 16) launch<T, 16, HALVES>(bwd, a, blocks, s);
+  else if (lanes <= 32) launch<T, 32, HALVES>(bwd, a, blocks, s);
+  else launch<T, 64, HALVES>(bwd, a, blocks, s);
+}
+
+// Tokens per block: enough vectors for a few passes of the block, while the
+// grid still covers the chip twice over.
+int tokens_per_block(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int64_t rope) {
+  const int64_t per = heads * ((dim + (io_bf16 ? 7 : 3)) / (io_bf16 ? 8 : 4));  // lanes of a token
+  int64_t t = (1024 + per - 1) / per;
+  if (t > rows / 512) t = rows / 512;
+  if (rope > 0 && t > kTable / (rope / 2)) t = kTable / (rope / 2);
+  return t < 1 ? 1 : t > 64 ? 64 : (int)t;
+}
+
+}  // namespace
+
+int64_t norm_rope_parts(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int64_t rope) {
+  const int64_t t = tokens_per_block(io_bf16, rows, heads, dim, rope), groups = (rows + t - 1) / t;
+  return groups < 1024 ? groups : 1024;
+}
+
+hipError_t launch_norm_rope(int io_bf16, bool bwd, NormRopeArgs a, hipStream_t s) {
+  const int64_t heads = a.q_heads + a.k_heads;
+  a.tokens = tokens_per_block(io_bf16, a.rows, heads, a.dim, a.rope);
+  const int64_t groups = (a.rows + a.tokens - 1) / a.tokens;
+  const unsigned blocks = (unsigned)(bwd ? norm_rope_parts(io_bf16, a.rows, heads, a.dim, a.rope) : groups);
+  if (io_bf16) {
+    if (a.halves) launch_lanes<bf16_t, true>(bwd, a, blocks, s);
+    else launch_lanes<bf16_t, false>(bwd, a, blocks, s);
+  } else {
+    if (a.halves) launch_lanes<float, true>(bwd, a, blocks, s);
+    else launch_lanes<float, false>(bwd, a, blocks, s);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !bwd || !a.part) return e;
+  return launch_reduce_parts(a.part, blocks, 2 * (int64_t)a.dim, 2 * (int64_t)a.dim, a.dgain_q, a.dim, a.dgain_k, s);
+}
+
+}  // namespace m3

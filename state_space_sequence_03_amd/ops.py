@@ -9,7 +9,9 @@ Entry points keep the ABI's names:
   mamba3_ssm_chunked_fwd, mamba3_ssm_chunked_bwd, mamba3_ssm_decode_step,
   mamba3_rope_bc, mamba3_bc_prologue,
   mamba3_layer_norm_fwd, mamba3_layer_norm_bwd, mamba3_linear_fwd,
-  mamba3_linear_bwd, mamba3_gated_ffn_fwd, mamba3_gated_ffn_bwd
+  mamba3_linear_bwd, mamba3_gated_ffn_fwd, mamba3_gated_ffn_bwd,
+  mamba3_qk_norm_rope_fwd, mamba3_qk_norm_rope_bwd, mamba3_window_attn_fwd,
+  mamba3_window_attn_bwd, mamba3_window_attn_decode
 (and the friendlier aliases without the prefix: chunked_fwd, chunked_bwd,
 decode_step, rope_bc, bc_prologue, layer_norm_fwd, ...), plus the workspace
 size queries.
@@ -39,8 +41,14 @@ ABI_SYMBOLS = ("mamba3_ssm_chunked_fwd", "mamba3_ssm_chunked_fwd_workspace_size"
                "mamba3_layer_norm_bwd_workspace_size", "mamba3_linear_fwd", "mamba3_linear_fwd_workspace_size",
                "mamba3_linear_bwd", "mamba3_linear_bwd_workspace_size", "mamba3_gated_ffn_fwd",
                "mamba3_gated_ffn_fwd_workspace_size", "mamba3_gated_ffn_bwd", "mamba3_gated_ffn_bwd_workspace_size",
+               "mamba3_qk_norm_rope_fwd", "mamba3_qk_norm_rope_bwd", "mamba3_qk_norm_rope_bwd_workspace_size",
+               "mamba3_window_attn_fwd", "mamba3_window_attn_bwd", "mamba3_window_attn_bwd_workspace_size",
+               "mamba3_window_attn_decode", "mamba3_window_attn_decode_workspace_size",
                "mamba3_status_string", "mamba3_abi_version")
 M3_FLAG_UNALIGNED = 0x40000    # linear, gated_ffn: operands off 16 bytes are copied first
+M3_FLAG_ROPE_HALVES = 0x80000  # qk_norm_rope: pairs half of rope_dim apart
+M3_FLAG_PACKED = 0x100000      # window_attn: sequences of any lengths, given by starts
+M3_DECODE_MAX_TOKENS = 16      # new tokens of a sequence that window_attn_decode takes
 # activations of linear and gated_ffn
 M3_ACT_NONE, M3_ACT_RELU, M3_ACT_SILU, M3_ACT_GELU, M3_ACT_GELU_TANH, M3_ACT_SIGMOID = range(6)
 
@@ -61,6 +69,30 @@ class LinearDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
                 ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class NormRopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("rows", "seqlen", "q_heads", "k_heads", "head_dim", "rope_dim", "q_stride", "k_stride",
+                 "q_out_stride", "k_out_stride", "dq_stride", "dk_stride")] + \
+               [("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "q_len", "kv_len", "rows", "kv_rows", "q_heads", "kv_heads", "head_dim", "window", "sinks",
+                 "q_stride", "k_stride", "v_stride", "o_stride", "do_stride", "dq_stride", "dk_stride",
+                 "dv_stride")] + \
+               [("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class AttnDecodeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "tokens", "capacity", "q_heads", "kv_heads", "head_dim", "window", "sinks", "q_stride",
+                 "k_stride", "v_stride", "o_stride", "k_cache_stride", "v_cache_stride")] + \
+               [("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
 
 
@@ -110,7 +142,14 @@ def lib() -> ctypes.CDLL:
         L.mamba3_linear_bwd.argtypes = [ld] + [vp] * 7 + [vp, sz, vp]
         L.mamba3_gated_ffn_fwd.argtypes = [ld] + [vp] * 5 + [vp, sz, vp]
         L.mamba3_gated_ffn_bwd.argtypes = [ld] + [vp] * 7 + [vp, sz, vp]
-        for name, dims in (("layer_norm_bwd", nd), ("linear_fwd", ld), ("linear_bwd", ld), ("gated_ffn_fwd", ld),
+        rd, ad, cd = ctypes.POINTER(NormRopeDims), ctypes.POINTER(AttnDims), ctypes.POINTER(AttnDecodeDims)
+        L.mamba3_qk_norm_rope_fwd.argtypes = [rd] + [vp] * 4 + [ctypes.c_float] + [vp] * 5
+        L.mamba3_qk_norm_rope_bwd.argtypes = [rd] + [vp] * 6 + [ctypes.c_float] + [vp] * 6 + [vp, sz, vp]
+        L.mamba3_window_attn_fwd.argtypes = [ad] + [vp] * 7
+        L.mamba3_window_attn_bwd.argtypes = [ad] + [vp] * 10 + [vp, sz, vp]
+        L.mamba3_window_attn_decode.argtypes = [cd] + [vp] * 7 + [vp, sz, vp]
+        for name, dims in (("qk_norm_rope_bwd", rd), ("window_attn_bwd", ad), ("window_attn_decode", cd),
+                           ("layer_norm_bwd", nd), ("linear_fwd", ld), ("linear_bwd", ld), ("gated_ffn_fwd", ld),
                            ("gated_ffn_bwd", ld)):
             query = getattr(L, f"mamba3_{name}_workspace_size")
             query.argtypes = [dims]
@@ -721,6 +760,309 @@ def mamba3_gated_ffn_bwd(x, W, dh, pre, *, act=M3_ACT_SILU, want_dx=True, want_d
                         workspace, stream)
 
 
+# ---------------------------------------------------------------------------
+# the attention layer beside the core: norms of queries and keys with their
+# rotation, windowed attention with sinks, the same over a cache
+# ---------------------------------------------------------------------------
+def _tokens(name, t, lead, heads, dim, dtype, device):
+    """(pointer, elements from token to token; 0: contiguous) of an operand
+    (*lead, heads, dim): contiguous, or with heads side by side and tokens
+    evenly further apart (a slice of the heads of a wider tensor)."""
+    if t.dtype is not dtype or t.device != device or t.shape != lead + (heads, dim):
+        _expect(name, t, lead + (heads, dim), dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    st, size = t.stride(), t.shape
+    if (dim == 1 or st[-1] == 1) and (heads == 1 or st[-2] == dim):
+        step = None  # elements between tokens; dimensions of one entry say nothing
+        inner = 1    # tokens that the dimensions looked at so far hold
+        for i in range(len(lead) - 1, -1, -1):
+            if size[i] != 1:
+                if step is None:
+                    step = st[i]
+                elif st[i] != inner * step:
+                    break
+            inner *= size[i]
+        else:
+            if step is None:
+                return t.data_ptr(), 0
+            if step >= heads * dim:
+                return t.data_ptr(), step
+    raise ValueError(f"{name}: must be contiguous, or with heads side by side and evenly spaced tokens")
+
+
+def _heads_of(name, t, least):
+    if t.dim() < least or t.shape[-1] == 0:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (..., heads, head_dim)")
+    return t.shape[:-2], t.shape[-2], t.shape[-1]
+
+
+def _norm_rope_operands(q, k, gain_q, gain_k, theta, pos):
+    """What both directions check of the operands they share."""
+    torch = _torch()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is required")
+    lead, _, D = _heads_of("q" if q is not None else "k", x, 3)
+    io, dev, f32 = x.dtype, x.device, torch.float32
+    rows = 1
+    for n in lead:
+        rows *= n
+    ops = []
+    for name, t in (("q", q), ("k", k)):
+        ops.append((None, 0, 0) if t is None else
+                   _tokens(name, t, lead, _heads_of(name, t, 3)[1], D, io, dev) + (t.shape[-2],))
+    pg = _vec("gain_q", gain_q, (D,), f32, dev), _vec("gain_k", gain_k, (D,), f32, dev)
+    rope = 0
+    if theta is not None:
+        rope = 2 * theta.numel()
+        if rope > D:
+            raise ValueError(f"theta: {theta.numel()} pairs, more than head_dim {D} holds")
+    pt = _vec("theta", theta, (rope // 2,), f32, dev)
+    pp = _vec("pos", pos, tuple(lead), torch.int64, dev)
+    return x, lead, D, io, dev, rows, ops, pg, rope, pt, pp
+
+
+def mamba3_qk_norm_rope_fwd(q, k, gain_q=None, gain_k=None, eps=1e-5, *, theta=None, pos=None, halves=False,
+                            q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q (..., L, q_heads, D) and k (..., L, k_heads, D),
+    gains (D) fp32, and the rotation of the first 2 * len(theta) entries by
+    pos theta (theta fp32; None: no rotation).  pos: (..., L) int64, or None: a
+    token's index along L.  halves: pairs are (j, j + len(theta)), else (2j, 2j + 1).
+    q and k may be slices of one projection's heads; either may be None.
+    Returns (q_out, k_out), which may be given (q and k themselves, too)."""
+    if stream is not None:
+        return _on_stream(stream, q if q is not None else k, mamba3_qk_norm_rope_fwd, q, k, gain_q, gain_k, eps,
+                          theta=theta, pos=pos, halves=halves, q_out=q_out, k_out=k_out)
+    x, lead, D, io, dev, rows, (oq, ok), (pgq, pgk), rope, pt, pp = _norm_rope_operands(q, k, gain_q, gain_k, theta, pos)
+    outs = []
+    for name, t, o, n in (("q_out", q, q_out, oq[2]), ("k_out", k, k_out, ok[2])):
+        if t is None:
+            outs.append((None, None, 0))
+        elif o is None:
+            o = x.new_empty(t.shape)
+            outs.append((o, o.data_ptr(), 0))
+        else:
+            outs.append((o,) + _tokens(name, o, lead, n, D, io, dev))
+    (q_out, pqo, sqo), (k_out, pko, sko) = outs
+    dims = NormRopeDims(rows, lead[-1], oq[2], ok[2], D, rope, oq[1], ok[1], sqo, sko, 0, 0, _io_code(x),
+                        M3_FLAG_ROPE_HALVES if halves else 0)
+    st = lib().mamba3_qk_norm_rope_fwd(dims, oq[0], ok[0], pgq, pgk, eps, pt, pp, pqo, pko, _raw_stream(dev))
+    _check(st, "mamba3_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_size(dims: NormRopeDims) -> int:
+    return int(lib().mamba3_qk_norm_rope_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def mamba3_qk_norm_rope_bwd(q, k, dq_out, dk_out, gain_q=None, gain_k=None, eps=1e-5, *, theta=None, pos=None,
+                            halves=False, want_dgain=True, dq=None, dk=None, dgain_q=None, dgain_k=None,
+                            workspace=None, stream=None):
+    """Backward of qk_norm_rope_fwd from its inputs and the gradients of its
+    results.  Returns a dict with dq, dk (io dtype; those of q and k that are
+    given) and, as wanted or given, dgain_q, dgain_k (fp32).  dq and dk may be
+    dq_out and dk_out themselves."""
+    if stream is not None:
+        return _on_stream(stream, q if q is not None else k, mamba3_qk_norm_rope_bwd, q, k, dq_out, dk_out, gain_q,
+                          gain_k, eps, theta=theta, pos=pos, halves=halves, want_dgain=want_dgain, dq=dq, dk=dk,
+                          dgain_q=dgain_q, dgain_k=dgain_k, workspace=workspace)
+    torch = _torch()
+    x, lead, D, io, dev, rows, (oq, ok), (pgq, pgk), rope, pt, pp = _norm_rope_operands(q, k, gain_q, gain_k, theta, pos)
+    out, ptrs = {}, []
+    for n, t, g, o, gain, heads in (("q", q, dq_out, dq, dgain_q, oq[2]), ("k", k, dk_out, dk, dgain_k, ok[2])):
+        if t is None:
+            ptrs.append((None, 0, None, 0, None))
+            continue
+        if g is None:
+            raise ValueError(f"d{n}_out is required with {n}")
+        pg, sg = _tokens(f"d{n}_out", g, lead, heads, D, io, dev)
+        if o is None:
+            o = x.new_empty(t.shape)
+            po, so = o.data_ptr(), 0
+        else:
+            po, so = _tokens(f"d{n}", o, lead, heads, D, io, dev)
+        out[f"d{n}"], pgain = o, None
+        if gain is not None:
+            out[f"dgain_{n}"], pgain = gain, _vec(f"dgain_{n}", gain, (D,), torch.float32, dev)
+        elif want_dgain:
+            out[f"dgain_{n}"] = gain = torch.empty(D, dtype=torch.float32, device=dev)
+            pgain = gain.data_ptr()
+        ptrs.append((pg, sg, po, so, pgain))
+    (pgq_, sgq, pdq, sdq, pnq), (pgk_, sgk, pdk, sdk, pnk) = ptrs
+    dims = NormRopeDims(rows, lead[-1], oq[2], ok[2], D, rope, oq[1], ok[1], sgq, sgk, sdq, sdk, _io_code(x),
+                        M3_FLAG_ROPE_HALVES if halves else 0)
+    L, pws, nws = lib(), None, 0
+    if pnq or pnk:
+        workspace, pws, nws = _workspace(L.mamba3_qk_norm_rope_bwd_workspace_size, dims, workspace, dev)
+    st = L.mamba3_qk_norm_rope_bwd(dims, oq[0], ok[0], pgq_, pgk_, pgq, pgk, eps, pt, pp, pdq, pdk, pnq, pnk, pws, nws,
+                                   _raw_stream(dev))
+    _check(st, "mamba3_qk_norm_rope_bwd")
+    return out
+
+
+def _attn_operands(q, k, v, starts, window, sinks, scale):
+    """Dims of a windowed attention (strides of q, k, v set), pointers of q, k, v, starts."""
+    torch = _torch()
+    lead, Hq, D = _heads_of("q", q, 3)
+    if k.dim() < 3:
+        raise ValueError(f"k: shape {tuple(k.shape)}, expected (..., heads, head_dim)")
+    klead, Hk = k.shape[:-2], k.shape[-2]
+    io, dev, kv_rows, ps = q.dtype, q.device, 0, None
+    if starts is not None:
+        if len(lead) != 1 or klead != lead:
+            raise ValueError("with starts, q, k and v are (tokens, heads, head_dim) of the same tokens")
+        if starts.dim() != 1 or starts.numel() < 1:
+            raise ValueError(f"starts: shape {tuple(starts.shape)}, expected (sequences + 1,)")
+        ps = _vec("starts", starts, starts.shape, torch.int64, dev)
+        batch, q_len, kv_len, rows = starts.numel() - 1, 0, 0, lead[0]
+        pk, sk = _tokens("k", k, klead, Hk, D, io, dev)
+        pv, sv = _tokens("v", v, klead, Hk, D, io, dev)
+    else:
+        if len(lead) != 2 or len(klead) != 2 or klead[0] != lead[0]:
+            raise ValueError("q is (batch, q_len, heads, head_dim), k and v (batch, kv_len, heads, head_dim)")
+        batch, q_len, kv_len, rows = lead[0], lead[1], klead[1], 0
+        (pk, sk, bk), (pv, sv, bv) = (_sequences(n, t, klead, Hk, D, io, dev) for n, t in (("k", k), ("v", v)))
+        if bk != bv:
+            raise ValueError("k and v must have as many rows from sequence to sequence")
+        kv_rows = bk
+    pq, sq = _tokens("q", q, lead, Hq, D, io, dev)
+    dims = AttnDims(batch, q_len, kv_len, rows, kv_rows, Hq, Hk, D, window, sinks, sq, sk, sv, 0, 0, 0, 0, 0,
+                    D ** -0.5 if scale is None else scale, _io_code(q), 0 if starts is None else M3_FLAG_PACKED, 0)
+    return dims, pq, pk, pv, ps
+
+
+def _sequences(name, t, lead, heads, dim, dtype, device):
+    """(pointer, elements from token to token, tokens from sequence to sequence;
+    0: the length) of keys (batch, length, heads, dim), which may be the first
+    tokens of longer sequences (a cache's)."""
+    if t.dim() == 4 and t.shape == lead + (heads, dim) and t.shape[0] > 1 and t.shape[1] > 0 and not t.is_contiguous():
+        step = t.stride(1) if t.shape[1] > 1 else heads * dim
+        if step > 0 and t.stride(0) % step == 0 and t.stride(0) // step > t.shape[1]:
+            p, s = _tokens(name, t[0], lead[1:], heads, dim, dtype, device)
+            return p, s, t.stride(0) // (s or heads * dim)
+    return _tokens(name, t, lead, heads, dim, dtype, device) + (0,)
+
+
+def mamba3_window_attn_fwd(q, k, v, *, window=0, sinks=0, scale=None, starts=None, o=None, lse=None, want_lse=False,
+                           stream=None):
+    """Causal attention of q (batch, q_len, q_heads, D) over k, v (batch, kv_len,
+    kv_heads, D): the queries are the last q_len of kv_len positions and see the
+    `window` last keys up to their own (0: all) and the first `sinks`.  starts
+    (sequences + 1, int64): packed sequences, q, k, v (tokens, heads, D).  scale:
+    of the scores, D^-1/2 by default.  k and v may be the first tokens of a
+    longer cache.  Returns (o, lse); lse (tokens, q_heads) fp32 with q's leading
+    shape (for the backward) is None unless wanted or given."""
+    if stream is not None:
+        return _on_stream(stream, q, mamba3_window_attn_fwd, q, k, v, window=window, sinks=sinks, scale=scale,
+                          starts=starts, o=o, lse=lse, want_lse=want_lse)
+    torch = _torch()
+    dims, pq, pk, pv, ps = _attn_operands(q, k, v, starts, window, sinks, scale)
+    lead, Hq, D, dev = q.shape[:-2], dims.q_heads, dims.head_dim, q.device
+    if o is None:
+        o = q.new_empty(q.shape)
+        po = o.data_ptr()
+    else:
+        po, dims.o_stride = _tokens("o", o, lead, Hq, D, q.dtype, dev)
+    pl = None
+    if lse is not None:
+        pl = _vec("lse", lse, lead + (Hq,), torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(lead + (Hq,), dtype=torch.float32, device=dev)
+        pl = lse.data_ptr()
+    st = lib().mamba3_window_attn_fwd(dims, pq, pk, pv, ps, po, pl, _raw_stream(dev))
+    _check(st, "mamba3_window_attn_fwd")
+    return o, lse
+
+
+def window_attn_bwd_workspace_size(dims: AttnDims) -> int:
+    return int(lib().mamba3_window_attn_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def mamba3_window_attn_bwd(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, starts=None, want_dq=True,
+                           want_dk=True, want_dv=True, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Backward of window_attn_fwd (the same q, k, v, window, sinks, scale,
+    starts; its o and lse).  Returns a dict with dq, dk, dv (io dtype), as
+    wanted.  With starts, gradients that the call makes itself hold nothing in
+    the rows of no sequence."""
+    if stream is not None:
+        return _on_stream(stream, q, mamba3_window_attn_bwd, q, k, v, o, lse, do, window=window, sinks=sinks,
+                          scale=scale, starts=starts, want_dq=want_dq, want_dk=want_dk, want_dv=want_dv, dq=dq, dk=dk,
+                          dv=dv, workspace=workspace)
+    torch = _torch()
+    dims, pq, pk, pv, ps = _attn_operands(q, k, v, starts, window, sinks, scale)
+    lead, Hq, Hk, D, io, dev = q.shape[:-2], dims.q_heads, dims.kv_heads, dims.head_dim, q.dtype, q.device
+    po, dims.o_stride = _tokens("o", o, lead, Hq, D, io, dev)
+    pdo, dims.do_stride = _tokens("do", do, lead, Hq, D, io, dev)
+    pl = _vec("lse", lse, lead + (Hq,), torch.float32, dev)
+    out, ptr = {}, {}
+    for n, t, given, want, heads in (("dq", q, dq, want_dq, Hq), ("dk", k, dk, want_dk, Hk), ("dv", v, dv, want_dv, Hk)):
+        ptr[n] = None
+        if given is not None:
+            ptr[n], step = _tokens(n, given, t.shape[:-2], heads, D, io, dev)
+            setattr(dims, n + "_stride", step)
+            out[n] = given
+        elif want:
+            out[n] = t.new_empty(t.shape)
+            ptr[n] = out[n].data_ptr()
+    if dims.kv_rows and (ptr["dk"] or ptr["dv"]):
+        raise ValueError("gradients of keys that are part of a longer cache: pass k and v as contiguous sequences")
+    L = lib()
+    workspace, pws, nws = _workspace(L.mamba3_window_attn_bwd_workspace_size, dims, workspace, dev)
+    st = L.mamba3_window_attn_bwd(dims, pq, pk, pv, po, pl, pdo, ps, ptr["dq"], ptr["dk"], ptr["dv"], pws, nws,
+                                  _raw_stream(dev))
+    _check(st, "mamba3_window_attn_bwd")
+    return out
+
+
+def window_attn_decode_workspace_size(dims: AttnDecodeDims) -> int:
+    return int(lib().mamba3_window_attn_decode_workspace_size(ctypes.byref(dims)))
+
+
+def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sinks=0, scale=None, o=None,
+                              workspace=None, stream=None):
+    """The T new tokens q (batch, T, q_heads, D), k, v (batch, T, kv_heads, D),
+    written to the caches (batch, capacity, kv_heads, D) in place and attending
+    over them.  lens (batch, int64): tokens in each cache before the call
+    (negative: an idle sequence).  Position p lies in slot p below `sinks`, else
+    in slot sinks + (p - sinks) mod (capacity - sinks) (window_cache_slots).
+    Returns o (batch, T, q_heads, D)."""
+    if stream is not None:
+        return _on_stream(stream, q, mamba3_window_attn_decode, q, k, v, k_cache, v_cache, lens, window=window,
+                          sinks=sinks, scale=scale, o=o, workspace=workspace)
+    torch = _torch()
+    if q.dim() != 4 or k.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q, k, v are (batch, tokens, heads, head_dim), the caches (batch, capacity, heads, head_dim)")
+    lead, Hq, D = _heads_of("q", q, 4)
+    B, T, Hk, C = lead[0], lead[1], k.shape[2], k_cache.shape[1]
+    io, dev = q.dtype, q.device
+    pq, sq = _tokens("q", q, lead, Hq, D, io, dev)
+    pk, sk = _tokens("k", k, lead, Hk, D, io, dev)
+    pv, sv = _tokens("v", v, lead, Hk, D, io, dev)
+    pkc, skc = _tokens("k_cache", k_cache, (B, C), Hk, D, io, dev)
+    pvc, svc = _tokens("v_cache", v_cache, (B, C), Hk, D, io, dev)
+    so = 0
+    if o is None:
+        o = q.new_empty(q.shape)
+        po = o.data_ptr()
+    else:
+        po, so = _tokens("o", o, lead, Hq, D, io, dev)
+    dims = AttnDecodeDims(B, T, C, Hq, Hk, D, window, sinks, sq, sk, sv, so, skc, svc,
+                          D ** -0.5 if scale is None else scale, _io_code(q), 0, 0)
+    L = lib()
+    workspace, pws, nws = _workspace(L.mamba3_window_attn_decode_workspace_size, dims, workspace, dev)
+    st = L.mamba3_window_attn_decode(dims, pq, pk, pv, pkc, pvc, _vec("lens", lens, (B,), torch.int64, dev), po, pws,
+                                     nws, _raw_stream(dev))
+    _check(st, "mamba3_window_attn_decode")
+    return o
+
+
+def window_cache_slots(pos, sinks, capacity):
+    """Slots of a cache of `capacity` slots where window_attn_decode keeps the
+    tokens at positions pos (an integer tensor): for filling one after a prefill."""
+    return _torch().where(pos < sinks, pos, sinks + (pos - sinks) % (capacity - sinks))
+
+
 chunked_fwd = mamba3_ssm_chunked_fwd
 chunked_fwd_noalloc = mamba3_ssm_chunked_fwd_noalloc
 chunked_bwd = mamba3_ssm_chunked_bwd
@@ -733,3 +1075,8 @@ linear_fwd = mamba3_linear_fwd
 linear_bwd = mamba3_linear_bwd
 gated_ffn_fwd = mamba3_gated_ffn_fwd
 gated_ffn_bwd = mamba3_gated_ffn_bwd
+qk_norm_rope_fwd = mamba3_qk_norm_rope_fwd
+qk_norm_rope_bwd = mamba3_qk_norm_rope_bwd
+window_attn_fwd = mamba3_window_attn_fwd
+window_attn_bwd = mamba3_window_attn_bwd
+window_attn_decode = mamba3_window_attn_decode

@@ -1,0 +1,231 @@
+"""Parity of windowed attention with sinks, forward and backward, with its fp64
+oracle (oracle/attention.py, pinned in tests/test_oracle_attention_pins.py).
+Needs an MI355X.  Every output entry is held to the oracle's bound for it."""
+import numpy as np
+import pytest
+
+from oracle import attention as oracle
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# half a step of the outputs' type, and of p and ds as the products take them
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from state_space_sequence_03_amd import ops as o
+    o.lib()
+    return o
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def draw(rng, shape, io, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).cuda().to(IO[io])
+
+
+def within(name, got, ref, bound):
+    got = host(got)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    with np.errstate(invalid="ignore"):
+        bad = ~((np.abs(got - ref) <= bound) | (got == ref))
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(f"{name}: {bad.sum()} of {bad.size} entries off, first {i}: {got[i]} against {ref[i]}, "
+                             f"bound {np.broadcast_to(bound, ref.shape)[i]}")
+
+
+def check_forward(io, o, lse, q, k, v, window, sinks, scale, what=""):
+    """One sequence's outputs against the oracle."""
+    u = HALF_STEP[io]
+    a = (host(q), host(k), host(v), window, sinks, scale)
+    for name, got, want, bound in zip(("o", "lse"), (o, lse), oracle.attention(*a), oracle.attention_bound(*a, u, u)):
+        within(f"{what} {name}", got, want, bound)
+
+
+def check_backward(io, grads, q, k, v, o, lse, do, window, sinks, scale, what=""):
+    u = HALF_STEP[io]
+    a = tuple(host(t) for t in (q, k, v, o, lse, do)) + (window, sinks, scale)
+    for name, got, want, bound in zip(("dq", "dk", "dv"), grads, oracle.attention_bwd(*a),
+                                      oracle.attention_bwd_bound(*a, u, u)):
+        within(f"{what} {name}", got, want, bound)
+
+
+# q_len, kv_len, q_heads, kv_heads, D, window, sinks
+SHAPES = [
+    (1, 1, 1, 1, 8, 0, 0), (5, 5, 2, 1, 24, 0, 0), (33, 33, 3, 3, 32, 7, 2), (64, 64, 4, 2, 64, 64, 1),
+    (65, 65, 2, 2, 72, 1, 0), (128, 128, 2, 1, 128, 0, 0), (129, 129, 6, 2, 96, 32, 5), (300, 300, 4, 1, 128, 40, 3),
+    (300, 300, 5, 5, 40, 64, 70), (257, 257, 2, 2, 64, 100, 300), (200, 450, 4, 2, 64, 60, 4), (1, 300, 8, 2, 128, 33, 1),
+    (17, 1000, 2, 1, 80, 0, 0), (450, 200, 2, 1, 64, 50, 3), (300, 40, 2, 2, 128, 0, 0), (700, 700, 2, 1, 64, 130, 130),
+    (1100, 1100, 2, 2, 64, 20, 4), (1500, 1500, 2, 1, 128, 100, 200), (1300, 1700, 1, 1, 32, 30, 1),
+]
+
+
+@pytest.mark.parametrize("n,m,Hq,Hk,D,window,sinks", SHAPES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_against_the_oracle(ops, io, n, m, Hq, Hk, D, window, sinks):
+    print(f"attention {io} {n} of {m}, heads {Hq}/{Hk} x {D}, window {window} sinks {sinks}", flush=True)
+    r = np.random.default_rng(n + m + D)
+    q, k, v, do = (draw(r, (2, l, h, D), io) for l, h in ((n, Hq), (m, Hk), (m, Hk), (n, Hq)))
+    scale = D ** -0.5
+    see = {"window": window, "sinks": sinks}
+    o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+    torch.cuda.synchronize()
+    for b in range(2):
+        check_forward(io, o[b], lse[b], q[b], k[b], v[b], window, sinks, float(np.float32(scale)), b)
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+    torch.cuda.synchronize()
+    assert set(g) == {"dq", "dk", "dv"}
+    for b in range(2):
+        check_backward(io, [g[x][b] for x in ("dq", "dk", "dv")], q[b], k[b], v[b], o[b], lse[b], do[b], window, sinks,
+                       float(np.float32(scale)), b)
+    # any subset of the gradients, and a forward without statistics: the same values
+    one = ops.window_attn_bwd(q, k, v, o, lse, do, want_dq=False, want_dk=False, **see)
+    assert set(one) == {"dv"} and torch.equal(one["dv"], g["dv"])
+    one = ops.window_attn_bwd(q, k, v, o, lse, do, want_dk=False, want_dv=False, **see)
+    assert set(one) == {"dq"} and torch.equal(one["dq"], g["dq"])
+    assert torch.equal(ops.window_attn_fwd(q, k, v, **see)[0], o)
+
+
+PACKED = [([1], 0, 0, 64), ([5, 1, 200, 64, 1], 50, 3, 64), ([130, 0, 0, 129, 128, 3], 0, 0, 128),
+          ([1] * 70 + [300] + [2] * 70, 40, 5, 32), ([1200, 7, 1030, 1024], 60, 2, 64), ([0, 0, 40], 9, 150, 72)]
+
+
+@pytest.mark.parametrize("lens,window,sinks,D", PACKED)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_packed_sequences(ops, io, lens, window, sinks, D):
+    # every sequence by itself, and the rows before the first and behind the last left as they were
+    print(f"packed {io} {len(lens)} sequences", flush=True)
+    Hq, Hk, before, behind = 4, 2, 3, 70
+    rows = before + sum(lens) + behind
+    r = np.random.default_rng(rows)
+    q, k, v, do = (draw(r, (rows, h, D), io) for h in (Hq, Hk, Hk, Hq))
+    ends = [before]
+    for n in lens:
+        ends.append(ends[-1] + n)
+    for t in (q, k, v, do):
+        t[:before] = t[ends[-1]:] = float("nan")
+    starts = torch.tensor(ends, device="cuda")
+    see = {"window": window, "sinks": sinks, "starts": starts, "scale": 0.25}
+    o, lse = torch.full_like(q, 5.0), torch.full((rows, Hq), 5.0, device="cuda")
+    ops.window_attn_fwd(q, k, v, o=o, lse=lse, **see)
+    out = {"dq": torch.full_like(q, 5.0), "dk": torch.full_like(k, 5.0), "dv": torch.full_like(v, 5.0)}
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, **see, **out)
+    torch.cuda.synchronize()
+    for a, b in zip(ends, ends[1:]):
+        if a < b:
+            s = slice(a, b)
+            check_forward(io, o[s], lse[s], q[s], k[s], v[s], window, sinks, 0.25, (a, b))
+            check_backward(io, [g[x][s] for x in ("dq", "dk", "dv")], q[s], k[s], v[s], o[s], lse[s], do[s], window, sinks,
+                           0.25, (a, b))
+    for t in (o, lse, g["dq"], g["dk"], g["dv"]):
+        assert bool((t[:before] == 5.0).all()) and bool((t[ends[-1]:] == 5.0).all())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_slices_of_a_projection(ops, io):
+    # q, k, v and their gradients as slices of rows of all heads, o beside something else
+    r = np.random.default_rng(11)
+    B, L, Hq, Hk, D = 2, 150, 4, 2, 64
+    qkv = draw(r, (B, L, Hq + 2 * Hk, D), io)
+    cut = lambda t: (t[:, :, :Hq], t[:, :, Hq:Hq + Hk], t[:, :, Hq + Hk:])
+    see = {"window": 60, "sinks": 2}
+    q, k, v = cut(qkv)
+    o, lse = ops.window_attn_fwd(*(t.contiguous() for t in (q, k, v)), want_lse=True, **see)
+    wide = torch.full((B, L, Hq + 1, D), float("nan"), dtype=IO[io], device="cuda")
+    ops.window_attn_fwd(q, k, v, o=wide[:, :, 1:], **see)
+    assert torch.equal(wide[:, :, 1:], o) and bool(wide[:, :, 0].isnan().all())
+    do = draw(r, (B, L, Hq, D), io)
+    g = ops.window_attn_bwd(*(t.contiguous() for t in (q, k, v)), o, lse, do, **see)
+    wide_do = torch.zeros((B, L, Hq + 1, D), dtype=IO[io], device="cuda")
+    wide_do[:, :, :Hq] = do
+    dqkv = torch.empty_like(qkv)
+    dq, dk, dv = cut(dqkv)
+    ops.window_attn_bwd(q, k, v, wide[:, :, 1:], lse, wide_do[:, :, :Hq], dq=dq, dk=dk, dv=dv, **see)
+    assert torch.equal(dqkv, torch.cat((g["dq"], g["dk"], g["dv"]), 2))
+
+
+def test_keys_of_a_longer_cache(ops):
+    # the first tokens of a cache as keys: what lies behind them is not read
+    r = np.random.default_rng(12)
+    cache = [draw(r, (3, 400, 2, 64), "bf16") for _ in range(2)]
+    for t in cache:
+        t[:, 210:] = float("nan")
+    q = draw(r, (3, 50, 4, 64), "bf16")
+    k, v = (t[:, :210] for t in cache)
+    want, _ = ops.window_attn_fwd(q, k.contiguous(), v.contiguous(), window=70, sinks=3)
+    got, _ = ops.window_attn_fwd(q, k, v, window=70, sinks=3)
+    assert torch.equal(got, want) and bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_large_scores(ops, io):
+    # softmaxes that are nearly one-hot, rising and falling along the keys; the
+    # running maximum moves by far more than what it is let behind by
+    r = np.random.default_rng(13)
+    L, D = 400, 64
+    q, v, do = (draw(r, (1, L, 2, D), io) for _ in range(3))
+    for ramp in (np.linspace(0.2, 12, L), np.linspace(12, 0.2, L)):
+        k = (draw(r, (1, L, 2, D), "f32") * torch.from_numpy(ramp.astype(np.float32)).cuda()[None, :, None, None]).to(IO[io])
+        o, lse = ops.window_attn_fwd(q, k, v, window=333, sinks=1, want_lse=True, scale=1.0)
+        check_forward(io, o[0], lse[0], q[0], k[0], v[0], 333, 1, 1.0)
+        g = ops.window_attn_bwd(q, k, v, o, lse, do, window=333, sinks=1, scale=1.0)
+        check_backward(io, [g[x][0] for x in ("dq", "dk", "dv")], q[0], k[0], v[0], o[0], lse[0], do[0], 333, 1, 1.0)
+
+
+def test_gradients_against_differences(ops):
+    # fp32: directional differences of the forward itself, in fp64 sums
+    r = np.random.default_rng(14)
+    L, D = 200, 32
+    q, k, v, do = (draw(r, (1, L, h, D), "f32") for h in (4, 2, 2, 4))
+    see = {"window": 50, "sinks": 2}
+    loss = lambda *a: float((ops.window_attn_fwd(*a, **see)[0].double() * do.double()).sum())
+    o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+    for i, n in enumerate(("dq", "dk", "dv")):
+        d = draw(r, tuple((q, k, v)[i].shape), "f32")
+        step = 2.0 ** -7
+        shifted = [[t + s * step * d if j == i else t for j, t in enumerate((q, k, v))] for s in (1, -1)]
+        quotient = (loss(*shifted[0]) - loss(*shifted[1])) / (2 * step)
+        slope = float((g[n].double() * d.double()).sum())
+        # the sums of both losses carry 25600 terms' fp32 errors of about 2e-7
+        # each: 25600^(1/2) 3e-7 / step = 6e-3; the third derivatives' part,
+        # step^2 / 6 of a slope's size, is 1e-5 of it
+        assert abs(quotient - slope) < 2e-2 + 1e-3 * abs(slope), (n, quotient, slope)
+
+
+def test_small_calls(ops):
+    empty = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")
+    o, lse = ops.window_attn_fwd(empty(0, 7, 2, 64), empty(0, 7, 1, 64), empty(0, 7, 1, 64), want_lse=True)
+    assert o.shape == (0, 7, 2, 64) and lse.shape == (0, 7, 2)
+    # no queries: keys still get their zero gradients; no keys: outputs are zero
+    k = torch.ones((2, 9, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q0 = empty(2, 0, 2, 64)
+    o, lse = ops.window_attn_fwd(q0, k, k, want_lse=True)
+    g = ops.window_attn_bwd(q0, k, k, o, lse, q0)
+    assert g["dq"].shape == q0.shape and not bool(g["dk"].any()) and not bool(g["dv"].any())
+    q = torch.ones((2, 9, 2, 64), dtype=torch.bfloat16, device="cuda")
+    k0 = empty(2, 0, 1, 64)
+    o, lse = ops.window_attn_fwd(q, k0, k0, want_lse=True)
+    assert not bool(o.any()) and bool((lse == -float("inf")).all())
+    assert not bool(ops.window_attn_bwd(q, k0, k0, o, lse, q)["dq"].any())
+
+
+def test_repeats_bit_for_bit(ops):
+    r = np.random.default_rng(15)
+    q, k, v, do = (draw(r, (2, 1400, h, 64), "bf16") for h in (8, 2, 2, 8))
+    see = {"window": 90, "sinks": 4}
+    o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+    for _ in range(3):
+        p, l = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+        assert torch.equal(p, o) and torch.equal(l, lse)
+        h = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+        assert all(torch.equal(h[n], g[n]) for n in g)
