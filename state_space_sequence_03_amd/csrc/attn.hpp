@@ -216,6 +216,29 @@ struct RowRegs {
   }
 };
 
+// The same for consecutive rows, which may be requested ahead of their use.
+template <typename T, int DP>
+struct RowStream {
+  static constexpr int KS = DP * io<T>::BYTES / 32;
+  uint4 v[KS];
+  int voff, ldb, last;  // last: chunks of a row past it do not exist
+  __device__ __forceinline__ void init(int64_t ld, int width, int lane) {
+    ldb = (int)(ld * io<T>::BYTES);
+    voff = (lane & 31) * ldb + (lane >> 5) * 16;
+    last = width * io<T>::BYTES / 16 - (lane >> 5);
+  }
+  // base: the first of `rows` rows (from 1, 32 at most); others read as zero
+  __device__ __forceinline__ void load(const char* base, int rows, int width) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)base, 0, (uint32_t)((rows - 1) * ldb + width * io<T>::BYTES), 0x00020000);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      v[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, 2 * s < last ? voff + s * 32 : kFar, 0, 0));
+#endif
+  }
+};
+
 // Step ks of a result (its rows 16 ks .. or 8 ks ..) as the operand that goes
 // with Tile::col.
 template <typename T>

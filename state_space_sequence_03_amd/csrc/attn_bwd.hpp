@@ -9,7 +9,8 @@
 
 namespace m3 {
 
-// lse in powers of two and delta, (heads, rows) each.  16 lanes per vector.
+// lse in powers of two and delta, (heads, rows) each, where no kernel of dq
+// takes them on its way.  16 lanes per vector.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a) {
   constexpr int V = io<T>::VEC;
@@ -96,6 +97,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, int64_t it
     if (r0 < piece * a.piece) r0 = piece * a.piece;
     if (r1 > piece * a.piece + a.piece - 1) r1 = piece * a.piece + a.piece - 1;
   }
+  r0 = r0 / BQ * BQ;  // whole tiles, so that a piece's last one ends with it
   const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, count = per * G;
 
   const int64_t row = s.k0 + (in ? j : s.nk - 1);
@@ -191,11 +193,10 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, int64_t it
   }
 }
 
-// The pieces of a sinks' tile joined in order; the blocks of a tile's pieces
-// share its elements.
+// The pieces of a sinks' tile joined in order, four entries to a thread; the
+// blocks of a tile's pieces share its entries.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  constexpr int ES = io<T>::BYTES;
   const int sunk = (a.sinks + 127) / 128;
   const int64_t hk = blockIdx.x % a.kv_heads, id = blockIdx.x / a.kv_heads;
   const int t = (int)(id % sunk);
@@ -208,19 +209,27 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int64_t step = (int64_t)sunk * a.kv_heads * 2 * 128 * a.dim;  // from piece to piece
   const float* part = a.part + (int64_t)blockIdx.x * 2 * 128 * a.dim - piece * step;
   const int n = keys * a.dim;
-  for (int e = piece * 256 + threadIdx.x; e < 2 * n; e += pieces * 256) {
-    const int which = e >= n, f = which ? e - n : e, j = f / a.dim, d = f - j * a.dim;
-    float x = 0.0f;
-    for (int i = 0; i < pieces; ++i) x += part[i * step + which * 128 * a.dim + f];
-    void* out = which ? a.dv : a.dk;
-    const int64_t row = s.k0 + t * 128 + j;
-    if (out) io<T>::store1(out, row * (which ? a.dv_stride : a.dk_stride) + hk * a.dim + d, x);
+  const bool key = blockIdx.y == 0;
+  void* out = key ? a.dk : a.dv;
+  if (!out) return;
+  if (!key) part += 128 * a.dim;
+  for (int e = (piece * 256 + (int)threadIdx.x) * 4; e < n; e += pieces * 1024) {
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const f32x4 y = *(const f32x4*)(part + i * step + e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] += y[j];
+    }
+    const int j = e / a.dim;
+    io<T>::store4(out, (s.k0 + t * 128 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, x);
   }
 }
 
 // dq of 128 queries: each wave holds 32 of them as the columns of its products
 // (scores = K q^T, dp = V do^T, dq^T += K^T ds) and walks the keys they see as
-// the forward does.
+// the forward does.  It comes first and leaves the queries' statistics to the
+// other kernel.
 template <typename T, int DP, int BN>
 __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, BN, 4>;
@@ -248,7 +257,26 @@ __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a, int64_t ite
   RowRegs<T, DP> q, y;
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
   y.load((const char*)a.dout + (row * a.do_stride + hq * a.dim) * ES, in, a.dim, h);
-  const float l2 = a.lse2[hq * a.rows + row], delta = a.delta[hq * a.rows + row];
+  float delta = 0.0f;
+  {
+    RowRegs<T, DP> o;
+    o.load((const char*)a.o + (row * a.o_stride + hq * a.dim) * ES, in, a.dim, h);
+#pragma unroll
+    for (int st = 0; st < RowRegs<T, DP>::KS; ++st) {
+      constexpr int V = io<T>::VEC;
+      float x[V], z[V];
+      io<T>::unpack(__builtin_bit_cast(typename io<T>::vec, o.v[st]), x);
+      io<T>::unpack(__builtin_bit_cast(typename io<T>::vec, y.v[st]), z);
+#pragma unroll
+      for (int e = 0; e < V; ++e) delta += x[e] * z[e];
+    }
+    delta = swap_sum32(delta);
+  }
+  const float lse = a.lse[row * a.q_heads + hq], l2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  if (in && h == 0) {
+    a.lse2[hq * a.rows + row] = l2;
+    a.delta[hq * a.rows + row] = delta;
+  }
 
   KV kt, vt;
   kt.init(a.k_stride, a.dim, lane, wave);
@@ -315,16 +343,16 @@ hipError_t attn_bwd_run(const AttnArgs& a, hipStream_t s) {
   constexpr int BN = io<T>::BYTES == 2 ? 64 : 32, BQ = BN;
   const dim3 block(256);
   const int64_t vectors = a.rows * a.q_heads, items = attn_items(a, false, 128), tiles = attn_items(a, true, 128);
-  if (vectors > 0)
+  if (a.dq && items > 0)
+    hipLaunchKernelGGL((attn_dq_kernel<T, DP, BN>), dim3((unsigned)(items * a.q_heads)), block, 0, s, a, items);
+  else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);
   if ((a.dk || a.dv) && tiles > 0) {
     const int64_t pieces = attn_pieces(a) * ((a.sinks + 127) / 128) * a.kv_heads;
     hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BQ>), dim3((unsigned)(pieces + tiles * a.kv_heads)), block, 0, s, a,
                        tiles, pieces);
-    if (pieces > 0) hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)pieces), block, 0, s, a);
+    if (pieces > 0) hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)pieces, 2), block, 0, s, a);
   }
-  if (a.dq && items > 0)
-    hipLaunchKernelGGL((attn_dq_kernel<T, DP, BN>), dim3((unsigned)(items * a.q_heads)), block, 0, s, a, items);
   return hipGetLastError();
 }
 

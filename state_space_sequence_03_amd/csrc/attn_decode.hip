@@ -7,16 +7,18 @@ namespace m3 {
 template hipError_t launch_attn_decode<bf16_t>(const AttnDecodeArgs&, hipStream_t);
 template hipError_t launch_attn_decode<float>(const AttnDecodeArgs&, hipStream_t);
 
-// Enough blocks for every CU, each wave with two tiles of 32 slots at least.
+// Enough blocks to fill the chip, each wave with two tiles of 32 slots at
+// least.
 int attn_decode_splits(int io_bf16, const AttnDecodeArgs& a) {
   const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
-  const int64_t blocks = a.batch * a.kv_heads * groups, waves = !io_bf16 && a.dim > 64 ? 2 : 4;
+  const int64_t blocks = a.batch * a.kv_heads * groups, room = 256 * (io_bf16 ? 2 : 1) * (a.dim <= 64 ? 2 : 1);
   int64_t slots = a.capacity;
   if (a.window < kNoWindow && slots > (int64_t)a.sinks + a.window + a.tokens - 1)
     slots = (int64_t)a.sinks + a.window + a.tokens - 1;
-  const int64_t most = (slots + 31) / 32 / (2 * waves), want = blocks > 0 ? (256 + blocks - 1) / blocks : 1;
-  const int64_t n = want < most ? want : most;
-  return n < 1 ? 1 : (int)n;
+  int64_t n = blocks > 0 ? (room + blocks - 1) / blocks : 1;
+  const int64_t most = (slots + 31) / 32 / 8;
+  n = n < most ? n : most;
+  return n < 1 ? 1 : n < kMaxSplits ? (int)n : kMaxSplits;
 }
 size_t attn_decode_part_bytes(const AttnDecodeArgs& a) {
   return a.splits == 1 ? 0 : (size_t)a.batch * a.tokens * a.q_heads * a.splits * (a.dim + 2) * 4;
@@ -27,7 +29,7 @@ size_t attn_decode_part_bytes(const AttnDecodeArgs& a) {
 int attn_bwd_piece(const AttnArgs& a) {
   int64_t n = (a.window < (1 << 24) ? a.window : 1 << 24) + 128;
   const int64_t work = a.rows * ((a.sinks + 127) / 128) * a.kv_heads;
-  if (n < 1024) n = 1024;
+  if (n < 256) n = 256;
   if (n < work / 1024) n = work / 1024;
   n = (n + 127) / 128 * 128;
   return (int)(n < (1 << 25) ? n : 1 << 25);

@@ -5,6 +5,8 @@
 
 namespace m3 {
 
+constexpr int kMaxSplits = 256;
+
 // The slots of a sequence's cache that its new tokens see, as two runs, and
 // the position that each holds.  Positions are taken relative to the first new
 // token's, n: those that matter lie within the cache's length of it.
@@ -66,18 +68,18 @@ struct CacheView {
 
 // A block takes the heads and tokens that share a head's keys, 32 at a time,
 // as the columns of its products, and a share of the slots they see; each wave
-// walks 32 slots at a time of its own, straight from memory into its part of
-// LDS, the next ones' while this one's products run, and needs no other wave
-// until the end, when the waves' results are joined.  The new tokens' keys and
+// walks 32 slots at a time of its own, keys from memory into registers and
+// values straight into its part of LDS, the next ones' while this one's products
+// run, and needs no other wave until the end, when the waves' results are joined.  The new tokens' keys and
 // values are written to the cache by the wave that then reads their slots.
 //
 // Bound by HBM: the slots seen are read once per 32 columns.
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs a) {
+template <typename T, int DP>
+__global__ __launch_bounds__(256, io<T>::BYTES == 2 ? 2 : 1) void attn_decode_kernel(AttnDecodeArgs a) {
   using KV = Tile<T, DP, 32, 1>;
-  constexpr int ES = io<T>::BYTES, STEPS = 32 / KV::CK, LD = DP + 4;
-  static_assert(32 * LD * 4 <= 4 * KV::BYTES, "a wave's result fits its part");
-  __shared__ __attribute__((aligned(1024))) char smem[NW * 4 * KV::BYTES];
+  constexpr int NW = 4, ES = io<T>::BYTES, STEPS = 32 / KV::CK, PART = 2 * KV::BYTES;
+  static_assert(32 * DP * 4 <= PART, "a wave's result fits its part");
+  __shared__ __attribute__((aligned(1024))) char smem[NW * PART];
   __shared__ float stat[NW][2][32];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -106,12 +108,13 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
     begin = (split * NW + wave) * per;
     end = begin + per < view.tiles() ? begin + per : view.tiles();
   }
-  KV kt, vt;
-  kt.init(a.kc_stride, a.dim, lane, 0);
+  KV vt;
+  RowStream<T, DP> kt;
+  kt.init(a.kc_stride, a.dim, lane);
   vt.init(a.vc_stride, a.dim, lane, 0);
   char* kc = (char*)a.k_cache + (b * a.capacity * a.kc_stride + hk * a.dim) * ES;
   char* vc = (char*)a.v_cache + (b * a.capacity * a.vc_stride + hk * a.dim) * ES;
-  char* mine = smem + wave * 4 * KV::BYTES;
+  char* mine = smem + wave * PART;
   auto load = [&](int i, int buf) {
     int x, e;
     view.tile(i, x, e);
@@ -133,8 +136,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
       __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores are done
       asm volatile("" ::: "memory");
     }
-    kt.load(kc + (int64_t)x * a.kc_stride * ES, e - x, a.dim, mine + buf * 2 * KV::BYTES, 0);
-    vt.load(vc + (int64_t)x * a.vc_stride * ES, e - x, a.dim, mine + (buf * 2 + 1) * KV::BYTES, 0);
+    kt.load(kc + (int64_t)x * a.kc_stride * ES, e - x, a.dim);
+    vt.load(vc + (int64_t)x * a.vc_stride * ES, e - x, a.dim, mine + buf * KV::BYTES, 0);
   };
   f32x16 acc[KV::CT];
 #pragma unroll
@@ -149,13 +152,16 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
+    uint4 k[KV::KS];
+#pragma unroll
+    for (int st = 0; st < KV::KS; ++st) k[st] = kt.v[st];
     if (i + 1 < end) load(i + 1, buf ^ 1);
-    const char* kl = mine + buf * 2 * KV::BYTES;
+    const char* vl = mine + buf * KV::BYTES;
     int x, e;
     view.tile(i, x, e);
     f32x16 sc = f32x16{};
 #pragma unroll
-    for (int st = 0; st < KV::KS; ++st) sc = mma32<T>(kt.row(kl, 0, st), q.v[st], sc);
+    for (int st = 0; st < KV::KS; ++st) sc = mma32<T>(k[st], q.v[st], sc);
     float z[16];
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
@@ -164,10 +170,10 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
     }
     soft.template step<16>(z, c, acc);
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      const uint4 w = result_step<T>(z, k);
+    for (int n = 0; n < STEPS; ++n) {
+      const uint4 w = result_step<T>(z, n);
 #pragma unroll
-      for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(vt.col(kl + KV::BYTES, d, k), w, acc[d]);
+      for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(vt.col(vl, d, n), w, acc[d]);
     }
   }
   // the waves' results: maximum, sum and unscaled output of each column
@@ -182,7 +188,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
   for (int d = 0; d < KV::CT; ++d)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *(f32x4*)(res + col * LD + d * 32 + 8 * i + 4 * h) =
+      *(f32x4*)(res + col * DP + (((d * 8 + 2 * i + h) ^ (col & 15)) << 2)) =
           f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
   __syncthreads();
   const int width = a.dim / 4, valid = cols - c0 < 32 ? cols - c0 : 32;
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
     for (int w = 0; w < NW; ++w) {
       const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[w][0][k] - m) * c);
       sum += f * stat[w][1][k];
-      const f32x4 x = *(const f32x4*)((const float*)(smem + w * 4 * KV::BYTES) + k * LD + d);
+      const f32x4 x = *(const f32x4*)((const float*)(smem + w * PART) + k * DP + (((d >> 2) ^ (k & 15)) << 2));
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] += f * x[j];
     }
@@ -219,47 +225,63 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_decode_kernel(AttnDecodeArgs 
   }
 }
 
-// The splits joined in order: a wave per row and head.
+// The splits joined in order: a block per row and head.  Lane i of every wave
+// takes the statistics of splits i, i + 64, ...; then eight groups of threads
+// each sum an eighth of the splits, four entries to a thread.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnDecodeArgs a) {
+  __shared__ float weight[kMaxSplits];
+  __shared__ f32x4 sums[8][32];
   const int lane = threadIdx.x & 63;
-  const int64_t all = a.batch * a.tokens * a.q_heads, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= all) return;
+  const int64_t all = a.batch * a.tokens * a.q_heads, id = blockIdx.x;
   const float* stat = a.part + all * a.splits * a.dim + 2 * id * a.splits;
   const float c = a.scale * kLog2e;
   float m = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, stat[2 * i]);
-  float o[2] = {0.0f, 0.0f}, sum = 0.0f;
-  const float* part = a.part + id * a.splits * a.dim;
-  const int d0 = lane < a.dim ? lane : 0, d1 = lane + 64 < a.dim ? lane + 64 : 0;
-#pragma unroll 4
-  for (int i = 0; i < a.splits; ++i) {
+  for (int i = lane; i < a.splits; i += 64) m = fmaxf(m, stat[2 * i]);
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o, 64));
+  float sum = 0.0f;
+  for (int i = lane; i < a.splits; i += 64) {
     const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[2 * i] - m) * c);
     sum += f * stat[2 * i + 1];
-    o[0] += f * part[i * a.dim + d0];
-    o[1] += f * part[i * a.dim + d1];
+    if (threadIdx.x < 64) weight[i] = f;
   }
+  sum = lane_sum<1, 64>(sum);
+  __syncthreads();
+  const int g = threadIdx.x >> 5, d = (threadIdx.x & 31) * 4;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (d < a.dim) {
+    const float* part = a.part + id * a.splits * a.dim + d;
+#pragma unroll 8
+    for (int i = g; i < a.splits; i += 8) {
+      const f32x4 x = *(const f32x4*)(part + (int64_t)i * a.dim);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] += weight[i] * x[j];
+    }
+  }
+  sums[g][threadIdx.x & 31] = o;
+  __syncthreads();
+  if (g != 0 || d >= a.dim) return;
+  float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] += sums[i][threadIdx.x & 31][j];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t row = id / a.q_heads, at = row * a.o_stride + (id - row * a.q_heads) * a.dim;
-  if (lane < a.dim) io<T>::store1(a.o, at + lane, o[0] * inv);
-  if (lane + 64 < a.dim) io<T>::store1(a.o, at + lane + 64, o[1] * inv);
-}
-
-template <typename T, int DP, int NW>
-void attn_decode_run(const AttnDecodeArgs& a, hipStream_t s) {
-  const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
-  hipLaunchKernelGGL((attn_decode_kernel<T, DP, NW>), dim3((unsigned)(a.batch * a.kv_heads * groups * a.splits)),
-                     dim3(64 * NW), 0, s, a);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] *= inv;
+  const int64_t row = id / a.q_heads;
+  io<T>::store4(a.o, row * a.o_stride + (id - row * a.q_heads) * a.dim + d, f);
 }
 
 template <typename T>
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s) {
-  if (a.dim <= 64) attn_decode_run<T, 64, 4>(a, s);
-  else attn_decode_run<T, 128, io<T>::BYTES == 2 ? 4 : 2>(a, s);
-  if (a.splits > 1) {
-    const int64_t rows = a.batch * a.tokens * a.q_heads;
-    hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
-  }
+  const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
+  const dim3 grid((unsigned)(a.batch * a.kv_heads * groups * a.splits)), block(256);
+  if (a.dim <= 64) hipLaunchKernelGGL((attn_decode_kernel<T, 64>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_decode_kernel<T, 128>), grid, block, 0, s, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)(a.batch * a.tokens * a.q_heads)), block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -764,29 +764,29 @@ def mamba3_gated_ffn_bwd(x, W, dh, pre, *, act=M3_ACT_SILU, want_dx=True, want_d
 # the attention layer beside the core: norms of queries and keys with their
 # rotation, windowed attention with sinks, the same over a cache
 # ---------------------------------------------------------------------------
-def _tokens(name, t, lead, heads, dim, dtype, device):
-    """(pointer, elements from token to token; 0: contiguous) of an operand
-    (*lead, heads, dim): contiguous, or with heads side by side and tokens
-    evenly further apart (a slice of the heads of a wider tensor)."""
-    if t.dtype is not dtype or t.device != device or t.shape != lead + (heads, dim):
-        _expect(name, t, lead + (heads, dim), dtype, device)
+def _tokens(name, t, shape, dtype, device):
+    """(pointer, elements from token to token; 0: contiguous) of an operand of
+    the given shape (..., heads, dim): contiguous, or with heads side by side
+    and tokens evenly further apart (a slice of the heads of a wider tensor)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _expect(name, t, shape, dtype, device)
     if t.is_contiguous():
         return t.data_ptr(), 0
-    st, size = t.stride(), t.shape
+    st = t.stride()
+    heads, dim = shape[-2:]
     if (dim == 1 or st[-1] == 1) and (heads == 1 or st[-2] == dim):
-        step = None  # elements between tokens; dimensions of one entry say nothing
-        inner = 1    # tokens that the dimensions looked at so far hold
-        for i in range(len(lead) - 1, -1, -1):
-            if size[i] != 1:
-                if step is None:
+        step = 0    # elements between tokens; dimensions of one entry say nothing
+        inner = 1   # tokens that the dimensions looked at so far hold
+        for i in range(len(shape) - 3, -1, -1):
+            n = shape[i]
+            if n != 1:
+                if step == 0:
                     step = st[i]
                 elif st[i] != inner * step:
                     break
-            inner *= size[i]
+                inner *= n
         else:
-            if step is None:
-                return t.data_ptr(), 0
-            if step >= heads * dim:
+            if step == 0 or step >= heads * dim:
                 return t.data_ptr(), step
     raise ValueError(f"{name}: must be contiguous, or with heads side by side and evenly spaced tokens")
 
@@ -797,30 +797,47 @@ def _heads_of(name, t, least):
     return t.shape[:-2], t.shape[-2], t.shape[-1]
 
 
-def _norm_rope_operands(q, k, gain_q, gain_k, theta, pos):
-    """What both directions check of the operands they share."""
+def _norm_rope_dims(q, k, gain_q, gain_k, theta, pos, halves):
+    """What both directions check of the operands they share: dims (the strides
+    of what is not shared left 0), shapes of q and k, pointers of q, k, the
+    gains, theta and pos, type, device."""
     torch = _torch()
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is required")
-    lead, _, D = _heads_of("q" if q is not None else "k", x, 3)
     io, dev, f32 = x.dtype, x.device, torch.float32
+    lead, Hq, D = _heads_of("q" if q is not None else "k", x, 3)
+    qs = ks = pq = pk = None
+    sq = sk = Hk = 0
+    if q is not None:
+        qs = q.shape
+        pq, sq = _tokens("q", q, qs, io, dev)
+    else:
+        Hq = 0
+    if k is not None:
+        ks = k.shape
+        if len(ks) != len(lead) + 2 or ks[:-2] != lead or ks[-1] != D:
+            raise ValueError(f"k: shape {tuple(ks)}, expected {tuple(lead)} tokens of heads of {D}")
+        Hk = ks[-2]
+        pk, sk = _tokens("k", k, ks, io, dev)
+    rope = 0
+    if theta is not None:
+        rope = 2 * theta.shape[0] if theta.dim() == 1 else -1
+        if not 0 <= rope <= D:
+            raise ValueError(f"theta: shape {tuple(theta.shape)}, expected at most (head_dim / 2,) = ({D // 2},)")
+        theta = _vec("theta", theta, (rope // 2,), f32, dev)
+    if pos is not None:
+        pos = _vec("pos", pos, lead, torch.int64, dev)
     rows = 1
     for n in lead:
         rows *= n
-    ops = []
-    for name, t in (("q", q), ("k", k)):
-        ops.append((None, 0, 0) if t is None else
-                   _tokens(name, t, lead, _heads_of(name, t, 3)[1], D, io, dev) + (t.shape[-2],))
-    pg = _vec("gain_q", gain_q, (D,), f32, dev), _vec("gain_k", gain_k, (D,), f32, dev)
-    rope = 0
-    if theta is not None:
-        rope = 2 * theta.numel()
-        if rope > D:
-            raise ValueError(f"theta: {theta.numel()} pairs, more than head_dim {D} holds")
-    pt = _vec("theta", theta, (rope // 2,), f32, dev)
-    pp = _vec("pos", pos, tuple(lead), torch.int64, dev)
-    return x, lead, D, io, dev, rows, ops, pg, rope, pt, pp
+    if gain_q is not None:
+        gain_q = _vec("gain_q", gain_q, (D,), f32, dev)
+    if gain_k is not None:
+        gain_k = _vec("gain_k", gain_k, (D,), f32, dev)
+    dims = NormRopeDims(rows, lead[-1], Hq, Hk, D, rope, sq, sk, 0, 0, 0, 0, _io_code(x),
+                        M3_FLAG_ROPE_HALVES if halves else 0)
+    return dims, qs, ks, (pq, pk, gain_q, gain_k, theta, pos), io, dev
 
 
 def mamba3_qk_norm_rope_fwd(q, k, gain_q=None, gain_k=None, eps=1e-5, *, theta=None, pos=None, halves=False,
@@ -834,20 +851,23 @@ def mamba3_qk_norm_rope_fwd(q, k, gain_q=None, gain_k=None, eps=1e-5, *, theta=N
     if stream is not None:
         return _on_stream(stream, q if q is not None else k, mamba3_qk_norm_rope_fwd, q, k, gain_q, gain_k, eps,
                           theta=theta, pos=pos, halves=halves, q_out=q_out, k_out=k_out)
-    x, lead, D, io, dev, rows, (oq, ok), (pgq, pgk), rope, pt, pp = _norm_rope_operands(q, k, gain_q, gain_k, theta, pos)
-    outs = []
-    for name, t, o, n in (("q_out", q, q_out, oq[2]), ("k_out", k, k_out, ok[2])):
-        if t is None:
-            outs.append((None, None, 0))
-        elif o is None:
-            o = x.new_empty(t.shape)
-            outs.append((o, o.data_ptr(), 0))
-        else:
-            outs.append((o,) + _tokens(name, o, lead, n, D, io, dev))
-    (q_out, pqo, sqo), (k_out, pko, sko) = outs
-    dims = NormRopeDims(rows, lead[-1], oq[2], ok[2], D, rope, oq[1], ok[1], sqo, sko, 0, 0, _io_code(x),
-                        M3_FLAG_ROPE_HALVES if halves else 0)
-    st = lib().mamba3_qk_norm_rope_fwd(dims, oq[0], ok[0], pgq, pgk, eps, pt, pp, pqo, pko, _raw_stream(dev))
+    dims, qs, ks, (pq, pk, pgq, pgk, pt, pp), io, dev = _norm_rope_dims(q, k, gain_q, gain_k, theta, pos, halves)
+    pqo = pko = None
+    if qs is None:
+        q_out = None
+    elif q_out is None:
+        q_out = q.new_empty(qs)
+        pqo = q_out.data_ptr()
+    else:
+        pqo, dims.q_out_stride = _tokens("q_out", q_out, qs, io, dev)
+    if ks is None:
+        k_out = None
+    elif k_out is None:
+        k_out = k.new_empty(ks)
+        pko = k_out.data_ptr()
+    else:
+        pko, dims.k_out_stride = _tokens("k_out", k_out, ks, io, dev)
+    st = lib().mamba3_qk_norm_rope_fwd(dims, pq, pk, pgq, pgk, eps, pt, pp, pqo, pko, _raw_stream(dev))
     _check(st, "mamba3_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -867,81 +887,85 @@ def mamba3_qk_norm_rope_bwd(q, k, dq_out, dk_out, gain_q=None, gain_k=None, eps=
         return _on_stream(stream, q if q is not None else k, mamba3_qk_norm_rope_bwd, q, k, dq_out, dk_out, gain_q,
                           gain_k, eps, theta=theta, pos=pos, halves=halves, want_dgain=want_dgain, dq=dq, dk=dk,
                           dgain_q=dgain_q, dgain_k=dgain_k, workspace=workspace)
-    torch = _torch()
-    x, lead, D, io, dev, rows, (oq, ok), (pgq, pgk), rope, pt, pp = _norm_rope_operands(q, k, gain_q, gain_k, theta, pos)
-    out, ptrs = {}, []
-    for n, t, g, o, gain, heads in (("q", q, dq_out, dq, dgain_q, oq[2]), ("k", k, dk_out, dk, dgain_k, ok[2])):
-        if t is None:
-            ptrs.append((None, 0, None, 0, None))
-            continue
-        if g is None:
-            raise ValueError(f"d{n}_out is required with {n}")
-        pg, sg = _tokens(f"d{n}_out", g, lead, heads, D, io, dev)
-        if o is None:
-            o = x.new_empty(t.shape)
-            po, so = o.data_ptr(), 0
+    dims, qs, ks, (pq, pk, pgq, pgk, pt, pp), io, dev = _norm_rope_dims(q, k, gain_q, gain_k, theta, pos, halves)
+    f32, D, out = _torch().float32, dims.head_dim, {}
+    pdqo = pdko = pdq = pdk = pnq = pnk = pws = None
+    nws = 0
+    if qs is not None:
+        if dq_out is None:
+            raise ValueError("dq_out is required with q")
+        pdqo, dims.q_out_stride = _tokens("dq_out", dq_out, qs, io, dev)
+        if dq is None:
+            dq = q.new_empty(qs)
+            pdq = dq.data_ptr()
         else:
-            po, so = _tokens(f"d{n}", o, lead, heads, D, io, dev)
-        out[f"d{n}"], pgain = o, None
-        if gain is not None:
-            out[f"dgain_{n}"], pgain = gain, _vec(f"dgain_{n}", gain, (D,), torch.float32, dev)
-        elif want_dgain:
-            out[f"dgain_{n}"] = gain = torch.empty(D, dtype=torch.float32, device=dev)
-            pgain = gain.data_ptr()
-        ptrs.append((pg, sg, po, so, pgain))
-    (pgq_, sgq, pdq, sdq, pnq), (pgk_, sgk, pdk, sdk, pnk) = ptrs
-    dims = NormRopeDims(rows, lead[-1], oq[2], ok[2], D, rope, oq[1], ok[1], sgq, sgk, sdq, sdk, _io_code(x),
-                        M3_FLAG_ROPE_HALVES if halves else 0)
-    L, pws, nws = lib(), None, 0
+            pdq, dims.dq_stride = _tokens("dq", dq, qs, io, dev)
+        out["dq"] = dq
+        if dgain_q is not None or want_dgain:
+            if dgain_q is None:
+                dgain_q = q.new_empty(D, dtype=f32)
+            out["dgain_q"], pnq = dgain_q, _vec("dgain_q", dgain_q, (D,), f32, dev)
+    if ks is not None:
+        if dk_out is None:
+            raise ValueError("dk_out is required with k")
+        pdko, dims.k_out_stride = _tokens("dk_out", dk_out, ks, io, dev)
+        if dk is None:
+            dk = k.new_empty(ks)
+            pdk = dk.data_ptr()
+        else:
+            pdk, dims.dk_stride = _tokens("dk", dk, ks, io, dev)
+        out["dk"] = dk
+        if dgain_k is not None or want_dgain:
+            if dgain_k is None:
+                dgain_k = k.new_empty(D, dtype=f32)
+            out["dgain_k"], pnk = dgain_k, _vec("dgain_k", dgain_k, (D,), f32, dev)
+    L = lib()
     if pnq or pnk:
         workspace, pws, nws = _workspace(L.mamba3_qk_norm_rope_bwd_workspace_size, dims, workspace, dev)
-    st = L.mamba3_qk_norm_rope_bwd(dims, oq[0], ok[0], pgq_, pgk_, pgq, pgk, eps, pt, pp, pdq, pdk, pnq, pnk, pws, nws,
+    st = L.mamba3_qk_norm_rope_bwd(dims, pq, pk, pdqo, pdko, pgq, pgk, eps, pt, pp, pdq, pdk, pnq, pnk, pws, nws,
                                    _raw_stream(dev))
     _check(st, "mamba3_qk_norm_rope_bwd")
     return out
 
 
-def _attn_operands(q, k, v, starts, window, sinks, scale):
-    """Dims of a windowed attention (strides of q, k, v set), pointers of q, k, v, starts."""
-    torch = _torch()
+def _attn_dims(q, k, v, starts, window, sinks, scale):
+    """Dims of a windowed attention (strides of q, k, v set), pointers of q, k, v
+    and starts, shapes of q and k, type, device."""
+    io, dev, ps, rows, kv_rows, flags = q.dtype, q.device, None, 0, 0, 0
+    qs, ks = q.shape, k.shape
     lead, Hq, D = _heads_of("q", q, 3)
-    if k.dim() < 3:
-        raise ValueError(f"k: shape {tuple(k.shape)}, expected (..., heads, head_dim)")
-    klead, Hk = k.shape[:-2], k.shape[-2]
-    io, dev, kv_rows, ps = q.dtype, q.device, 0, None
-    if starts is not None:
-        if len(lead) != 1 or klead != lead:
-            raise ValueError("with starts, q, k and v are (tokens, heads, head_dim) of the same tokens")
-        if starts.dim() != 1 or starts.numel() < 1:
-            raise ValueError(f"starts: shape {tuple(starts.shape)}, expected (sequences + 1,)")
-        ps = _vec("starts", starts, starts.shape, torch.int64, dev)
-        batch, q_len, kv_len, rows = starts.numel() - 1, 0, 0, lead[0]
-        pk, sk = _tokens("k", k, klead, Hk, D, io, dev)
-        pv, sv = _tokens("v", v, klead, Hk, D, io, dev)
-    else:
-        if len(lead) != 2 or len(klead) != 2 or klead[0] != lead[0]:
+    pq, sq = _tokens("q", q, qs, io, dev)
+    if starts is None:
+        if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[3] != D:
             raise ValueError("q is (batch, q_len, heads, head_dim), k and v (batch, kv_len, heads, head_dim)")
-        batch, q_len, kv_len, rows = lead[0], lead[1], klead[1], 0
-        (pk, sk, bk), (pv, sv, bv) = (_sequences(n, t, klead, Hk, D, io, dev) for n, t in (("k", k), ("v", v)))
-        if bk != bv:
+        batch, q_len, kv_len = qs[0], qs[1], ks[1]
+        (pk, sk, kv_rows), (pv, sv, rv) = _sequences("k", k, ks, io, dev), _sequences("v", v, ks, io, dev)
+        if kv_rows != rv:
             raise ValueError("k and v must have as many rows from sequence to sequence")
-        kv_rows = bk
-    pq, sq = _tokens("q", q, lead, Hq, D, io, dev)
-    dims = AttnDims(batch, q_len, kv_len, rows, kv_rows, Hq, Hk, D, window, sinks, sq, sk, sv, 0, 0, 0, 0, 0,
-                    D ** -0.5 if scale is None else scale, _io_code(q), 0 if starts is None else M3_FLAG_PACKED, 0)
-    return dims, pq, pk, pv, ps
+    else:
+        if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != D:
+            raise ValueError("with starts, q, k and v are (tokens, heads, head_dim) of the same tokens")
+        if starts.dim() != 1 or starts.shape[0] < 1:
+            raise ValueError(f"starts: shape {tuple(starts.shape)}, expected (sequences + 1,)")
+        ps = _vec("starts", starts, starts.shape, _torch().int64, dev)
+        batch, q_len, kv_len, rows, flags = starts.shape[0] - 1, 0, 0, qs[0], M3_FLAG_PACKED
+        (pk, sk), (pv, sv) = _tokens("k", k, ks, io, dev), _tokens("v", v, ks, io, dev)
+    dims = AttnDims(batch, q_len, kv_len, rows, kv_rows, Hq, ks[-2], D, window, sinks, sq, sk, sv, 0, 0, 0, 0, 0,
+                    D ** -0.5 if scale is None else scale, _io_code(q), flags, 0)
+    return dims, (pq, pk, pv, ps), qs, ks, io, dev
 
 
-def _sequences(name, t, lead, heads, dim, dtype, device):
+def _sequences(name, t, shape, dtype, device):
     """(pointer, elements from token to token, tokens from sequence to sequence;
     0: the length) of keys (batch, length, heads, dim), which may be the first
     tokens of longer sequences (a cache's)."""
-    if t.dim() == 4 and t.shape == lead + (heads, dim) and t.shape[0] > 1 and t.shape[1] > 0 and not t.is_contiguous():
-        step = t.stride(1) if t.shape[1] > 1 else heads * dim
-        if step > 0 and t.stride(0) % step == 0 and t.stride(0) // step > t.shape[1]:
-            p, s = _tokens(name, t[0], lead[1:], heads, dim, dtype, device)
-            return p, s, t.stride(0) // (s or heads * dim)
-    return _tokens(name, t, lead, heads, dim, dtype, device) + (0,)
+    if not t.is_contiguous() and t.shape == shape and shape[0] > 1 and shape[1] > 0:
+        row, between = shape[2] * shape[3], t.stride(0)
+        step = t.stride(1) if shape[1] > 1 else row
+        if step > 0 and between % step == 0 and between // step > shape[1]:
+            p, s = _tokens(name, t[0], shape[1:], dtype, device)
+            return p, s, between // (s or row)
+    return _tokens(name, t, shape, dtype, device) + (0,)
 
 
 def mamba3_window_attn_fwd(q, k, v, *, window=0, sinks=0, scale=None, starts=None, o=None, lse=None, want_lse=False,
@@ -956,19 +980,17 @@ def mamba3_window_attn_fwd(q, k, v, *, window=0, sinks=0, scale=None, starts=Non
     if stream is not None:
         return _on_stream(stream, q, mamba3_window_attn_fwd, q, k, v, window=window, sinks=sinks, scale=scale,
                           starts=starts, o=o, lse=lse, want_lse=want_lse)
-    torch = _torch()
-    dims, pq, pk, pv, ps = _attn_operands(q, k, v, starts, window, sinks, scale)
-    lead, Hq, D, dev = q.shape[:-2], dims.q_heads, dims.head_dim, q.device
+    dims, (pq, pk, pv, ps), qs, _, io, dev = _attn_dims(q, k, v, starts, window, sinks, scale)
     if o is None:
-        o = q.new_empty(q.shape)
+        o = q.new_empty(qs)
         po = o.data_ptr()
     else:
-        po, dims.o_stride = _tokens("o", o, lead, Hq, D, q.dtype, dev)
+        po, dims.o_stride = _tokens("o", o, qs, io, dev)
     pl = None
     if lse is not None:
-        pl = _vec("lse", lse, lead + (Hq,), torch.float32, dev)
+        pl = _vec("lse", lse, qs[:-1], _torch().float32, dev)
     elif want_lse:
-        lse = torch.empty(lead + (Hq,), dtype=torch.float32, device=dev)
+        lse = q.new_empty(qs[:-1], dtype=_torch().float32)
         pl = lse.data_ptr()
     st = lib().mamba3_window_attn_fwd(dims, pq, pk, pv, ps, po, pl, _raw_stream(dev))
     _check(st, "mamba3_window_attn_fwd")
@@ -989,28 +1011,33 @@ def mamba3_window_attn_bwd(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None
         return _on_stream(stream, q, mamba3_window_attn_bwd, q, k, v, o, lse, do, window=window, sinks=sinks,
                           scale=scale, starts=starts, want_dq=want_dq, want_dk=want_dk, want_dv=want_dv, dq=dq, dk=dk,
                           dv=dv, workspace=workspace)
-    torch = _torch()
-    dims, pq, pk, pv, ps = _attn_operands(q, k, v, starts, window, sinks, scale)
-    lead, Hq, Hk, D, io, dev = q.shape[:-2], dims.q_heads, dims.kv_heads, dims.head_dim, q.dtype, q.device
-    po, dims.o_stride = _tokens("o", o, lead, Hq, D, io, dev)
-    pdo, dims.do_stride = _tokens("do", do, lead, Hq, D, io, dev)
-    pl = _vec("lse", lse, lead + (Hq,), torch.float32, dev)
-    out, ptr = {}, {}
-    for n, t, given, want, heads in (("dq", q, dq, want_dq, Hq), ("dk", k, dk, want_dk, Hk), ("dv", v, dv, want_dv, Hk)):
-        ptr[n] = None
-        if given is not None:
-            ptr[n], step = _tokens(n, given, t.shape[:-2], heads, D, io, dev)
-            setattr(dims, n + "_stride", step)
-            out[n] = given
-        elif want:
-            out[n] = t.new_empty(t.shape)
-            ptr[n] = out[n].data_ptr()
-    if dims.kv_rows and (ptr["dk"] or ptr["dv"]):
+    dims, (pq, pk, pv, ps), qs, ks, io, dev = _attn_dims(q, k, v, starts, window, sinks, scale)
+    po, dims.o_stride = _tokens("o", o, qs, io, dev)
+    pdo, dims.do_stride = _tokens("do", do, qs, io, dev)
+    pl = _vec("lse", lse, qs[:-1], _torch().float32, dev)
+    if pl is None:
+        raise ValueError("lse is required (the forward's want_lse)")
+    out, pdq, pdk, pdv = {}, None, None, None
+    if dq is not None:
+        out["dq"], (pdq, dims.dq_stride) = dq, _tokens("dq", dq, qs, io, dev)
+    elif want_dq:
+        out["dq"] = dq = q.new_empty(qs)
+        pdq = dq.data_ptr()
+    if dk is not None:
+        out["dk"], (pdk, dims.dk_stride) = dk, _tokens("dk", dk, ks, io, dev)
+    elif want_dk:
+        out["dk"] = dk = q.new_empty(ks)
+        pdk = dk.data_ptr()
+    if dv is not None:
+        out["dv"], (pdv, dims.dv_stride) = dv, _tokens("dv", dv, ks, io, dev)
+    elif want_dv:
+        out["dv"] = dv = q.new_empty(ks)
+        pdv = dv.data_ptr()
+    if dims.kv_rows and (dk is not None or dv is not None):
         raise ValueError("gradients of keys that are part of a longer cache: pass k and v as contiguous sequences")
     L = lib()
     workspace, pws, nws = _workspace(L.mamba3_window_attn_bwd_workspace_size, dims, workspace, dev)
-    st = L.mamba3_window_attn_bwd(dims, pq, pk, pv, po, pl, pdo, ps, ptr["dq"], ptr["dk"], ptr["dv"], pws, nws,
-                                  _raw_stream(dev))
+    st = L.mamba3_window_attn_bwd(dims, pq, pk, pv, po, pl, pdo, ps, pdq, pdk, pdv, pws, nws, _raw_stream(dev))
     _check(st, "mamba3_window_attn_bwd")
     return out
 
@@ -1030,29 +1057,29 @@ def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sink
     if stream is not None:
         return _on_stream(stream, q, mamba3_window_attn_decode, q, k, v, k_cache, v_cache, lens, window=window,
                           sinks=sinks, scale=scale, o=o, workspace=workspace)
-    torch = _torch()
-    if q.dim() != 4 or k.dim() != 4 or k_cache.dim() != 4:
-        raise ValueError("q, k, v are (batch, tokens, heads, head_dim), the caches (batch, capacity, heads, head_dim)")
-    lead, Hq, D = _heads_of("q", q, 4)
-    B, T, Hk, C = lead[0], lead[1], k.shape[2], k_cache.shape[1]
-    io, dev = q.dtype, q.device
-    pq, sq = _tokens("q", q, lead, Hq, D, io, dev)
-    pk, sk = _tokens("k", k, lead, Hk, D, io, dev)
-    pv, sv = _tokens("v", v, lead, Hk, D, io, dev)
-    pkc, skc = _tokens("k_cache", k_cache, (B, C), Hk, D, io, dev)
-    pvc, svc = _tokens("v_cache", v_cache, (B, C), Hk, D, io, dev)
+    io, dev, qs, ks, cs = q.dtype, q.device, q.shape, k.shape, k_cache.shape
+    if len(qs) != 4 or len(ks) != 4 or len(cs) != 4 or ks[:2] != qs[:2] or cs[0] != qs[0] or cs[2:] != ks[2:]:
+        raise ValueError("q, k, v are (batch, tokens, heads, head_dim), the caches (batch, capacity, heads of k, head_dim)")
+    _, Hq, D = _heads_of("q", q, 4)
+    pq, sq = _tokens("q", q, qs, io, dev)
+    if ks[3] != D:
+        raise ValueError(f"k: head_dim {ks[3]}, expected {D}")
+    pk, sk = _tokens("k", k, ks, io, dev)
+    pv, sv = _tokens("v", v, ks, io, dev)
+    pkc, skc = _tokens("k_cache", k_cache, cs, io, dev)
+    pvc, svc = _tokens("v_cache", v_cache, cs, io, dev)
     so = 0
     if o is None:
-        o = q.new_empty(q.shape)
+        o = q.new_empty(qs)
         po = o.data_ptr()
     else:
-        po, so = _tokens("o", o, lead, Hq, D, io, dev)
-    dims = AttnDecodeDims(B, T, C, Hq, Hk, D, window, sinks, sq, sk, sv, so, skc, svc,
+        po, so = _tokens("o", o, qs, io, dev)
+    dims = AttnDecodeDims(qs[0], qs[1], cs[1], Hq, ks[2], D, window, sinks, sq, sk, sv, so, skc, svc,
                           D ** -0.5 if scale is None else scale, _io_code(q), 0, 0)
     L = lib()
     workspace, pws, nws = _workspace(L.mamba3_window_attn_decode_workspace_size, dims, workspace, dev)
-    st = L.mamba3_window_attn_decode(dims, pq, pk, pv, pkc, pvc, _vec("lens", lens, (B,), torch.int64, dev), po, pws,
-                                     nws, _raw_stream(dev))
+    st = L.mamba3_window_attn_decode(dims, pq, pk, pv, pkc, pvc, _vec("lens", lens, qs[:1], _torch().int64, dev), po,
+                                     pws, nws, _raw_stream(dev))
     _check(st, "mamba3_window_attn_decode")
     return o
 
