@@ -252,6 +252,29 @@ __device__ __forceinline__ uint4 result_step(const float* v, int ks) {
   }
 }
 
+// N products, the fragment of each read from LDS (READS instructions) AHEAD
+// products before its use: left to itself the compiler reads it right before,
+// and every product waits for LDS.
+template <int AHEAD, int N, int READS, typename T, typename Read, typename Multiply>
+__device__ __forceinline__ void ahead(Read&& read, Multiply&& multiply) {
+  constexpr int RING = AHEAD + 1;
+  uint4 f[RING];
+#pragma unroll
+  for (int i = 0; i < AHEAD && i < N; ++i) f[i % RING] = read(i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + AHEAD < N) f[(i + AHEAD) % RING] = read(i + AHEAD);
+    multiply(i, f[i % RING]);
+  }
+  if constexpr (io<T>::BYTES == 2) {
+#pragma unroll
+    for (int i = -AHEAD; i < N; ++i) {
+      if (i >= 0) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    }
+  }
+}
+
 // Larger of lane l's and lane l ^ 32's.
 __device__ __forceinline__ float max_halves(float v) {
   uint32_t a = __float_as_uint(v), b = a;
@@ -273,13 +296,31 @@ __device__ __forceinline__ void attn_settle() {
   asm volatile("" ::: "memory");
 }
 
-// The softmax of 32 columns over rows that come in pieces: running maximum
-// and sum, and the result's columns scaled along.
+// A barrier of the block that code does not move across; loads into LDS that
+// the wave has in flight may go on.
+__device__ __forceinline__ void attn_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// ... the wave's own have landed
+__device__ __forceinline__ void attn_landed() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The softmax of 32 columns over rows that come in pieces: weights against a
+// running reference m of each column, their sum, and the result's columns scaled
+// along when m moves.
 //
-// The maximum is let behind by up to kSlack powers of two before what was
-// summed is scaled anew: p stays below 2^kSlack, where fp32 sums and bf16
-// roundings are as exact as below 1.
-constexpr float kSlack = 8.0f;
+// m need not be the maximum: a weight may be as large as 2^12, where fp32
+// sums and bf16 roundings are as exact as below 1.  So no maximum is taken while
+// the sum of a piece's weights, which is needed anyway, stays below that; only
+// when it does not is the piece weighed again, against its maximum.  (That moved
+// 30 of 145 vector instructions out of a piece of 64 keys.)
 template <int CT>
 struct Softmax {
   float m, l;  // m of both halves of the wave, l of the lane's own rows
@@ -287,15 +328,26 @@ struct Softmax {
     m = -INFINITY;
     l = 0.0f;
   }
-  // s: NS scores of the lane's column (-inf: not seen), turned into weights
   template <int NS>
-  __device__ __forceinline__ void step(float* s, float c, f32x16 (&acc)[CT]) {
-    float t = s[0];
+  __device__ __forceinline__ static float weights(const float* s, float c, float mc, float* p) {
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // four chains: a lone wave waits for every dependent addition
 #pragma unroll
-    for (int i = 1; i < NS; ++i) t = fmaxf(t, s[i]);
-    t = max_halves(t);
-    if (__any((t - m) * c > kSlack || (m == -INFINITY && t > m))) {
-      const float n = fmaxf(m, t);
+    for (int i = 0; i < NS; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+      sum[i & 3] += p[i];
+    }
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+  // p: weights of the NS scores s of the lane's column (-inf: not seen)
+  template <int NS>
+  __device__ __forceinline__ void step(const float* s, float c, f32x16 (&acc)[CT], float* p) {
+    // before any score is met, m is as good as 0: what that yields is in order or too large
+    float sum = weights<NS>(s, c, m == -INFINITY ? 0.0f : m * c, p);
+    if (__any(sum > 0x1p12f || m == -INFINITY)) {
+      float t = s[0];
+#pragma unroll
+      for (int i = 1; i < NS; ++i) t = fmaxf(t, s[i]);
+      const float n = fmaxf(m, max_halves(t));
       const float scale = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - n) * c);
       m = n;
       l *= scale;
@@ -303,13 +355,9 @@ struct Softmax {
       for (int i = 0; i < CT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[i][j] *= scale;
+      sum = weights<NS>(s, c, m == -INFINITY ? 0.0f : m * c, p);
     }
-    const float mc = m == -INFINITY ? 0.0f : m * c;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
-      l += s[i];
-    }
+    l += sum;
   }
 };
 

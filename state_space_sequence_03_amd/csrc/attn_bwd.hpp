@@ -57,7 +57,7 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // `pieces`), each with a.piece queries, whose sums go to the workspace in fp32
 // and are joined in order.
 template <typename T, int DP, int BQ>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, int64_t items, int64_t pieces) {
+__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t items, int64_t pieces) {
   using QD = Tile<T, DP, BQ, 4>;
   constexpr int ES = io<T>::BYTES, STEPS = 32 / QD::CK;
   constexpr int STAGE = 2 * QD::BYTES + 512;  // Q, dO, statistics
@@ -127,41 +127,62 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, int64_t it
     const char* dl = ql + QD::BYTES;
     const float* stat = (const float*)(dl + QD::BYTES);
     const int r = r0 + n % per * BQ;
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < BQ / 32; ++b) {
       const int p0 = past + r + 32 * b;
       if (sees_none(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) continue;
-      f32x16 z = f32x16{}, y = f32x16{};
-#pragma unroll
-      for (int st = 0; st < QD::KS; ++st) z = mma32<T>(qt.row(ql, b, st), k.v[st], z);
-#pragma unroll
-      for (int st = 0; st < QD::KS; ++st) y = mma32<T>(dt.row(dl, b, st), v.v[st], y);
+      // one product after the other: their operands together would not fit
+      // the registers that two waves on a SIMD have each
+      const bool all = sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks);
       float p[16], ds[16];
+      {
+        f32x16 z = f32x16{};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 l2 = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 32 * b + 8 * i + 4 * h)));
-        const f32x4 de = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 64 + 32 * b + 8 * i + 4 * h)));
+        for (int st = 0; st < QD::KS; ++st) z = mma32<T>(qt.row(ql, b, st), k.v[st], z);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[4 * i + e] = __builtin_amdgcn_exp2f(fmaf(z[4 * i + e], c, -l2[e]));
-          ds[4 * i + e] = y[4 * i + e] - de[e];
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 l2 = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 32 * b + 8 * i + 4 * h)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[4 * i + e] = __builtin_amdgcn_exp2f(fmaf(z[4 * i + e], c, -l2[e]));
         }
       }
-      if (!sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) {
+      if (!all) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) p[i] = ds[i] = 0.0f;
+          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) p[i] = 0.0f;
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ds[i] *= p[i];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const uint4 w = result_step<T>(p, st), x = result_step<T>(ds, st);
+        const uint4 w = result_step<T>(p, st);
 #pragma unroll
         for (int d = 0; d < QD::CT; ++d) dv[d] = mma32<T>(dt.col(dl, d, b * STEPS + st), w, dv[d]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      {
+        f32x16 y = f32x16{};
+#pragma unroll
+        for (int st = 0; st < QD::KS; ++st) y = mma32<T>(dt.row(dl, b, st), v.v[st], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 de = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 64 + 32 * b + 8 * i + 4 * h)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ds[4 * i + e] = p[4 * i + e] * (y[4 * i + e] - de[e]);
+        }
+      }
+      if (!all) {  // what is not seen may have met an infinity
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) ds[i] = 0.0f;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const uint4 x = result_step<T>(ds, st);
 #pragma unroll
         for (int d = 0; d < QD::CT; ++d) dk[d] = mma32<T>(qt.col(ql, d, b * STEPS + st), x, dk[d]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (cut) {
@@ -231,7 +252,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // the forward does.  It comes first and leaves the queries' statistics to the
 // other kernel.
 template <typename T, int DP, int BN>
-__global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, BN, 4>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V

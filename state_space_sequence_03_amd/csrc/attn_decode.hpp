@@ -168,10 +168,11 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 ? 2 : 1) void attn_decode_ke
       const int j = x + v / 4 * 8 + 4 * h + v % 4;
       z[v] = j < e && view.seen(j, tok, a.window) ? sc[v] : -INFINITY;
     }
-    soft.template step<16>(z, c, acc);
+    float p[16];
+    soft.template step<16>(z, c, acc, p);
 #pragma unroll
     for (int n = 0; n < STEPS; ++n) {
-      const uint4 w = result_step<T>(z, n);
+      const uint4 w = result_step<T>(p, n);
 #pragma unroll
       for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(vt.col(vl, d, n), w, acc[d]);
     }

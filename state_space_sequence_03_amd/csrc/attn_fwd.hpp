@@ -5,15 +5,21 @@
 
 namespace m3 {
 
-// A block of four waves takes 128 queries of one head, each wave 32 of them as
-// the columns of its products: scores = K q^T, o^T += V^T p.  It walks the
-// tiles of BN keys that its queries see: the sinks' first, then the window's.
-// Keys and values come straight from memory into LDS, the next tile's while
+// A block of four waves takes 128 queries, 128 / HT positions of HT heads that
+// share a head of keys, each wave 32 of one head as the columns of its products:
+// scores = K q^T, o^T += V^T p.  (As many heads as there are, up to 4: the fewer
+// positions, the fewer keys that only some of the block's queries see.)  The
+// block walks the tiles of BN keys that its queries see, the sinks' first, then
+// the window's.  Keys and values come straight from memory into LDS, the next tile's while
 // this one's products run.
-template <typename T, int DP, int BN>
+//
+// Two blocks share a CU, so that one's softmax (vector units) runs under the
+// other's products (matrix cores).  They overlap in part only: products alone
+// would take 0.53 of the time, the softmax 0.65.
+template <typename T, int DP, int BN, int HT>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, BN, 4>;
-  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK;
+  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -21,20 +27,19 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   const int G = a.q_heads / a.kv_heads;
   // heads that share keys are neighbours, then the tiles of a sequence, the
   // longest first
-  const int64_t i = xcd_order(blockIdx.x, gridDim.x);
-  const int g = (int)(i % G);
-  const int64_t hk = i / G / items;
+  const uint32_t id = (uint32_t)xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
+  const int64_t hk = kg / (uint32_t)items;
   AttnSeq s;
   int t;
-  if (!attn_item<false>(a, i / G % items, 128, 0, s, t)) return;
-  t = (s.nq + 127) / 128 - 1 - t;
-  const int64_t hq = hk * G + g;
+  if (!attn_item<false>(a, kg % (uint32_t)items, BM, 0, s, t)) return;
+  t = (s.nq + BM - 1) / BM - 1 - t;
+  const int64_t hq = hk * G + id % (uint32_t)(G / HT) * HT + wave % HT;
 
-  const int r = t * 128 + wave * 32 + (lane & 31);
+  const int r = t * BM + wave / HT * 32 + (lane & 31);
   const bool in = r < s.nq;
   const int p = s.past() + r;
-  const int p0 = s.past() + t * 128, p1 = s.past() + (s.nq - 1 < t * 128 + 127 ? s.nq - 1 : t * 128 + 127);
-  const int w0 = p0 + wave * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
+  const int p0 = s.past() + t * BM, p1 = s.past() + (s.nq < t * BM + BM ? s.nq : t * BM + BM) - 1;
+  const int w0 = p0 + wave / HT * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
   const int64_t row = s.q0 + (in ? r : s.nq - 1);
   RowRegs<T, DP> q;
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
@@ -46,10 +51,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   const char* vb = (const char*)a.v + (s.k0 * a.v_stride + hk * a.dim) * ES;
   int first = p0 - a.window + 1;
   first = first < 0 ? 0 : first / BN;
-  const int sunk = (int)(((int64_t)a.sinks + BN - 1) / BN), ns = sunk < first ? sunk : first;
+  const int sunk = (a.sinks + BN - 1) / BN, ns = sunk < first ? sunk : first;
   const int count = p1 < 0 ? 0 : ns + p1 / BN - first + 1;
+  auto first_key = [&](int n) { return (n < ns ? n : first + n - ns) * BN; };
   auto load = [&](int n, int buf) {
-    const int64_t j0 = (int64_t)(n < ns ? n : first + n - ns) * BN;
+    const int64_t j0 = first_key(n);
     kt.load(kb + j0 * a.k_stride * ES, s.nk - (int)j0, a.dim, smem + buf * 2 * KV::BYTES, wave);
     vt.load(vb + j0 * a.v_stride * ES, s.nk - (int)j0, a.dim, smem + (buf * 2 + 1) * KV::BYTES, wave);
   };
@@ -66,29 +72,27 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
     if (n + 1 < count) load(n + 1, (n + 1) & 1);
     const char* kl = smem + (n & 1) * 2 * KV::BYTES;
     const char* vl = kl + KV::BYTES;
-    const int j0 = (n < ns ? n : first + n - ns) * BN;
-    if (sees_none(w0, w1, j0, j0 + BN - 1, a.window, a.sinks)) continue;
-    float z[NT * 16];
+    const int j0 = first_key(n);
+    f32x16 sc[NT];
+    ahead<6, KV::KS * NT, 1, T>(
+        [&](int i) { return kt.row(kl, i % NT, i / NT); },
+        [&](int i, const uint4& f) { sc[i % NT] = mma32<T>(f, q.v[i / NT], i < NT ? f32x16{} : sc[i % NT]); });
+    float z[NT * 16], e[NT * 16];
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      f32x16 sc = f32x16{};
-#pragma unroll
-      for (int st = 0; st < KV::KS; ++st) sc = mma32<T>(kt.row(kl, k, st), q.v[st], sc);
-#pragma unroll
-      for (int v = 0; v < 16; ++v) z[k * 16 + v] = sc[v];
-    }
+    for (int v = 0; v < NT * 16; ++v) z[v] = sc[v / 16][v % 16];
     if (!sees_all(w0, w1, j0, j0 + BN - 1, a.window, a.sinks)) {
+      asm volatile("");  // a branch, not selects in every step
 #pragma unroll
       for (int v = 0; v < NT * 16; ++v)
         if (!sees(p, j0 + v / 16 * 32 + v % 16 / 4 * 8 + 4 * h + v % 4, a.window, a.sinks)) z[v] = -INFINITY;
     }
-    soft.template step<NT * 16>(z, c, acc);
+    soft.template step<NT * 16>(z, c, acc, e);
+    uint4 w[NT * STEPS];
 #pragma unroll
-    for (int k = 0; k < NT * STEPS; ++k) {
-      const uint4 w = result_step<T>(z, k);
-#pragma unroll
-      for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(vt.col(vl, d, k), w, acc[d]);
-    }
+    for (int k = 0; k < NT * STEPS; ++k) w[k] = result_step<T>(e, k);
+    ahead<6, NT * STEPS * KV::CT, 2, T>(
+        [&](int i) { return vt.col(vl, i % KV::CT, i / KV::CT); },
+        [&](int i, const uint4& f) { acc[i % KV::CT] = mma32<T>(f, w[i / KV::CT], acc[i % KV::CT]); });
   }
   const float l = swap_sum32(soft.l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing: 0
@@ -104,13 +108,21 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   }
 }
 
+template <typename T, int HT>
+void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
+  const int64_t items = attn_items(a, false, 128 / HT);
+  const dim3 grid((unsigned)(items * (a.q_heads / HT))), block(256);
+  constexpr int BN = io<T>::BYTES == 2 ? 64 : 32;
+  if (a.dim <= 64) hipLaunchKernelGGL((attn_fwd_kernel<T, 64, BN, HT>), grid, block, 0, s, a, items);
+  else hipLaunchKernelGGL((attn_fwd_kernel<T, 128, BN, HT>), grid, block, 0, s, a, items);
+}
+
 template <typename T>
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
-  const int64_t items = attn_items(a, false, 128);
-  const dim3 grid((unsigned)(items * a.q_heads)), block(256);
-  constexpr int BN = io<T>::BYTES == 2 ? 64 : 32;
-  if (a.dim <= 64) hipLaunchKernelGGL((attn_fwd_kernel<T, 64, BN>), grid, block, 0, s, a, items);
-  else hipLaunchKernelGGL((attn_fwd_kernel<T, 128, BN>), grid, block, 0, s, a, items);
+  const int G = a.q_heads / a.kv_heads;
+  if (G % 4 == 0) attn_fwd_run<T, 4>(a, s);
+  else if (G % 2 == 0) attn_fwd_run<T, 2>(a, s);
+  else attn_fwd_run<T, 1>(a, s);
   return hipGetLastError();
 }
 
