@@ -53,49 +53,56 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // BQ rows that all four waves read.
 //
 // The sinks are seen from the whole sequence.  Where that is longer than
-// a.piece queries, a sinks' tile is left to blocks of its own (the first
-// `pieces`), each with a.piece queries, whose sums go to the workspace in fp32
-// and are joined in order.
+// a.piece queries, each 32 keys with sinks among them are left to blocks of
+// their own (the first `pieces`), each with a.piece queries, of which each wave
+// takes every fourth 32; the four sums go to the workspace in fp32 and are
+// joined in order.
+//
+// Two waves share a SIMD, which the registers just allow (fragments three
+// products ahead: 620 us for 8 x 4096 queries, 16/4 heads of 128, window 1024;
+// six ahead with spills 740, one wave per SIMD 780).
 template <typename T, int DP, int BQ>
-__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t items, int64_t pieces) {
+__global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, int64_t items,
+                                                                                             int64_t pieces) {
   using QD = Tile<T, DP, BQ, 4>;
-  constexpr int ES = io<T>::BYTES, STEPS = 32 / QD::CK;
+  constexpr int ES = io<T>::BYTES, STEPS = 32 / QD::CK, AHEAD = 3;
   constexpr int STAGE = 2 * QD::BYTES + 512;  // Q, dO, statistics
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
-  const int sunk = (a.sinks + 127) / 128;
+  const int sunk = (a.sinks + 31) / 32;
   const bool cut = blockIdx.x < pieces;
-  int64_t id = blockIdx.x;
   AttnSeq s;
-  int t, piece = 0;
+  int jw, piece = 0;  // the wave's first key
   int64_t hk;
   if (cut) {
-    hk = id % a.kv_heads;
-    id /= a.kv_heads;
-    t = (int)(id % sunk);
-    if (!attn_item<false>(a, id / sunk, a.piece, a.piece, s, piece)) return;
-    if (t * 128 >= s.nk) return;
+    const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;
+    hk = blockIdx.x % (uint32_t)a.kv_heads;
+    jw = (int)(id % (uint32_t)sunk) * 32;
+    if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
+    if (jw >= s.nk) return;
   } else {
-    id = xcd_order(id - pieces, gridDim.x - pieces);
-    hk = id / items;
-    if (!attn_item<true>(a, id % items, 128, 0, s, t)) return;
-    if (t < sunk && s.nq > a.piece) return;
+    const uint32_t id = (uint32_t)xcd_order(blockIdx.x - pieces, gridDim.x - pieces);
+    int t;
+    hk = id / (uint32_t)items;
+    if (!attn_item<true>(a, id % (uint32_t)items, 128, 0, s, t)) return;
+    jw = t * 128 + wave * 32;
   }
+  const bool apart = s.nq > a.piece;  // the sinks are summed in pieces
+  const bool idle = !cut && apart && jw < sunk * 32;
   const int past = s.past();
-  const int j0 = t * 128, jw = j0 + wave * 32, j = jw + (lane & 31);
+  const int j0 = cut ? jw : jw - wave * 32, j = jw + (lane & 31);
   const bool in = j < s.nk;
   // queries that see some of the block's keys
   int r0 = j0 - past < 0 ? 0 : j0 - past, r1 = s.nq - 1;
-  if (a.window < kNoWindow && j0 >= a.sinks) {
-    const int64_t last = (int64_t)j0 + 127 + a.window - 1 - past;
-    if (last < r1) r1 = (int)last;
-  }
   if (cut) {
     if (r0 < piece * a.piece) r0 = piece * a.piece;
     if (r1 > piece * a.piece + a.piece - 1) r1 = piece * a.piece + a.piece - 1;
+  } else if (a.window < kNoWindow && (apart || j0 >= a.sinks)) {
+    const int64_t last = (int64_t)j0 + 127 + a.window - 1 - past;
+    if (last < r1) r1 = (int)last;
   }
   r0 = r0 / BQ * BQ;  // whole tiles, so that a piece's last one ends with it
   const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, count = per * G;
@@ -107,9 +114,8 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t it
   QD qt, dt;
   qt.init(a.q_stride, a.dim, lane, wave);
   dt.init(a.do_stride, a.dim, lane, wave);
-  auto load = [&](int n, int buf) {
-    const int64_t hq = hk * G + n / per;
-    const int r = r0 + n % per * BQ;
+  auto load = [&](int head, int r, int buf) {
+    const int64_t hq = hk * G + head;
     char* lds = smem + buf * STAGE;
     qt.load((const char*)a.q + ((s.q0 + r) * a.q_stride + hq * a.dim) * ES, s.nq - r, a.dim, lds, wave);
     dt.load((const char*)a.dout + ((s.q0 + r) * a.do_stride + hq * a.dim) * ES, s.nq - r, a.dim, lds + QD::BYTES, wave);
@@ -119,75 +125,68 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t it
 #pragma unroll
   for (int i = 0; i < QD::CT; ++i) dk[i] = dv[i] = f32x16{};
   const float c = a.scale * kLog2e;
-  if (count > 0) load(0, 0);
+  int head = 0, r = r0;
+  if (count > 0) load(0, r0, 0);
   for (int n = 0; n < count; ++n) {
     attn_settle();
-    if (n + 1 < count) load(n + 1, (n + 1) & 1);
+    int next = r + BQ, other = head;
+    if (next > r1) {
+      next = r0;
+      ++other;
+    }
+    if (n + 1 < count) load(other, next, (n + 1) & 1);
     const char* ql = smem + (n & 1) * STAGE;
     const char* dl = ql + QD::BYTES;
     const float* stat = (const float*)(dl + QD::BYTES);
-    const int r = r0 + n % per * BQ;
 #pragma unroll 1
     for (int b = 0; b < BQ / 32; ++b) {
       const int p0 = past + r + 32 * b;
-      if (sees_none(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) continue;
-      // one product after the other: their operands together would not fit
-      // the registers that two waves on a SIMD have each
-      const bool all = sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks);
+      if (idle || sees_none(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) continue;
+      if (cut && ((n * (BQ / 32) + b) & 3) != wave) continue;
+      f32x16 x[2] = {f32x16{}, f32x16{}};  // scores, dp
+      ahead<AHEAD, QD::KS * 2, 1, T>(
+          [&](int i) { return i & 1 ? dt.row(dl, b, i / 2) : qt.row(ql, b, i / 2); },
+          [&](int i, const uint4& f) { x[i & 1] = mma32<T>(f, i & 1 ? v.v[i / 2] : k.v[i / 2], x[i & 1]); });
       float p[16], ds[16];
-      {
-        f32x16 z = f32x16{};
 #pragma unroll
-        for (int st = 0; st < QD::KS; ++st) z = mma32<T>(qt.row(ql, b, st), k.v[st], z);
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 l2 = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 32 * b + 8 * i + 4 * h)));
+        const f32x4 de = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 64 + 32 * b + 8 * i + 4 * h)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 l2 = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 32 * b + 8 * i + 4 * h)));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[4 * i + e] = __builtin_amdgcn_exp2f(fmaf(z[4 * i + e], c, -l2[e]));
+        for (int e = 0; e < 4; ++e) {
+          p[4 * i + e] = __builtin_amdgcn_exp2f(fmaf(x[0][4 * i + e], c, -l2[e]));
+          ds[4 * i + e] = p[4 * i + e] * (x[1][4 * i + e] - de[e]);
         }
       }
-      if (!all) {
+      if (!sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) {
+        asm volatile("");  // a branch, not selects in every step
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) p[i] = 0.0f;
+          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) p[i] = ds[i] = 0.0f;
       }
-      __builtin_amdgcn_sched_barrier(0);
+      uint4 w[2][STEPS];
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const uint4 w = result_step<T>(p, st);
-#pragma unroll
-        for (int d = 0; d < QD::CT; ++d) dv[d] = mma32<T>(dt.col(dl, d, b * STEPS + st), w, dv[d]);
+        w[0][st] = result_step<T>(p, st);
+        w[1][st] = result_step<T>(ds, st);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      {
-        f32x16 y = f32x16{};
-#pragma unroll
-        for (int st = 0; st < QD::KS; ++st) y = mma32<T>(dt.row(dl, b, st), v.v[st], y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 de = __builtin_bit_cast(f32x4, read16((const u32x4*)(stat + 64 + 32 * b + 8 * i + 4 * h)));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ds[4 * i + e] = p[4 * i + e] * (y[4 * i + e] - de[e]);
-        }
-      }
-      if (!all) {  // what is not seen may have met an infinity
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) ds[i] = 0.0f;
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const uint4 x = result_step<T>(ds, st);
-#pragma unroll
-        for (int d = 0; d < QD::CT; ++d) dk[d] = mma32<T>(qt.col(ql, d, b * STEPS + st), x, dk[d]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      ahead<AHEAD, 2 * STEPS * QD::CT, 2, T>(
+          [&](int i) {
+            const int d = i % QD::CT, st = i / QD::CT % STEPS;
+            return i < STEPS * QD::CT ? dt.col(dl, d, b * STEPS + st) : qt.col(ql, d, b * STEPS + st);
+          },
+          [&](int i, const uint4& f) {
+            const int d = i % QD::CT, st = i / QD::CT % STEPS;
+            if (i < STEPS * QD::CT) dv[d] = mma32<T>(f, w[0][st], dv[d]);
+            else dk[d] = mma32<T>(f, w[1][st], dk[d]);
+          });
     }
+    head = other;
+    r = next;
   }
   if (cut) {
-    // (2, 128 keys, dim) per piece
-    float* part = a.part + (int64_t)blockIdx.x * 2 * 128 * a.dim + (int64_t)(wave * 32 + (lane & 31)) * a.dim;
+    // (dk, dv; wave; 32 keys; dim) per piece
+    float* part = a.part + ((int64_t)blockIdx.x * 8 + wave) * 32 * a.dim + (int64_t)(lane & 31) * a.dim;
 #pragma unroll
     for (int d = 0; d < QD::CT; ++d) {
       if (d * 32 >= a.dim) break;
@@ -197,9 +196,9 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t it
       tile_store<float, false>((char*)part, true, d * 32, a.dim, x, h);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = dv[d][i];
-      tile_store<float, false>((char*)(part + 128 * a.dim), true, d * 32, a.dim, x, h);
+      tile_store<float, false>((char*)(part + 4 * 32 * a.dim), true, d * 32, a.dim, x, h);
     }
-  } else {
+  } else if (!idle) {
 #pragma unroll
     for (int d = 0; d < QD::CT; ++d) {
       if (d * 32 >= a.dim) break;
@@ -214,66 +213,67 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a, int64_t it
   }
 }
 
-// The pieces of a sinks' tile joined in order, four entries to a thread; the
-// blocks of a tile's pieces share its entries.
+// The pieces of 32 keys joined in order, four entries to a thread; the blocks
+// of their pieces share the entries.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int sunk = (a.sinks + 127) / 128;
-  const int64_t hk = blockIdx.x % a.kv_heads, id = blockIdx.x / a.kv_heads;
-  const int t = (int)(id % sunk);
+  const int sunk = (a.sinks + 31) / 32;
+  const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;
+  const int64_t hk = blockIdx.x % (uint32_t)a.kv_heads;
+  const int j0 = (int)(id % (uint32_t)sunk) * 32;
   AttnSeq s;
   int piece;
-  if (!attn_item<false>(a, id / sunk, a.piece, a.piece, s, piece)) return;
-  const int keys = s.nk - t * 128 < 128 ? s.nk - t * 128 : 128;
+  if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
+  const int keys = s.nk - j0 < 32 ? s.nk - j0 : 32;
   if (keys <= 0) return;
   const int pieces = (s.nq + a.piece - 1) / a.piece;
-  const int64_t step = (int64_t)sunk * a.kv_heads * 2 * 128 * a.dim;  // from piece to piece
-  const float* part = a.part + (int64_t)blockIdx.x * 2 * 128 * a.dim - piece * step;
-  const int n = keys * a.dim;
+  const int64_t half = 32 * a.dim, step = (int64_t)sunk * a.kv_heads * 8 * half;  // from piece to piece
   const bool key = blockIdx.y == 0;
   void* out = key ? a.dk : a.dv;
   if (!out) return;
-  if (!key) part += 128 * a.dim;
+  const float* part = a.part + (int64_t)blockIdx.x * 8 * half - piece * step + (key ? 0 : 4 * half);
+  const int n = keys * a.dim;
   for (int e = (piece * 256 + (int)threadIdx.x) * 4; e < n; e += pieces * 1024) {
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const f32x4 y = *(const f32x4*)(part + i * step + e);
+#pragma unroll 2
+    for (int i = 0; i < pieces; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] += y[j];
-    }
+      for (int w = 0; w < 4; ++w) {
+        const f32x4 y = *(const f32x4*)(part + i * step + w * half + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += y[j];
+      }
     const int j = e / a.dim;
-    io<T>::store4(out, (s.k0 + t * 128 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, x);
+    io<T>::store4(out, (s.k0 + j0 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, x);
   }
 }
 
-// dq of 128 queries: each wave holds 32 of them as the columns of its products
-// (scores = K q^T, dp = V do^T, dq^T += K^T ds) and walks the keys they see as
-// the forward does.  It comes first and leaves the queries' statistics to the
-// other kernel.
-template <typename T, int DP, int BN>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int64_t items) {
+// dq of 128 queries, 128 / HT positions of HT heads as in the forward: each wave
+// holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
+// dq^T += K^T ds) and walks the keys they see as the forward does.  It comes
+// first and leaves the queries' statistics to the other kernel.
+template <typename T, int DP, int BN, int HT>
+__global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, BN, 4>;
-  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK;
+  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT, HALF = 32 * KV::ROWB;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
-  const int64_t i = xcd_order(blockIdx.x, gridDim.x);
-  const int g = (int)(i % G);
-  const int64_t hk = i / G / items;
+  const uint32_t id = (uint32_t)xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
+  const int64_t hk = kg / (uint32_t)items;
   AttnSeq s;
   int t;
-  if (!attn_item<false>(a, i / G % items, 128, 0, s, t)) return;
-  t = (s.nq + 127) / 128 - 1 - t;
-  const int64_t hq = hk * G + g;
+  if (!attn_item<false>(a, kg % (uint32_t)items, BM, 0, s, t)) return;
+  t = (s.nq + BM - 1) / BM - 1 - t;
+  const int64_t hq = hk * G + id % (uint32_t)(G / HT) * HT + wave % HT;
 
-  const int r = t * 128 + wave * 32 + (lane & 31);
+  const int r = t * BM + wave / HT * 32 + (lane & 31);
   const bool in = r < s.nq;
   const int p = s.past() + r;
-  const int p0 = s.past() + t * 128, p1 = s.past() + (s.nq - 1 < t * 128 + 127 ? s.nq - 1 : t * 128 + 127);
-  const int w0 = p0 + wave * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
+  const int p0 = s.past() + t * BM, p1 = s.past() + (s.nq < t * BM + BM ? s.nq : t * BM + BM) - 1;
+  const int w0 = p0 + wave / HT * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
   const int64_t row = s.q0 + (in ? r : s.nq - 1);
   RowRegs<T, DP> q, y;
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
@@ -308,8 +308,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int64_t ite
   first = first < 0 ? 0 : first / BN;
   const int sunk = (a.sinks + BN - 1) / BN, ns = sunk < first ? sunk : first;
   const int count = p1 < 0 ? 0 : ns + p1 / BN - first + 1;
+  auto first_key = [&](int n) { return (n < ns ? n : first + n - ns) * BN; };
   auto load = [&](int n, int buf) {
-    const int64_t j0 = (int64_t)(n < ns ? n : first + n - ns) * BN;
+    const int64_t j0 = first_key(n);
     kt.load(kb + j0 * a.k_stride * ES, s.nk - (int)j0, a.dim, smem + buf * 2 * KV::BYTES, wave);
     vt.load(vb + j0 * a.v_stride * ES, s.nk - (int)j0, a.dim, smem + (buf * 2 + 1) * KV::BYTES, wave);
   };
@@ -321,31 +322,31 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int64_t ite
   for (int n = 0; n < count; ++n) {
     attn_settle();
     if (n + 1 < count) load(n + 1, (n + 1) & 1);
-    const char* kl = smem + (n & 1) * 2 * KV::BYTES;
-    const char* vl = kl + KV::BYTES;
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < NT; ++b) {
-      const int j0 = (n < ns ? n : first + n - ns) * BN + 32 * b;
+      const int j0 = first_key(n) + 32 * b;
       if (sees_none(w0, w1, j0, j0 + 31, a.window, a.sinks)) continue;
-      f32x16 z = f32x16{}, dp = f32x16{};
-#pragma unroll
-      for (int st = 0; st < KV::KS; ++st) z = mma32<T>(kt.row(kl, b, st), q.v[st], z);
-#pragma unroll
-      for (int st = 0; st < KV::KS; ++st) dp = mma32<T>(vt.row(vl, b, st), y.v[st], dp);
+      const char* kl = smem + (n & 1) * 2 * KV::BYTES + b * HALF;
+      const char* vl = kl + KV::BYTES;
+      f32x16 x[2] = {f32x16{}, f32x16{}};  // scores, dp
+      ahead<6, KV::KS * 2, 1, T>(
+          [&](int i) { return i & 1 ? vt.row(vl, 0, i / 2) : kt.row(kl, 0, i / 2); },
+          [&](int i, const uint4& f) { x[i & 1] = mma32<T>(f, i & 1 ? y.v[i / 2] : q.v[i / 2], x[i & 1]); });
       float ds[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ds[i] = __builtin_amdgcn_exp2f(fmaf(z[i], c, -l2)) * (dp[i] - delta);
+      for (int i = 0; i < 16; ++i) ds[i] = __builtin_amdgcn_exp2f(fmaf(x[0][i], c, -l2)) * (x[1][i] - delta);
       if (!sees_all(w0, w1, j0, j0 + 31, a.window, a.sinks)) {
+        asm volatile("");  // a branch, not selects in every step
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (!sees(p, j0 + i / 4 * 8 + 4 * h + i % 4, a.window, a.sinks)) ds[i] = 0.0f;
       }
+      uint4 w[STEPS];
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const uint4 w = result_step<T>(ds, st);
-#pragma unroll
-        for (int d = 0; d < KV::CT; ++d) acc[d] = mma32<T>(kt.col(kl, d, b * STEPS + st), w, acc[d]);
-      }
+      for (int st = 0; st < STEPS; ++st) w[st] = result_step<T>(ds, st);
+      ahead<6, STEPS * KV::CT, 2, T>(
+          [&](int i) { return kt.col(kl, i % KV::CT, i / KV::CT); },
+          [&](int i, const uint4& f) { acc[i % KV::CT] = mma32<T>(f, w[i / KV::CT], acc[i % KV::CT]); });
     }
   }
   char* out = (char*)a.dq + (row * a.dq_stride + hq * a.dim) * ES;
@@ -359,17 +360,27 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int64_t ite
   }
 }
 
+template <typename T, int DP, int HT>
+void attn_dq_run(const AttnArgs& a, hipStream_t s) {
+  const int64_t items = attn_items(a, false, 128 / HT);
+  if (items > 0)
+    hipLaunchKernelGGL((attn_dq_kernel<T, DP, io<T>::BYTES == 2 ? 64 : 32, HT>),
+                       dim3((unsigned)(items * (a.q_heads / HT))), dim3(256), 0, s, a, items);
+}
+
 template <typename T, int DP>
 hipError_t attn_bwd_run(const AttnArgs& a, hipStream_t s) {
-  constexpr int BN = io<T>::BYTES == 2 ? 64 : 32, BQ = BN;
+  constexpr int BQ = io<T>::BYTES == 2 ? 64 : 32;
   const dim3 block(256);
-  const int64_t vectors = a.rows * a.q_heads, items = attn_items(a, false, 128), tiles = attn_items(a, true, 128);
-  if (a.dq && items > 0)
-    hipLaunchKernelGGL((attn_dq_kernel<T, DP, BN>), dim3((unsigned)(items * a.q_heads)), block, 0, s, a, items);
+  const int64_t vectors = a.rows * a.q_heads, tiles = attn_items(a, true, 128);
+  const int G = a.q_heads / a.kv_heads;
+  if (a.dq && G % 4 == 0) attn_dq_run<T, DP, 4>(a, s);
+  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, 2>(a, s);
+  else if (a.dq) attn_dq_run<T, DP, 1>(a, s);
   else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);
   if ((a.dk || a.dv) && tiles > 0) {
-    const int64_t pieces = attn_pieces(a) * ((a.sinks + 127) / 128) * a.kv_heads;
+    const int64_t pieces = attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads;
     hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BQ>), dim3((unsigned)(pieces + tiles * a.kv_heads)), block, 0, s, a,
                        tiles, pieces);
     if (pieces > 0) hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)pieces, 2), block, 0, s, a);

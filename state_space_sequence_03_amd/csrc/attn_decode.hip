@@ -24,18 +24,19 @@ size_t attn_decode_part_bytes(const AttnDecodeArgs& a) {
   return a.splits == 1 ? 0 : (size_t)a.batch * a.tokens * a.q_heads * a.splits * (a.dim + 2) * 4;
 }
 
-// Queries of a piece of a sinks' tile: about as many as see a tile behind the
-// sinks, and so many that there are 2048 pieces at most.
+// Queries of a piece of 32 keys with sinks among them: half of what sees a tile
+// behind the sinks, so that its block is done well before a tile's, and so many
+// that there are 8192 pieces at most.
 int attn_bwd_piece(const AttnArgs& a) {
-  int64_t n = (a.window < (1 << 24) ? a.window : 1 << 24) + 128;
-  const int64_t work = a.rows * ((a.sinks + 127) / 128) * a.kv_heads;
+  int64_t n = ((a.window < (1 << 24) ? a.window : 1 << 24) + 128) / 2;
+  const int64_t work = a.rows * ((a.sinks + 31) / 32) * a.kv_heads;
   if (n < 256) n = 256;
-  if (n < work / 1024) n = work / 1024;
+  if (n < work / 4096) n = work / 4096;
   n = (n + 127) / 128 * 128;
   return (int)(n < (1 << 25) ? n : 1 << 25);
 }
 size_t attn_bwd_part_bytes(const AttnArgs& a) {
-  return (size_t)attn_pieces(a) * ((a.sinks + 127) / 128) * a.kv_heads * 2 * 128 * a.dim * 4;
+  return (size_t)attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads * 8 * 32 * a.dim * 4;
 }
 
 }  // namespace m3
