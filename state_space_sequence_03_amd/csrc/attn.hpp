@@ -32,7 +32,7 @@ __device__ __forceinline__ int64_t start_of(const AttnArgs& a, int64_t i) {
   return s < 0 ? 0 : s > a.rows ? a.rows : s;
 }
 
-// Item `flat` of all sequences' tiles of `tile` rows, longer than `over` rows
+// Item `flat` (below 2^32) of all sequences' tiles of `tile` rows, longer than `over` rows
 // (queries, or keys with KEYS): the sequence and the tile within it.  false:
 // there are fewer.  Every lane of a wave calls it with the same arguments.
 template <bool KEYS>
@@ -41,7 +41,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int64_t flat, int t
     const int n = KEYS ? a.kv_len : a.q_len;
     const int per = n > over ? (n + tile - 1) / tile : 0;
     if (per == 0) return false;
-    s.id = flat / per;
+    s.id = (uint32_t)flat / (uint32_t)per;
     if (s.id >= a.batch) return false;
     t = (int)(flat - s.id * per);
     s.q0 = s.id * a.q_len;
@@ -93,8 +93,8 @@ inline int64_t attn_pieces(const AttnArgs& a) {
 
 // Blocks go to the 8 XCDs in turn, each with an L2 of its own: XCD x gets the
 // x-th contiguous eighth of the work, whose neighbours share keys and values.
-__device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
-  const int64_t x = i & 7, per = n >> 3, rem = n & 7;
+__device__ __forceinline__ uint32_t xcd_order(uint32_t i, uint32_t n) {
+  const uint32_t x = i & 7, per = n >> 3, rem = n & 7;
   return x * per + (x < rem ? x : rem) + (i >> 3);
 }
 
@@ -114,8 +114,9 @@ __device__ __forceinline__ bool sees_none(int p0, int p1, int j0, int j1, int wi
 // ROWS rows of DP entries in LDS, 16-byte chunk c of row r at chunk c ^ f(r):
 // f spreads the 16 rows of a row read over all banks, and the 4 rows of a
 // transposed read over the quarters of them.  Filled straight from memory by
-// NW waves; entries past the width and rows past the last read as zero.
-template <typename T, int DP, int ROWS, int NW>
+// NW waves; entries past the width and rows past the last read as zero.  DU: the
+// entries that products take, where fewer than DP do.
+template <typename T, int DP, int DU, int ROWS, int NW>
 struct Tile {
   static constexpr int ES = io<T>::BYTES;
   static constexpr int ROWB = DP * ES;
@@ -123,8 +124,8 @@ struct Tile {
   static constexpr int LPR = ROWB / 16;           // lanes per row
   static constexpr int RPI = 64 / LPR;            // rows per 1 KB load
   static constexpr int NI = BYTES / 1024 / NW;    // loads per wave
-  static constexpr int KS = ROWB / 32;            // steps of a product over a row
-  static constexpr int CT = DP / 32;              // tiles of a product whose result's rows are the columns
+  static constexpr int KS = DU * ES / 32;         // steps of a product over a row
+  static constexpr int CT = DU / 32;              // tiles of a product whose result's rows are the columns
   static constexpr int CK = ES == 2 ? 16 : 8;     // rows a step of such a product takes
   static constexpr int NV = RPI * NW % 16 == 0 ? 1 : 16 / (RPI * NW);  // loads until f repeats
   static_assert(BYTES % (1024 * NW) == 0 && LPR <= 64, "whole loads");
@@ -202,9 +203,9 @@ struct Tile {
 
 // 32 rows from memory as the other operand of a product over their columns:
 // lane l holds row l mod 32.  in: that row exists.
-template <typename T, int DP>
+template <typename T, int DU>
 struct RowRegs {
-  static constexpr int KS = DP * io<T>::BYTES / 32;
+  static constexpr int KS = DU * io<T>::BYTES / 32;
   uint4 v[KS];
   __device__ __forceinline__ void load(const char* row, bool in, int width, int h) {
     constexpr int V = io<T>::VEC;
@@ -217,9 +218,9 @@ struct RowRegs {
 };
 
 // The same for consecutive rows, which may be requested ahead of their use.
-template <typename T, int DP>
+template <typename T, int DU>
 struct RowStream {
-  static constexpr int KS = DP * io<T>::BYTES / 32;
+  static constexpr int KS = DU * io<T>::BYTES / 32;
   uint4 v[KS];
   int voff, ldb, last;  // last: chunks of a row past it do not exist
   __device__ __forceinline__ void init(int64_t ld, int width, int lane) {
@@ -273,6 +274,20 @@ __device__ __forceinline__ void ahead(Read&& read, Multiply&& multiply) {
       if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
     }
   }
+}
+
+// Calls f with DP and DU of a head's width: 32, 64, 96 or 128 entries in rows of
+// 64 or 128.
+template <typename F>
+void with_width(int dim, F&& f) {
+  const std::integral_constant<int, 32> c32;
+  const std::integral_constant<int, 64> c64;
+  const std::integral_constant<int, 96> c96;
+  const std::integral_constant<int, 128> c128;
+  if (dim <= 32) f(c64, c32);
+  else if (dim <= 64) f(c64, c64);
+  else if (dim <= 96) f(c128, c96);
+  else f(c128, c128);
 }
 
 // Larger of lane l's and lane l ^ 32's.

@@ -61,10 +61,10 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // Two waves share a SIMD, which the registers just allow (fragments three
 // products ahead: 620 us for 8 x 4096 queries, 16/4 heads of 128, window 1024;
 // six ahead with spills 740, one wave per SIMD 780).
-template <typename T, int DP, int BQ>
+template <typename T, int DP, int DU, int BQ>
 __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, int64_t items,
                                                                                              int64_t pieces) {
-  using QD = Tile<T, DP, BQ, 4>;
+  using QD = Tile<T, DP, DU, BQ, 4>;
   constexpr int ES = io<T>::BYTES, STEPS = 32 / QD::CK, AHEAD = 3;
   constexpr int STAGE = 2 * QD::BYTES + 512;  // Q, dO, statistics
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
     if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
     if (jw >= s.nk) return;
   } else {
-    const uint32_t id = (uint32_t)xcd_order(blockIdx.x - pieces, gridDim.x - pieces);
+    const uint32_t id = xcd_order(blockIdx.x - (uint32_t)pieces, gridDim.x - (uint32_t)pieces);
     int t;
     hk = id / (uint32_t)items;
     if (!attn_item<true>(a, id % (uint32_t)items, 128, 0, s, t)) return;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, count = per * G;
 
   const int64_t row = s.k0 + (in ? j : s.nk - 1);
-  RowRegs<T, DP> k, v;
+  RowRegs<T, DU> k, v;
   k.load((const char*)a.k + (row * a.k_stride + hk * a.dim) * ES, in, a.dim, h);
   v.load((const char*)a.v + (row * a.v_stride + hk * a.dim) * ES, in, a.dim, h);
   QD qt, dt;
@@ -252,16 +252,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
 // dq^T += K^T ds) and walks the keys they see as the forward does.  It comes
 // first and leaves the queries' statistics to the other kernel.
-template <typename T, int DP, int BN, int HT>
+template <typename T, int DP, int DU, int BN, int HT>
 __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
-  using KV = Tile<T, DP, BN, 4>;
+  using KV = Tile<T, DP, DU, BN, 4>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT, HALF = 32 * KV::ROWB;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
-  const uint32_t id = (uint32_t)xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
+  const uint32_t id = xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
   const int64_t hk = kg / (uint32_t)items;
   AttnSeq s;
   int t;
@@ -275,15 +275,15 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   const int p0 = s.past() + t * BM, p1 = s.past() + (s.nq < t * BM + BM ? s.nq : t * BM + BM) - 1;
   const int w0 = p0 + wave / HT * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
   const int64_t row = s.q0 + (in ? r : s.nq - 1);
-  RowRegs<T, DP> q, y;
+  RowRegs<T, DU> q, y;
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
   y.load((const char*)a.dout + (row * a.do_stride + hq * a.dim) * ES, in, a.dim, h);
   float delta = 0.0f;
   {
-    RowRegs<T, DP> o;
+    RowRegs<T, DU> o;
     o.load((const char*)a.o + (row * a.o_stride + hq * a.dim) * ES, in, a.dim, h);
 #pragma unroll
-    for (int st = 0; st < RowRegs<T, DP>::KS; ++st) {
+    for (int st = 0; st < RowRegs<T, DU>::KS; ++st) {
       constexpr int V = io<T>::VEC;
       float x[V], z[V];
       io<T>::unpack(__builtin_bit_cast(typename io<T>::vec, o.v[st]), x);
@@ -360,37 +360,37 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
 }
 
-template <typename T, int DP, int HT>
+template <typename T, int DP, int DU, int HT>
 void attn_dq_run(const AttnArgs& a, hipStream_t s) {
   const int64_t items = attn_items(a, false, 128 / HT);
   if (items > 0)
-    hipLaunchKernelGGL((attn_dq_kernel<T, DP, io<T>::BYTES == 2 ? 64 : 32, HT>),
+    hipLaunchKernelGGL((attn_dq_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32, HT>),
                        dim3((unsigned)(items * (a.q_heads / HT))), dim3(256), 0, s, a, items);
 }
 
-template <typename T, int DP>
-hipError_t attn_bwd_run(const AttnArgs& a, hipStream_t s) {
+template <typename T, int DP, int DU>
+void attn_bwd_run(const AttnArgs& a, hipStream_t s) {
   constexpr int BQ = io<T>::BYTES == 2 ? 64 : 32;
   const dim3 block(256);
   const int64_t vectors = a.rows * a.q_heads, tiles = attn_items(a, true, 128);
   const int G = a.q_heads / a.kv_heads;
-  if (a.dq && G % 4 == 0) attn_dq_run<T, DP, 4>(a, s);
-  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, 2>(a, s);
-  else if (a.dq) attn_dq_run<T, DP, 1>(a, s);
+  if (a.dq && G % 4 == 0) attn_dq_run<T, DP, DU, 4>(a, s);
+  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, DU, 2>(a, s);
+  else if (a.dq) attn_dq_run<T, DP, DU, 1>(a, s);
   else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);
   if ((a.dk || a.dv) && tiles > 0) {
     const int64_t pieces = attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads;
-    hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BQ>), dim3((unsigned)(pieces + tiles * a.kv_heads)), block, 0, s, a,
+    hipLaunchKernelGGL((attn_dkv_kernel<T, DP, DU, BQ>), dim3((unsigned)(pieces + tiles * a.kv_heads)), block, 0, s, a,
                        tiles, pieces);
     if (pieces > 0) hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)pieces, 2), block, 0, s, a);
   }
-  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {
-  return a.dim <= 64 ? attn_bwd_run<T, 64>(a, s) : attn_bwd_run<T, 128>(a, s);
+  with_width(a.dim, [&](auto dp, auto du) { attn_bwd_run<T, decltype(dp)::value, decltype(du)::value>(a, s); });
+  return hipGetLastError();
 }
 
 }  // namespace m3

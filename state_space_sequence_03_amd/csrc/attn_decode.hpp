@@ -74,9 +74,9 @@ struct CacheView {
 // values are written to the cache by the wave that then reads their slots.
 //
 // Bound by HBM: the slots seen are read once per 32 columns.
-template <typename T, int DP>
+template <typename T, int DP, int DU>
 __global__ __launch_bounds__(256, io<T>::BYTES == 2 ? 2 : 1) void attn_decode_kernel(AttnDecodeArgs a) {
-  using KV = Tile<T, DP, 32, 1>;
+  using KV = Tile<T, DP, DU, 32, 1>;
   constexpr int NW = 4, ES = io<T>::BYTES, STEPS = 32 / KV::CK, PART = 2 * KV::BYTES;
   static_assert(32 * DP * 4 <= PART, "a wave's result fits its part");
   __shared__ __attribute__((aligned(1024))) char smem[NW * PART];
@@ -86,17 +86,17 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 ? 2 : 1) void attn_decode_ke
   const int h = lane >> 5, col = lane & 31;
   const int G = a.q_heads / a.kv_heads, cols = G * a.tokens;
   const int groups = (cols + 31) / 32;
-  int64_t id = xcd_order(blockIdx.x, gridDim.x);
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int group = (int)(id % groups);
-  id /= groups;
-  const int64_t hk = id % a.kv_heads, b = id / a.kv_heads;
+  uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+  const int split = (int)(id % (uint32_t)a.splits);
+  id /= (uint32_t)a.splits;
+  const int group = (int)(id % (uint32_t)groups);
+  id /= (uint32_t)groups;
+  const int64_t hk = id % (uint32_t)a.kv_heads, b = id / (uint32_t)a.kv_heads;
   const int c0 = group * 32;
   const bool in = c0 + col < cols;
   const int tok = in ? (c0 + col) / G : 0;
   const int64_t hq = hk * G + (in ? (c0 + col) - tok * G : 0);
-  RowRegs<T, DP> q;
+  RowRegs<T, DU> q;
   q.load((const char*)a.q + ((b * a.tokens + tok) * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
 
   CacheView view;
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 ? 2 : 1) void attn_decode_ke
     end = begin + per < view.tiles() ? begin + per : view.tiles();
   }
   KV vt;
-  RowStream<T, DP> kt;
+  RowStream<T, DU> kt;
   kt.init(a.kc_stride, a.dim, lane);
   vt.init(a.vc_stride, a.dim, lane, 0);
   char* kc = (char*)a.k_cache + (b * a.capacity * a.kc_stride + hk * a.dim) * ES;
@@ -275,14 +275,44 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnDecodeArgs a)
   io<T>::store4(a.o, row * a.o_stride + (id - row * a.q_heads) * a.dim + d, f);
 }
 
+// The same for few splits: 32 threads per row and head.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_decode_join_few_kernel(AttnDecodeArgs a) {
+  const int64_t all = a.batch * a.tokens * a.q_heads, id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int d = (threadIdx.x & 31) * 4;
+  if (id >= all || d >= a.dim) return;
+  const float* stat = a.part + all * a.splits * a.dim + 2 * id * a.splits;
+  const float* part = a.part + id * a.splits * a.dim + d;
+  const float c = a.scale * kLog2e;
+  float m = -INFINITY, sum = 0.0f;
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, stat[2 * i]);
+  float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) {
+    const float w = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[2 * i] - m) * c);
+    const f32x4 x = *(const f32x4*)(part + (int64_t)i * a.dim);
+    sum += w * stat[2 * i + 1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] += w * x[j];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] *= inv;
+  const int64_t row = id / a.q_heads;
+  io<T>::store4(a.o, row * a.o_stride + (id - row * a.q_heads) * a.dim + d, f);
+}
+
 template <typename T>
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s) {
   const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
   const dim3 grid((unsigned)(a.batch * a.kv_heads * groups * a.splits)), block(256);
-  if (a.dim <= 64) hipLaunchKernelGGL((attn_decode_kernel<T, 64>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_decode_kernel<T, 128>), grid, block, 0, s, a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)(a.batch * a.tokens * a.q_heads)), block, 0, s, a);
+  with_width(a.dim, [&](auto dp, auto du) {
+    hipLaunchKernelGGL((attn_decode_kernel<T, decltype(dp)::value, decltype(du)::value>), grid, block, 0, s, a);
+  });
+  const int64_t rows = a.batch * a.tokens * a.q_heads;
+  if (a.splits > 16) hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)rows), block, 0, s, a);
+  else if (a.splits > 1)
+    hipLaunchKernelGGL((attn_decode_join_few_kernel<T>), dim3((unsigned)((rows + 7) / 8)), block, 0, s, a);
   return hipGetLastError();
 }
 

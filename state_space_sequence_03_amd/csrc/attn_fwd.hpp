@@ -16,9 +16,9 @@ namespace m3 {
 // Two blocks share a CU, so that one's softmax (vector units) runs under the
 // other's products (matrix cores).  They overlap in part only: products alone
 // would take 0.53 of the time, the softmax 0.65.
-template <typename T, int DP, int BN, int HT>
+template <typename T, int DP, int DU, int BN, int HT>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
-  using KV = Tile<T, DP, BN, 4>;
+  using KV = Tile<T, DP, DU, BN, 4>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   const int G = a.q_heads / a.kv_heads;
   // heads that share keys are neighbours, then the tiles of a sequence, the
   // longest first
-  const uint32_t id = (uint32_t)xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
+  const uint32_t id = xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
   const int64_t hk = kg / (uint32_t)items;
   AttnSeq s;
   int t;
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   const int p0 = s.past() + t * BM, p1 = s.past() + (s.nq < t * BM + BM ? s.nq : t * BM + BM) - 1;
   const int w0 = p0 + wave / HT * 32, w1 = w0 + 31 < p1 ? w0 + 31 : p1;
   const int64_t row = s.q0 + (in ? r : s.nq - 1);
-  RowRegs<T, DP> q;
+  RowRegs<T, DU> q;
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
 
   KV kt, vt;
@@ -113,8 +113,10 @@ void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
   const int64_t items = attn_items(a, false, 128 / HT);
   const dim3 grid((unsigned)(items * (a.q_heads / HT))), block(256);
   constexpr int BN = io<T>::BYTES == 2 ? 64 : 32;
-  if (a.dim <= 64) hipLaunchKernelGGL((attn_fwd_kernel<T, 64, BN, HT>), grid, block, 0, s, a, items);
-  else hipLaunchKernelGGL((attn_fwd_kernel<T, 128, BN, HT>), grid, block, 0, s, a, items);
+  with_width(a.dim, [&](auto dp, auto du) {
+    hipLaunchKernelGGL((attn_fwd_kernel<T, decltype(dp)::value, decltype(du)::value, BN, HT>), grid, block, 0, s, a,
+                       items);
+  });
 }
 
 template <typename T>
