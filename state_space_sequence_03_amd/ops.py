@@ -775,18 +775,20 @@ def _tokens(name, t, shape, dtype, device):
     st = t.stride()
     heads, dim = shape[-2:]
     if (dim == 1 or st[-1] == 1) and (heads == 1 or st[-2] == dim):
-        step = 0    # elements between tokens; dimensions of one entry say nothing
-        inner = 1   # tokens that the dimensions looked at so far hold
+        step = None  # elements between tokens; dimensions of one entry say nothing
+        inner = 1    # tokens that the dimensions looked at so far hold
         for i in range(len(shape) - 3, -1, -1):
             n = shape[i]
             if n != 1:
-                if step == 0:
+                if step is None:
                     step = st[i]
                 elif st[i] != inner * step:
                     break
                 inner *= n
         else:
-            if step == 0 or step >= heads * dim:
+            if step is None:
+                return t.data_ptr(), 0
+            if step >= heads * dim:
                 return t.data_ptr(), step
     raise ValueError(f"{name}: must be contiguous, or with heads side by side and evenly spaced tokens")
 
