@@ -84,12 +84,19 @@ inline int64_t attn_items(const AttnArgs& a, bool keys, int tile) {
   return a.rows / tile + (a.batch < a.rows ? a.batch : a.rows);
 }
 
+// Whether blocks of four waves, 128 queries of a head, are too few to occupy the
+// chip: fp32 kernels, bound by their products, then take blocks of one wave (2 x
+// 777 queries, 5 heads of 72: forward 35 -> 27 us, dq 53 -> 36; bf16 gains nothing).
+inline bool attn_few(const AttnArgs& a) { return attn_items(a, false, 128) * a.q_heads < 256; }
+
 // Pieces of the sequences that are longer than one, at most.
 inline int64_t attn_pieces(const AttnArgs& a) {
   if (a.sinks == 0 || a.window >= kNoWindow) return 0;
   if (!a.starts) return a.q_len > a.piece ? a.batch * ((a.q_len + a.piece - 1) / a.piece) : 0;
   return a.rows / a.piece * 2;  // a sequence of more than a piece has fewer pieces than twice its whole ones
 }
+
+inline int64_t attn_piece_blocks(const AttnArgs& a) { return attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads; }
 
 // Blocks go to the 8 XCDs in turn, each with an L2 of its own: XCD x gets the
 // x-th contiguous eighth of the work, whose neighbours share keys and values.

@@ -39,12 +39,13 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a) {
 // The lse2 and delta of BQ queries in LDS, a load of 4 bytes per lane each.
 template <int BQ>
 __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int rows, float* lds, int wave) {
+#if defined(__HIP_DEVICE_COMPILE__)
   if (wave > 1) return;
-  const float* src = (wave ? a.delta : a.lse2) + at;
-  const int n = rows < BQ ? rows : BQ;
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, (uint32_t)(n * 4), 0x00020000);
-  const int lane = threadIdx.x & 63;
+  const int n = rows < BQ ? rows : BQ, lane = threadIdx.x & 63;
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc((void*)((wave ? a.delta : a.lse2) + at), 0, (uint32_t)(n * 4), 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + wave * 64), 4, lane < BQ ? lane * 4 : kFar, 0, 0, 0);
+#endif
 }
 
 // dk and dv of 128 keys: each wave holds 32 of them as the columns of its
@@ -58,12 +59,16 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // takes every fourth 32; the four sums go to the workspace in fp32 and are
 // joined in order.
 //
+// Where the keys' tiles alone would leave the chip half empty, a.splits blocks
+// share one, and a piece: each takes its part of the list of (head, queries) and
+// its sums go to the workspace as well.
+//
 // Two waves share a SIMD, which the registers just allow (fragments three
 // products ahead: 620 us for 8 x 4096 queries, 16/4 heads of 128, window 1024;
 // six ahead with spills 740, one wave per SIMD 780).
 template <typename T, int DP, int DU, int BQ>
-__global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a, int64_t items,
-                                                                                             int64_t pieces) {
+__global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(
+    AttnArgs a, int64_t items, int64_t pieces) {
   using QD = Tile<T, DP, DU, BQ, 4>;
   constexpr int ES = io<T>::BYTES, STEPS = 32 / QD::CK, AHEAD = 3;
   constexpr int STAGE = 2 * QD::BYTES + 512;  // Q, dO, statistics
@@ -75,19 +80,23 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   const int sunk = (a.sinks + 31) / 32;
   const bool cut = blockIdx.x < pieces;
   AttnSeq s;
-  int jw, piece = 0;  // the wave's first key
+  int jw, piece = 0, split = 0;  // jw: the wave's first key
   int64_t hk;
+  uint32_t item = 0;
   if (cut) {
-    const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;
-    hk = blockIdx.x % (uint32_t)a.kv_heads;
+    const uint32_t at = blockIdx.x / (uint32_t)a.splits, id = at / (uint32_t)a.kv_heads;
+    split = (int)(blockIdx.x % (uint32_t)a.splits);
+    hk = at % (uint32_t)a.kv_heads;
     jw = (int)(id % (uint32_t)sunk) * 32;
     if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
     if (jw >= s.nk) return;
   } else {
     const uint32_t id = xcd_order(blockIdx.x - (uint32_t)pieces, gridDim.x - (uint32_t)pieces);
     int t;
-    hk = id / (uint32_t)items;
-    if (!attn_item<true>(a, id % (uint32_t)items, 128, 0, s, t)) return;
+    item = id / (uint32_t)a.splits;
+    split = (int)(id % (uint32_t)a.splits);
+    hk = item / (uint32_t)items;
+    if (!attn_item<true>(a, item % (uint32_t)items, 128, 0, s, t)) return;
     jw = t * 128 + wave * 32;
   }
   const bool apart = s.nq > a.piece;  // the sinks are summed in pieces
@@ -105,7 +114,8 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
     if (last < r1) r1 = (int)last;
   }
   r0 = r0 / BQ * BQ;  // whole tiles, so that a piece's last one ends with it
-  const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, count = per * G;
+  const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, all = per * G;
+  const int begin = (int)((int64_t)all * split / a.splits), count = (int)((int64_t)all * (split + 1) / a.splits) - begin;
 
   const int64_t row = s.k0 + (in ? j : s.nk - 1);
   RowRegs<T, DU> k, v;
@@ -125,8 +135,8 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
 #pragma unroll
   for (int i = 0; i < QD::CT; ++i) dk[i] = dv[i] = f32x16{};
   const float c = a.scale * kLog2e;
-  int head = 0, r = r0;
-  if (count > 0) load(0, r0, 0);
+  int head = per > 0 ? begin / per : 0, r = r0 + (begin - head * per) * BQ;
+  if (count > 0) load(head, r, 0);
   for (int n = 0; n < count; ++n) {
     attn_settle();
     int next = r + BQ, other = head;
@@ -184,9 +194,10 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
     head = other;
     r = next;
   }
-  if (cut) {
-    // (dk, dv; wave; 32 keys; dim) per piece
-    float* part = a.part + ((int64_t)blockIdx.x * 8 + wave) * 32 * a.dim + (int64_t)(lane & 31) * a.dim;
+  if (cut || a.splits > 1) {
+    // per split of a piece, and behind those of an item: (dk, dv; wave; 32 keys; dim)
+    const int64_t at = cut ? blockIdx.x : pieces + (int64_t)item * a.splits + split;
+    float* part = a.part + (at * 8 + wave) * 32 * a.dim + (int64_t)(lane & 31) * a.dim;
 #pragma unroll
     for (int d = 0; d < QD::CT; ++d) {
       if (d * 32 >= a.dim) break;
@@ -213,12 +224,14 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
 }
 
-// The pieces of 32 keys joined in order, four entries to a thread; the blocks
-// of their pieces share the entries.
+// The sums of 32 keys' pieces joined in order: the blocks of the pieces (and
+// blockIdx.z) share the keys' entries, 128 at a time; eight groups of threads
+// each add an eighth of the sums, four entries to a thread.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  __shared__ f32x4 sums[8][32];
   const int sunk = (a.sinks + 31) / 32;
-  const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;
+  const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;  // of a piece, all its splits
   const int64_t hk = blockIdx.x % (uint32_t)a.kv_heads;
   const int j0 = (int)(id % (uint32_t)sunk) * 32;
   AttnSeq s;
@@ -227,22 +240,65 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int keys = s.nk - j0 < 32 ? s.nk - j0 : 32;
   if (keys <= 0) return;
   const int pieces = (s.nq + a.piece - 1) / a.piece;
-  const int64_t half = 32 * a.dim, step = (int64_t)sunk * a.kv_heads * 8 * half;  // from piece to piece
   const bool key = blockIdx.y == 0;
   void* out = key ? a.dk : a.dv;
   if (!out) return;
-  const float* part = a.part + (int64_t)blockIdx.x * 8 * half - piece * step + (key ? 0 : 4 * half);
-  const int n = keys * a.dim;
-  for (int e = (piece * 256 + (int)threadIdx.x) * 4; e < n; e += pieces * 1024) {
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-    for (int i = 0; i < pieces; ++i)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const f32x4 y = *(const f32x4*)(part + i * step + w * half + e);
+  const int64_t half = 32 * a.dim, one = 8 * half;                   // of four waves, of a split
+  const int64_t step = (int64_t)sunk * a.kv_heads * a.splits * one;  // from piece to piece
+  const float* part = a.part + (int64_t)blockIdx.x * a.splits * one - piece * step + (key ? 0 : 4 * half);
+  const int n = keys * a.dim, parts = a.splits * 4, g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int c = (piece * gridDim.z + blockIdx.z) * 128; c < n; c += pieces * gridDim.z * 128) {
+    const int e = c + lane * 4;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (e < n) {
+#pragma unroll 4
+      for (int w = g; w < pieces * parts; w += 8) {
+        const int i = w / parts, u = w - i * parts;
+        const f32x4 y = *(const f32x4*)(part + i * step + (u >> 2) * one + (u & 3) * half + e);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] += y[j];
       }
+    }
+    __syncthreads();
+    sums[g][lane] = x;
+    __syncthreads();
+    if (g == 0 && e < n) {
+      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] += sums[i][lane][j];
+      const int j = e / a.dim;
+      io<T>::store4(out, (s.k0 + j0 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, f);
+    }
+  }
+}
+
+// The splits of 128 keys joined in order (those of the sinks that are summed in
+// pieces excepted): a block per item, dk and dv by blockIdx.y, a quarter of the
+// keys by blockIdx.z.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64_t items, int64_t pieces) {
+  const int64_t hk = blockIdx.x / (uint32_t)items;
+  AttnSeq s;
+  int t;
+  if (!attn_item<true>(a, blockIdx.x % (uint32_t)items, 128, 0, s, t)) return;
+  const int j0 = t * 128 + blockIdx.z * 32;
+  if (s.nq > a.piece && j0 < (a.sinks + 31) / 32 * 32) return;
+  const bool key = blockIdx.y == 0;
+  void* out = key ? a.dk : a.dv;
+  if (!out) return;
+  const int keys = s.nk - j0 < 32 ? s.nk - j0 : 32, n = keys * a.dim;
+  const int64_t wave = 32 * a.dim;
+  const float* part = a.part + ((pieces + (int64_t)blockIdx.x * a.splits) * 8 + (key ? 0 : 4) + blockIdx.z) * wave;
+  for (int e = (int)threadIdx.x * 4; e < n; e += 1024) {
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < a.splits; ++i) {
+      const f32x4 y = *(const f32x4*)(part + i * 8 * wave + e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] += y[j];
+    }
     const int j = e / a.dim;
     io<T>::store4(out, (s.k0 + j0 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, x);
   }
@@ -252,10 +308,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
 // dq^T += K^T ds) and walks the keys they see as the forward does.  It comes
 // first and leaves the queries' statistics to the other kernel.
-template <typename T, int DP, int DU, int BN, int HT>
-__global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
-  using KV = Tile<T, DP, DU, BN, 4>;
-  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT, HALF = 32 * KV::ROWB;
+template <typename T, int DP, int DU, int BN, int HT, int NW>
+__global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
+  using KV = Tile<T, DP, DU, BN, NW>;
+  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT, HALF = 32 * KV::ROWB;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -360,31 +416,33 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
 }
 
-template <typename T, int DP, int DU, int HT>
+template <typename T, int DP, int DU, int HT, int NW>
 void attn_dq_run(const AttnArgs& a, hipStream_t s) {
-  const int64_t items = attn_items(a, false, 128 / HT);
+  const int64_t items = attn_items(a, false, 32 * NW / HT);
   if (items > 0)
-    hipLaunchKernelGGL((attn_dq_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32, HT>),
-                       dim3((unsigned)(items * (a.q_heads / HT))), dim3(256), 0, s, a, items);
+    hipLaunchKernelGGL((attn_dq_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32, HT, NW>),
+                       dim3((unsigned)(items * (a.q_heads / HT))), dim3(64 * NW), 0, s, a, items);
 }
 
 template <typename T, int DP, int DU>
 void attn_bwd_run(const AttnArgs& a, hipStream_t s) {
-  constexpr int BQ = io<T>::BYTES == 2 ? 64 : 32;
+  const int64_t vectors = a.rows * a.q_heads;
   const dim3 block(256);
-  const int64_t vectors = a.rows * a.q_heads, tiles = attn_items(a, true, 128);
   const int G = a.q_heads / a.kv_heads;
-  if (a.dq && G % 4 == 0) attn_dq_run<T, DP, DU, 4>(a, s);
-  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, DU, 2>(a, s);
-  else if (a.dq) attn_dq_run<T, DP, DU, 1>(a, s);
+  if (a.dq && io<T>::BYTES == 4 && attn_few(a)) attn_dq_run<T, DP, DU, 1, io<T>::BYTES == 4 ? 1 : 4>(a, s);
+  else if (a.dq && G % 4 == 0) attn_dq_run<T, DP, DU, 4, 4>(a, s);
+  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, DU, 2, 4>(a, s);
+  else if (a.dq) attn_dq_run<T, DP, DU, 1, 4>(a, s);
   else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);
-  if ((a.dk || a.dv) && tiles > 0) {
-    const int64_t pieces = attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads;
-    hipLaunchKernelGGL((attn_dkv_kernel<T, DP, DU, BQ>), dim3((unsigned)(pieces + tiles * a.kv_heads)), block, 0, s, a,
-                       tiles, pieces);
-    if (pieces > 0) hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)pieces, 2), block, 0, s, a);
-  }
+  const int64_t tiles = attn_items(a, true, 128), pieces = attn_piece_blocks(a) * a.splits, blocks = tiles * a.kv_heads;
+  if ((!a.dk && !a.dv) || tiles == 0) return;
+  hipLaunchKernelGGL((attn_dkv_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32>),
+                     dim3((unsigned)(pieces + blocks * a.splits)), block, 0, s, a, tiles, pieces);
+  if (pieces > 0)
+    hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)(pieces / a.splits), 2, 8), block, 0, s, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((attn_join_splits_kernel<T>), dim3((unsigned)blocks, 2, 4), block, 0, s, a, tiles, pieces);
 }
 
 template <typename T>

@@ -35,8 +35,23 @@ int attn_bwd_piece(const AttnArgs& a) {
   n = (n + 127) / 128 * 128;
   return (int)(n < (1 << 25) ? n : 1 << 25);
 }
+// Blocks that share a tile of 128 keys, where there are too few of those: two
+// steps of 64 queries for each at least.  (1 x 2048 queries, 16/4 heads of 64, no
+// window: dk and dv 176 us with one, 47 with six; from 192 tiles on one each is
+// faster: 4 x 2048, window 512, 103 us, 124 with two.)
+int attn_bwd_splits(const AttnArgs& a) {
+  const int64_t blocks = attn_items(a, true, 128) * a.kv_heads;
+  if (blocks == 0 || blocks >= 192) return 1;
+  int64_t rows = a.starts ? a.rows : a.q_len;
+  if (a.window < kNoWindow && rows > (int64_t)a.window + 128) rows = (int64_t)a.window + 128;
+  const int64_t most = (rows + 63) / 64 * (a.q_heads / a.kv_heads) / 2;
+  int64_t n = (384 + blocks - 1) / blocks;
+  n = n < most ? n : most;
+  return n < 1 ? 1 : n < 16 ? (int)n : 16;
+}
 size_t attn_bwd_part_bytes(const AttnArgs& a) {
-  return (size_t)attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads * 8 * 32 * a.dim * 4;
+  const int64_t shared = a.splits > 1 ? attn_items(a, true, 128) * a.kv_heads : 0;
+  return (size_t)(attn_piece_blocks(a) + shared) * a.splits * 8 * 32 * a.dim * 4;
 }
 
 }  // namespace m3

@@ -16,10 +16,10 @@ namespace m3 {
 // Two blocks share a CU, so that one's softmax (vector units) runs under the
 // other's products (matrix cores).  They overlap in part only: products alone
 // would take 0.53 of the time, the softmax 0.65.
-template <typename T, int DP, int DU, int BN, int HT>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
-  using KV = Tile<T, DP, DU, BN, 4>;
-  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 128 / HT;
+template <typename T, int DP, int DU, int BN, int HT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
+  using KV = Tile<T, DP, DU, BN, NW>;
+  constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT;
   __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -108,13 +108,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int64_t it
   }
 }
 
-template <typename T, int HT>
+template <typename T, int HT, int NW>
 void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
-  const int64_t items = attn_items(a, false, 128 / HT);
-  const dim3 grid((unsigned)(items * (a.q_heads / HT))), block(256);
+  const int64_t items = attn_items(a, false, 32 * NW / HT);
+  const dim3 grid((unsigned)(items * (a.q_heads / HT))), block(64 * NW);
   constexpr int BN = io<T>::BYTES == 2 ? 64 : 32;
   with_width(a.dim, [&](auto dp, auto du) {
-    hipLaunchKernelGGL((attn_fwd_kernel<T, decltype(dp)::value, decltype(du)::value, BN, HT>), grid, block, 0, s, a,
+    hipLaunchKernelGGL((attn_fwd_kernel<T, decltype(dp)::value, decltype(du)::value, BN, HT, NW>), grid, block, 0, s, a,
                        items);
   });
 }
@@ -122,9 +122,10 @@ void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
   const int G = a.q_heads / a.kv_heads;
-  if (G % 4 == 0) attn_fwd_run<T, 4>(a, s);
-  else if (G % 2 == 0) attn_fwd_run<T, 2>(a, s);
-  else attn_fwd_run<T, 1>(a, s);
+  if (io<T>::BYTES == 4 && attn_few(a)) attn_fwd_run<T, 1, io<T>::BYTES == 4 ? 1 : 4>(a, s);
+  else if (G % 4 == 0) attn_fwd_run<T, 4, 4>(a, s);
+  else if (G % 2 == 0) attn_fwd_run<T, 2, 4>(a, s);
+  else attn_fwd_run<T, 1, 4>(a, s);
   return hipGetLastError();
 }
 

@@ -287,11 +287,13 @@ struct AttnArgs {
   void *dq, *dk, *dv;  // each nullable
   int64_t do_stride, dq_stride, dk_stride, dv_stride;
   float *lse2, *delta;  // workspace: (q_heads, rows): lse in powers of two (+inf for a row that sees nothing), rowsum(do o)
-  float* part;          // workspace of the sinks' tiles
+  float* part;          // workspace of partial sums
   int piece;            // queries of a piece of a sinks' tile
+  int splits;           // blocks that share a tile of keys
 };
 size_t attn_bwd_part_bytes(const AttnArgs& a);
 int attn_bwd_piece(const AttnArgs& a);
+int attn_bwd_splits(const AttnArgs& a);
 template <typename T>
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 template <typename T>

@@ -764,6 +764,12 @@ def mamba3_gated_ffn_bwd(x, W, dh, pre, *, act=M3_ACT_SILU, want_dx=True, want_d
 # the attention layer beside the core: norms of queries and keys with their
 # rotation, windowed attention with sinks, the same over a cache
 # ---------------------------------------------------------------------------
+def _empty(t):
+    """A contiguous tensor like t."""
+    torch = _torch()
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _tokens(name, t, shape, dtype, device):
     """(pointer, elements from token to token; 0: contiguous) of an operand of
     the given shape (..., heads, dim): contiguous, or with heads side by side
@@ -858,14 +864,14 @@ def mamba3_qk_norm_rope_fwd(q, k, gain_q=None, gain_k=None, eps=1e-5, *, theta=N
     if qs is None:
         q_out = None
     elif q_out is None:
-        q_out = q.new_empty(qs)
+        q_out = _empty(q)
         pqo = q_out.data_ptr()
     else:
         pqo, dims.q_out_stride = _tokens("q_out", q_out, qs, io, dev)
     if ks is None:
         k_out = None
     elif k_out is None:
-        k_out = k.new_empty(ks)
+        k_out = _empty(k)
         pko = k_out.data_ptr()
     else:
         pko, dims.k_out_stride = _tokens("k_out", k_out, ks, io, dev)
@@ -898,7 +904,7 @@ def mamba3_qk_norm_rope_bwd(q, k, dq_out, dk_out, gain_q=None, gain_k=None, eps=
             raise ValueError("dq_out is required with q")
         pdqo, dims.q_out_stride = _tokens("dq_out", dq_out, qs, io, dev)
         if dq is None:
-            dq = q.new_empty(qs)
+            dq = _empty(q)
             pdq = dq.data_ptr()
         else:
             pdq, dims.dq_stride = _tokens("dq", dq, qs, io, dev)
@@ -912,7 +918,7 @@ def mamba3_qk_norm_rope_bwd(q, k, dq_out, dk_out, gain_q=None, gain_k=None, eps=
             raise ValueError("dk_out is required with k")
         pdko, dims.k_out_stride = _tokens("dk_out", dk_out, ks, io, dev)
         if dk is None:
-            dk = k.new_empty(ks)
+            dk = _empty(k)
             pdk = dk.data_ptr()
         else:
             pdk, dims.dk_stride = _tokens("dk", dk, ks, io, dev)
@@ -984,7 +990,7 @@ def mamba3_window_attn_fwd(q, k, v, *, window=0, sinks=0, scale=None, starts=Non
                           starts=starts, o=o, lse=lse, want_lse=want_lse)
     dims, (pq, pk, pv, ps), qs, _, io, dev = _attn_dims(q, k, v, starts, window, sinks, scale)
     if o is None:
-        o = q.new_empty(qs)
+        o = _empty(q)
         po = o.data_ptr()
     else:
         po, dims.o_stride = _tokens("o", o, qs, io, dev)
@@ -1023,17 +1029,17 @@ def mamba3_window_attn_bwd(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None
     if dq is not None:
         out["dq"], (pdq, dims.dq_stride) = dq, _tokens("dq", dq, qs, io, dev)
     elif want_dq:
-        out["dq"] = dq = q.new_empty(qs)
+        out["dq"] = dq = _empty(q)
         pdq = dq.data_ptr()
     if dk is not None:
         out["dk"], (pdk, dims.dk_stride) = dk, _tokens("dk", dk, ks, io, dev)
     elif want_dk:
-        out["dk"] = dk = q.new_empty(ks)
+        out["dk"] = dk = _empty(k)
         pdk = dk.data_ptr()
     if dv is not None:
         out["dv"], (pdv, dims.dv_stride) = dv, _tokens("dv", dv, ks, io, dev)
     elif want_dv:
-        out["dv"] = dv = q.new_empty(ks)
+        out["dv"] = dv = _empty(v)
         pdv = dv.data_ptr()
     if dims.kv_rows and (dk is not None or dv is not None):
         raise ValueError("gradients of keys that are part of a longer cache: pass k and v as contiguous sequences")
@@ -1072,7 +1078,7 @@ def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sink
     pvc, svc = _tokens("v_cache", v_cache, cs, io, dev)
     so = 0
     if o is None:
-        o = q.new_empty(qs)
+        o = _empty(q)
         po = o.data_ptr()
     else:
         po, so = _tokens("o", o, qs, io, dev)
