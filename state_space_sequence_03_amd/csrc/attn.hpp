@@ -318,22 +318,6 @@ __device__ __forceinline__ void attn_settle() {
   asm volatile("" ::: "memory");
 }
 
-// A barrier of the block that code does not move across; loads into LDS that
-// the wave has in flight may go on.
-__device__ __forceinline__ void attn_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-// ... the wave's own have landed
-__device__ __forceinline__ void attn_landed() {
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // The softmax of 32 columns over rows that come in pieces: weights against a
 // running reference m of each column, their sum, and the result's columns scaled
 // along when m moves.

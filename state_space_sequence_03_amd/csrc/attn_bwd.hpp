@@ -171,8 +171,11 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
       if (!sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) {
         asm volatile("");  // a branch, not selects in every step
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks)) p[i] = ds[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) {
+          const bool seen = sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks);
+          p[i] = seen ? p[i] : 0.0f;
+          ds[i] = seen ? ds[i] : 0.0f;
+        }
       }
       uint4 w[2][STEPS];
 #pragma unroll
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
         asm volatile("");  // a branch, not selects in every step
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (!sees(p, j0 + i / 4 * 8 + 4 * h + i % 4, a.window, a.sinks)) ds[i] = 0.0f;
+          ds[i] = sees(p, j0 + i / 4 * 8 + 4 * h + i % 4, a.window, a.sinks) ? ds[i] : 0.0f;
       }
       uint4 w[STEPS];
 #pragma unroll

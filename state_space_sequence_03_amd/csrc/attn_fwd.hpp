@@ -83,8 +83,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
     if (!sees_all(w0, w1, j0, j0 + BN - 1, a.window, a.sinks)) {
       asm volatile("");  // a branch, not selects in every step
 #pragma unroll
-      for (int v = 0; v < NT * 16; ++v)
-        if (!sees(p, j0 + v / 16 * 32 + v % 16 / 4 * 8 + 4 * h + v % 4, a.window, a.sinks)) z[v] = -INFINITY;
+      for (int v = 0; v < NT * 16; ++v) {
+        const int j = j0 + v / 16 * 32 + v % 16 / 4 * 8 + 4 * h + v % 4;
+        z[v] = sees(p, j, a.window, a.sinks) ? z[v] : -INFINITY;
+      }
     }
     soft.template step<NT * 16>(z, c, acc, e);
     uint4 w[NT * STEPS];
