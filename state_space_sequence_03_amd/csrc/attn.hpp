@@ -105,11 +105,23 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t i, uint32_t n) {
   return x * per + (x < rem ? x : rem) + (i >> 3);
 }
 
-// Whether key j is seen from position p.
-__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
-  return j <= p && (p - j < window || j < sinks);
-}
-// ... every key of [j0, j1] from every position of [p0, p1]
+// Position p sees key j when j <= p and (j > p - window or j < sinks).  Which of
+// a lane's rows of scores that is, with both taken from where the rows start
+// (lengths stay below 2^24): three comparisons with a constant each.
+struct KeysSeen {
+  int last, out, sinks;
+  __device__ __forceinline__ KeysSeen(const AttnArgs& a, int p, int j0)
+      : last(p - j0), out(p - j0 - a.window), sinks(a.sinks - j0) {}
+  __device__ __forceinline__ bool operator()(int k) const { return (k <= last) & ((k > out) | (k < sinks)); }
+};
+// ... where the rows are positions, from p0 on
+struct QueriesSeeing {
+  int first, end;
+  __device__ __forceinline__ QueriesSeeing(const AttnArgs& a, int p0, int j)
+      : first(j - p0), end(j < a.sinks ? 1 << 30 : j - p0 + a.window) {}
+  __device__ __forceinline__ bool operator()(int k) const { return (k >= first) & (k < end); }
+};
+// Whether every key of [j0, j1] is seen from every position of [p0, p1].
 __device__ __forceinline__ bool sees_all(int p0, int p1, int j0, int j1, int window, int sinks) {
   return j1 <= p0 && (p1 - j0 < window || j1 < sinks);
 }
@@ -185,6 +197,20 @@ struct Tile {
     for (int i = 0; i < NI; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * NW + wave) * 1024), 16, voff[i % NV],
                                                i * NW * RPI * ldb, 0, 0);
+#endif
+  }
+  // ... its rows [32 t, 32 t + 32) alone; rows: 0 or fewer read nothing
+  __device__ __forceinline__ void load32(const char* base, int rows, int width, char* lds, int wave, int t) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int N = 32 / (NW * RPI);
+    static_assert(N * NW * RPI == 32, "whole loads");
+    const int n = rows < 32 ? rows : 32;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)base, 0, n > 0 ? (uint32_t)((n - 1) * ldb + width * ES) : 0u, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + ((t * N + i) * NW + wave) * 1024), 16,
+                                               voff[(t * N + i) % NV], i * NW * RPI * ldb, 0, 0);
 #endif
   }
   // rows [32 t, 32 t + 32) as an operand whose sum runs over the columns, step s

@@ -170,11 +170,12 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
       }
       if (!sees_all(p0, p0 + 31, jw, jw + 31, a.window, a.sinks)) {
         asm volatile("");  // a branch, not selects in every step
+        const QueriesSeeing seen(a, p0 + 4 * h, j);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const bool seen = sees(p0 + i / 4 * 8 + 4 * h + i % 4, j, a.window, a.sinks);
-          p[i] = seen ? p[i] : 0.0f;
-          ds[i] = seen ? ds[i] : 0.0f;
+          const bool in = seen(i / 4 * 8 + i % 4);
+          p[i] = in ? p[i] : 0.0f;
+          ds[i] = in ? ds[i] : 0.0f;
         }
       }
       uint4 w[2][STEPS];
@@ -396,9 +397,9 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
       for (int i = 0; i < 16; ++i) ds[i] = __builtin_amdgcn_exp2f(fmaf(x[0][i], c, -l2)) * (x[1][i] - delta);
       if (!sees_all(w0, w1, j0, j0 + 31, a.window, a.sinks)) {
         asm volatile("");  // a branch, not selects in every step
+        const KeysSeen seen(a, p, j0 + 4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          ds[i] = sees(p, j0 + i / 4 * 8 + 4 * h + i % 4, a.window, a.sinks) ? ds[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) ds[i] = seen(i / 4 * 8 + i % 4) ? ds[i] : 0.0f;
       }
       uint4 w[STEPS];
 #pragma unroll

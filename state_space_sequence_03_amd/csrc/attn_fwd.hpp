@@ -9,8 +9,8 @@ namespace m3 {
 // share a head of keys, each wave 32 of one head as the columns of its products:
 // scores = K q^T, o^T += V^T p.  (As many heads as there are, up to 4: the fewer
 // positions, the fewer keys that only some of the block's queries see.)  The
-// block walks the tiles of BN keys that its queries see, the sinks' first, then
-// the window's.  Keys and values come straight from memory into LDS, the next tile's while
+// block walks the runs of 32 keys that its queries see, the sinks' first, then
+// the window's, BN / 32 at a time.  Keys and values come straight from memory into LDS, the next tile's while
 // this one's products run.
 //
 // Two blocks share a CU, so that one's softmax (vector units) runs under the
@@ -50,14 +50,31 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
   const char* kb = (const char*)a.k + (s.k0 * a.k_stride + hk * a.dim) * ES;
   const char* vb = (const char*)a.v + (s.k0 * a.v_stride + hk * a.dim) * ES;
   int first = p0 - a.window + 1;
-  first = first < 0 ? 0 : first / BN;
-  const int sunk = (a.sinks + BN - 1) / BN, ns = sunk < first ? sunk : first;
-  const int count = p1 < 0 ? 0 : ns + p1 / BN - first + 1;
-  auto first_key = [&](int n) { return (n < ns ? n : first + n - ns) * BN; };
-  auto load = [&](int n, int buf) {
-    const int64_t j0 = first_key(n);
-    kt.load(kb + j0 * a.k_stride * ES, s.nk - (int)j0, a.dim, smem + buf * 2 * KV::BYTES, wave);
-    vt.load(vb + j0 * a.v_stride * ES, s.nk - (int)j0, a.dim, smem + (buf * 2 + 1) * KV::BYTES, wave);
+  first = first < 0 ? 0 : first / 32;
+  const int sunk = (a.sinks + 31) / 32, ns = sunk < first ? sunk : first;
+  const int units = p1 < 0 ? 0 : ns + p1 / 32 - first + 1, count = (units + NT - 1) / NT;
+  // the runs in order, each loaded as its turn comes: its first key (past every
+  // position: there is none)
+  int u = 0, next = ns > 0 ? 0 : first * 32;
+  auto load = [&](int (&at)[NT], int buf) {
+    char* lds = smem + buf * 2 * KV::BYTES;
+    if (u >= ns && next + BN <= s.nk) {  // one after the other, as most are
+#pragma unroll
+      for (int b = 0; b < NT; ++b) at[b] = next + 32 * b;
+      kt.load(kb + (int64_t)next * a.k_stride * ES, BN, a.dim, lds, wave);
+      vt.load(vb + (int64_t)next * a.v_stride * ES, BN, a.dim, lds + KV::BYTES, wave);
+      u += NT;
+      next += BN;
+    } else {
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        at[b] = u < units ? next : 1 << 28;
+        const int64_t j = u < units ? next : 0;
+        kt.load32(kb + j * a.k_stride * ES, s.nk - at[b], a.dim, lds, wave, b);
+        vt.load32(vb + j * a.v_stride * ES, s.nk - at[b], a.dim, lds + KV::BYTES, wave, b);
+        next = ++u == ns ? first * 32 : next + 32;
+      }
+    }
   };
 
   f32x16 acc[KV::CT];
@@ -66,13 +83,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
   Softmax<KV::CT> soft;
   soft.init();
   const float c = a.scale * kLog2e;
-  if (count > 0) load(0, 0);
+  int at[NT], ahead_at[NT];
+  if (count > 0) load(ahead_at, 0);
   for (int n = 0; n < count; ++n) {
     attn_settle();
-    if (n + 1 < count) load(n + 1, (n + 1) & 1);
+#pragma unroll
+    for (int b = 0; b < NT; ++b) at[b] = ahead_at[b];
+    if (n + 1 < count) load(ahead_at, (n + 1) & 1);
     const char* kl = smem + (n & 1) * 2 * KV::BYTES;
     const char* vl = kl + KV::BYTES;
-    const int j0 = first_key(n);
     f32x16 sc[NT];
     ahead<6, KV::KS * NT, 1, T>(
         [&](int i) { return kt.row(kl, i % NT, i / NT); },
@@ -80,12 +99,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
     float z[NT * 16], e[NT * 16];
 #pragma unroll
     for (int v = 0; v < NT * 16; ++v) z[v] = sc[v / 16][v % 16];
-    if (!sees_all(w0, w1, j0, j0 + BN - 1, a.window, a.sinks)) {
+    if (at[NT - 1] + 31 > w0 || (at[0] <= w1 - a.window && at[NT - 1] + 31 >= a.sinks)) {
       asm volatile("");  // a branch, not selects in every step
 #pragma unroll
-      for (int v = 0; v < NT * 16; ++v) {
-        const int j = j0 + v / 16 * 32 + v % 16 / 4 * 8 + 4 * h + v % 4;
-        z[v] = sees(p, j, a.window, a.sinks) ? z[v] : -INFINITY;
+      for (int b = 0; b < NT; ++b) {
+        const KeysSeen seen(a, p, at[b] + 4 * h);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) z[16 * b + v] = seen(v / 4 * 8 + v % 4) ? z[16 * b + v] : -INFINITY;
       }
     }
     soft.template step<NT * 16>(z, c, acc, e);
