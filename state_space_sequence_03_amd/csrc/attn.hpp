@@ -84,10 +84,44 @@ inline int64_t attn_items(const AttnArgs& a, bool keys, int tile) {
   return a.rows / tile + (a.batch < a.rows ? a.batch : a.rows);
 }
 
-// Whether blocks of four waves, 128 queries of a head, are too few to occupy the
-// chip: fp32 kernels, bound by their products, then take blocks of one wave (2 x
-// 777 queries, 5 heads of 72: forward 35 -> 27 us, dq 53 -> 36; bf16 gains nothing).
-inline bool attn_few(const AttnArgs& a) { return attn_items(a, false, 128) * a.q_heads < 256; }
+// Which kernel of queries' blocks a call takes, by f(heads of a block, waves that
+// share tiles of keys, parts of the keys).  Blocks of four waves, 128 queries of
+// a head, that are no more than the chip's CUs leave half of each idle, or more.
+// Their keys are then walked in parts by waves of their own (1 x 2048 queries, 16
+// heads of 128, no window: forward 42.5 -> 36.5 us, dq 57 -> 49; with 512 keys or
+// fewer for a query what the parts' join costs is not made up for: 300 queries
+// 8.4 -> 8.8).  fp32 kernels, bound by their products, first take blocks of one
+// wave (2 x 777 queries, 5 heads of 72, window 100: forward 35 -> 28 us, dq 53 ->
+// 36; and 18, 23 in two parts, while those blocks are no more than the CUs).
+template <typename T, typename F>
+void attn_by_size(const AttnArgs& a, F&& f) {
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  const integral_constant<int, 4> four;
+  const int G = a.q_heads / a.kv_heads;
+  const int64_t blocks = attn_items(a, false, 128) * a.q_heads;
+  if constexpr (io<T>::BYTES == 4) {
+    if (blocks < 256) {
+      if (attn_items(a, false, 32) * a.q_heads <= 256) f(one, one, four);
+      else f(one, one, one);
+      return;
+    }
+  } else if (blocks <= 256 && (a.starts ? a.rows : (int64_t)a.kv_len) > 512 && a.window > 512) {
+    if (G % 4 == 0) f(four, four, two);
+    else if (G % 2 == 0) f(two, four, two);
+    else f(one, four, two);
+    return;
+  }
+  if (G % 4 == 0) f(four, four, one);
+  else if (G % 2 == 0) f(two, four, one);
+  else f(one, four, one);
+}
+// Parts of the keys for which a block's LDS has room.
+template <typename T, int DP>
+constexpr int attn_parts(int waves, int parts) {
+  return waves == 1 && DP == 128 && parts > 2 ? 2 : parts;
+}
 
 // Pieces of the sequences that are longer than one, at most.
 inline int64_t attn_pieces(const AttnArgs& a) {
@@ -392,5 +426,59 @@ struct Softmax {
     l += sum;
   }
 };
+
+// The results of a block's KW parts of the keys, joined in order by the first
+// part's waves (true for them): sums acc, and for a softmax (SOFT) its reference
+// m and sum l.  Each part leaves its sums in its own BYTES of LDS.
+template <int KW, int NW, int BYTES, bool SOFT, int CT>
+__device__ __forceinline__ bool join_parts(char* lds, f32x16 (&acc)[CT], float& m, float& l, float c, int part, int wave,
+                                           int lane) {
+  static_assert(NW * CT * 4096 <= BYTES, "a part's sums fit its LDS");
+  __shared__ float stat[SOFT ? KW : 1][NW][2][64];
+  attn_settle();  // the tiles are read
+  if (part > 0) {
+    f32x4* x = (f32x4*)(lds + part * BYTES + wave * CT * 4096) + lane;
+#pragma unroll
+    for (int i = 0; i < CT * 4; ++i)
+      x[i * 64] = f32x4{acc[i / 4][i % 4 * 4], acc[i / 4][i % 4 * 4 + 1], acc[i / 4][i % 4 * 4 + 2], acc[i / 4][i % 4 * 4 + 3]};
+    if constexpr (SOFT) {
+      stat[part][wave][0][lane] = m;
+      stat[part][wave][1][lane] = l;
+    }
+  }
+  __syncthreads();
+  if (part > 0) return false;
+  float f[KW];
+  f[0] = 1.0f;
+  if constexpr (SOFT) {
+    float top = m;
+#pragma unroll
+    for (int k = 1; k < KW; ++k) top = fmaxf(top, stat[k][wave][0][lane]);
+    f[0] = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
+    l *= f[0];
+#pragma unroll
+    for (int k = 1; k < KW; ++k) {
+      const float other = stat[k][wave][0][lane];
+      f[k] = other == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((other - top) * c);
+      l += f[k] * stat[k][wave][1][lane];
+    }
+    m = top;
+  }
+#pragma unroll
+  for (int i = 0; i < CT * 4; ++i) {
+    f32x4 sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = acc[i / 4][i % 4 * 4 + e] * f[0];
+#pragma unroll
+    for (int k = 1; k < KW; ++k) {
+      const f32x4 x = ((const f32x4*)(lds + k * BYTES + wave * CT * 4096))[i * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += SOFT ? f[k] * x[e] : x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i / 4][i % 4 * 4 + e] = sum[e];
+  }
+  return true;
+}
 
 }  // namespace m3

@@ -308,17 +308,18 @@ __global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64
   }
 }
 
-// dq of 128 queries, 128 / HT positions of HT heads as in the forward: each wave
-// holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
+// dq of 32 NW queries, 32 NW / HT positions of HT heads, by KW parties as in the
+// forward: each wave holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
 // dq^T += K^T ds) and walks the keys they see as the forward does.  It comes
 // first and leaves the queries' statistics to the other kernel.
-template <typename T, int DP, int DU, int BN, int HT, int NW>
-__global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
+template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
+__global__ __launch_bounds__(64 * NW * KW, NW * KW > 4 || (KW == 1 && (io<T>::BYTES == 2 || DP == 64)) ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT, HALF = 32 * KV::ROWB;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
+  __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each part
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all % NW, part = all / NW;
+  char* smem = lds + part * 4 * KV::BYTES;
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
@@ -354,7 +355,7 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
     delta = swap_sum32(delta);
   }
   const float lse = a.lse[row * a.q_heads + hq], l2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
-  if (in && h == 0) {
+  if (in && h == 0 && part == 0) {
     a.lse2[hq * a.rows + row] = l2;
     a.delta[hq * a.rows + row] = delta;
   }
@@ -378,15 +379,17 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
 #pragma unroll
   for (int i = 0; i < KV::CT; ++i) acc[i] = f32x16{};
   const float c = a.scale * kLog2e;
-  if (count > 0) load(0, 0);
-  for (int n = 0; n < count; ++n) {
+  if (part < count) load(part, 0);
+  for (int i = 0; i * KW < count; ++i) {
+    const int n = i * KW + part;
     attn_settle();
-    if (n + 1 < count) load(n + 1, (n + 1) & 1);
+    if (KW > 1 && n >= count) continue;
+    if (n + KW < count) load(n + KW, (i + 1) & 1);
 #pragma unroll 1
     for (int b = 0; b < NT; ++b) {
       const int j0 = first_key(n) + 32 * b;
       if (sees_none(w0, w1, j0, j0 + 31, a.window, a.sinks)) continue;
-      const char* kl = smem + (n & 1) * 2 * KV::BYTES + b * HALF;
+      const char* kl = smem + (i & 1) * 2 * KV::BYTES + b * HALF;
       const char* vl = kl + KV::BYTES;
       f32x16 x[2] = {f32x16{}, f32x16{}};  // scores, dp
       ahead<6, KV::KS * 2, 1, T>(
@@ -409,6 +412,10 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
           [&](int i, const uint4& f) { acc[i % KV::CT] = mma32<T>(f, w[i / KV::CT], acc[i % KV::CT]); });
     }
   }
+  if constexpr (KW > 1) {
+    float none = 0.0f;
+    if (!join_parts<KW, NW, 4 * KV::BYTES, false>(lds, acc, none, none, c, part, wave, lane)) return;
+  }
   char* out = (char*)a.dq + (row * a.dq_stride + hq * a.dim) * ES;
 #pragma unroll
   for (int d = 0; d < KV::CT; ++d) {
@@ -420,23 +427,23 @@ __global__ __launch_bounds__(64 * NW, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) voi
   }
 }
 
-template <typename T, int DP, int DU, int HT, int NW>
+template <typename T, int DP, int DU, int HT, int NW, int KW>
 void attn_dq_run(const AttnArgs& a, hipStream_t s) {
   const int64_t items = attn_items(a, false, 32 * NW / HT);
   if (items > 0)
-    hipLaunchKernelGGL((attn_dq_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32, HT, NW>),
-                       dim3((unsigned)(items * (a.q_heads / HT))), dim3(64 * NW), 0, s, a, items);
+    hipLaunchKernelGGL((attn_dq_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32, HT, NW, KW>),
+                       dim3((unsigned)(items * (a.q_heads / HT))), dim3(64 * NW * KW), 0, s, a, items);
 }
 
 template <typename T, int DP, int DU>
 void attn_bwd_run(const AttnArgs& a, hipStream_t s) {
   const int64_t vectors = a.rows * a.q_heads;
   const dim3 block(256);
-  const int G = a.q_heads / a.kv_heads;
-  if (a.dq && io<T>::BYTES == 4 && attn_few(a)) attn_dq_run<T, DP, DU, 1, io<T>::BYTES == 4 ? 1 : 4>(a, s);
-  else if (a.dq && G % 4 == 0) attn_dq_run<T, DP, DU, 4, 4>(a, s);
-  else if (a.dq && G % 2 == 0) attn_dq_run<T, DP, DU, 2, 4>(a, s);
-  else if (a.dq) attn_dq_run<T, DP, DU, 1, 4>(a, s);
+  if (a.dq)
+    attn_by_size<T>(a, [&](auto ht, auto nw, auto kw) {
+      constexpr int NW = decltype(nw)::value;
+      attn_dq_run<T, DP, DU, decltype(ht)::value, NW, attn_parts<T, DP>(NW, decltype(kw)::value)>(a, s);
+    });
   else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);
   const int64_t tiles = attn_items(a, true, 128), pieces = attn_piece_blocks(a) * a.splits, blocks = tiles * a.kv_heads;

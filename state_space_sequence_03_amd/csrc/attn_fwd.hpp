@@ -5,24 +5,31 @@
 
 namespace m3 {
 
-// A block of four waves takes 128 queries, 128 / HT positions of HT heads that
-// share a head of keys, each wave 32 of one head as the columns of its products:
+// NW waves take 32 NW queries, 32 NW / HT positions of HT heads that share a head
+// of keys, each wave 32 of one head as the columns of its products:
 // scores = K q^T, o^T += V^T p.  (As many heads as there are, up to 4: the fewer
-// positions, the fewer keys that only some of the block's queries see.)  The
-// block walks the runs of 32 keys that its queries see, the sinks' first, then
-// the window's, BN / 32 at a time.  Keys and values come straight from memory into LDS, the next tile's while
-// this one's products run.
+// positions, the fewer keys that only some of the block's queries see.)  They
+// walk the runs of 32 keys that their queries see, the sinks' first, then the
+// window's, BN / 32 at a time; with KW > 1 the block has as many such parties,
+// each with every KW-th of these tiles.  Keys and values come straight from memory
+// into LDS, the next tile's while this one's products run.
 //
-// Two blocks share a CU, so that one's softmax (vector units) runs under the
-// other's products (matrix cores).  They overlap in part only: products alone
-// would take 0.53 of the time, the softmax 0.65.
-template <typename T, int DP, int DU, int BN, int HT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
+// Bound by the vector units next to the matrix cores: two waves per SIMD (three to
+// a width of 64), so that one's softmax runs under another's products, overlap in
+// part only: at a width of 128 products alone would take 0.53 of the time, the
+// softmax 0.65.  1 x 32768 queries, 16/4 heads of 128, window 4096: 965 us, 1.07
+// PFLOP/s; 8 x 4096, window 1024: 277 us, 0.87; packed documents, 16384 rows, 32/8
+// heads of 64, window 512: 93 us.  Runs of 32 that need not be neighbours save the
+// rest of the sinks' tile and of the first of the window's: 103 -> 96 us in the
+// last of these, 29 -> 31 where there are few blocks and no window.
+template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
+__global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void attn_fwd_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * KV::BYTES];  // K V K V
+  __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all % NW, part = all / NW;
+  char* smem = lds + part * 4 * KV::BYTES;
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
   // heads that share keys are neighbours, then the tiles of a sequence, the
@@ -53,26 +60,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
   first = first < 0 ? 0 : first / 32;
   const int sunk = (a.sinks + 31) / 32, ns = sunk < first ? sunk : first;
   const int units = p1 < 0 ? 0 : ns + p1 / 32 - first + 1, count = (units + NT - 1) / NT;
-  // the runs in order, each loaded as its turn comes: its first key (past every
-  // position: there is none)
-  int u = 0, next = ns > 0 ? 0 : first * 32;
-  auto load = [&](int (&at)[NT], int buf) {
-    char* lds = smem + buf * 2 * KV::BYTES;
-    if (u >= ns && next + BN <= s.nk) {  // one after the other, as most are
+  // first keys of tile n's runs (past every position: there is none), which are
+  // loaded
+  auto load = [&](int n, int (&at)[NT], int buf) {
+    char* to = smem + buf * 2 * KV::BYTES;
+    const int next = (first + n * NT - ns) * 32;
+    if (n * NT >= ns && next + BN <= s.nk) {  // one after the other, as most are
 #pragma unroll
       for (int b = 0; b < NT; ++b) at[b] = next + 32 * b;
-      kt.load(kb + (int64_t)next * a.k_stride * ES, BN, a.dim, lds, wave);
-      vt.load(vb + (int64_t)next * a.v_stride * ES, BN, a.dim, lds + KV::BYTES, wave);
-      u += NT;
-      next += BN;
+      kt.load(kb + (int64_t)next * a.k_stride * ES, BN, a.dim, to, wave);
+      vt.load(vb + (int64_t)next * a.v_stride * ES, BN, a.dim, to + KV::BYTES, wave);
     } else {
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
-        at[b] = u < units ? next : 1 << 28;
-        const int64_t j = u < units ? next : 0;
-        kt.load32(kb + j * a.k_stride * ES, s.nk - at[b], a.dim, lds, wave, b);
-        vt.load32(vb + j * a.v_stride * ES, s.nk - at[b], a.dim, lds + KV::BYTES, wave, b);
-        next = ++u == ns ? first * 32 : next + 32;
+        const int u = n * NT + b;
+        const int64_t j = u < ns ? u * 32 : u < units ? next + 32 * b : 0;
+        at[b] = u < units ? (int)j : 1 << 28;
+        kt.load32(kb + j * a.k_stride * ES, s.nk - at[b], a.dim, to, wave, b);
+        vt.load32(vb + j * a.v_stride * ES, s.nk - at[b], a.dim, to + KV::BYTES, wave, b);
       }
     }
   };
@@ -84,13 +89,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
   soft.init();
   const float c = a.scale * kLog2e;
   int at[NT], ahead_at[NT];
-  if (count > 0) load(ahead_at, 0);
-  for (int n = 0; n < count; ++n) {
+  if (part < count) load(part, ahead_at, 0);
+  for (int i = 0; i * KW < count; ++i) {
+    const int n = i * KW + part;
     attn_settle();
+    if (KW > 1 && n >= count) continue;
 #pragma unroll
     for (int b = 0; b < NT; ++b) at[b] = ahead_at[b];
-    if (n + 1 < count) load(ahead_at, (n + 1) & 1);
-    const char* kl = smem + (n & 1) * 2 * KV::BYTES;
+    if (n + KW < count) load(n + KW, ahead_at, (i + 1) & 1);
+    const char* kl = smem + (i & 1) * 2 * KV::BYTES;
     const char* vl = kl + KV::BYTES;
     f32x16 sc[NT];
     ahead<6, KV::KS * NT, 1, T>(
@@ -116,6 +123,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
         [&](int i) { return vt.col(vl, i % KV::CT, i / KV::CT); },
         [&](int i, const uint4& f) { acc[i % KV::CT] = mma32<T>(f, w[i / KV::CT], acc[i % KV::CT]); });
   }
+  if constexpr (KW > 1)
+    if (!join_parts<KW, NW, 4 * KV::BYTES, true>(lds, acc, soft.m, soft.l, c, part, wave, lane)) return;
   const float l = swap_sum32(soft.l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing: 0
   if (a.lse && in && h == 0) a.lse[row * a.q_heads + hq] = l == 0.0f ? -INFINITY : soft.m * a.scale + logf(l);
@@ -130,24 +139,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int64_
   }
 }
 
-template <typename T, int HT, int NW>
+template <typename T, int HT, int NW, int KW>
 void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
   const int64_t items = attn_items(a, false, 32 * NW / HT);
-  const dim3 grid((unsigned)(items * (a.q_heads / HT))), block(64 * NW);
-  constexpr int BN = io<T>::BYTES == 2 ? 64 : 32;
+  const dim3 grid((unsigned)(items * (a.q_heads / HT)));
   with_width(a.dim, [&](auto dp, auto du) {
-    hipLaunchKernelGGL((attn_fwd_kernel<T, decltype(dp)::value, decltype(du)::value, BN, HT, NW>), grid, block, 0, s, a,
-                       items);
+    constexpr int DP = decltype(dp)::value, K = attn_parts<T, DP>(NW, KW), BN = io<T>::BYTES == 2 ? 64 : 32;
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, decltype(du)::value, BN, HT, NW, K>), grid, dim3(64 * NW * K), 0, s, a, items);
   });
 }
 
 template <typename T>
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
-  const int G = a.q_heads / a.kv_heads;
-  if (io<T>::BYTES == 4 && attn_few(a)) attn_fwd_run<T, 1, io<T>::BYTES == 4 ? 1 : 4>(a, s);
-  else if (G % 4 == 0) attn_fwd_run<T, 4, 4>(a, s);
-  else if (G % 2 == 0) attn_fwd_run<T, 2, 4>(a, s);
-  else attn_fwd_run<T, 1, 4>(a, s);
+  attn_by_size<T>(a, [&](auto ht, auto nw, auto kw) {
+    attn_fwd_run<T, decltype(ht)::value, decltype(nw)::value, decltype(kw)::value>(a, s);
+  });
   return hipGetLastError();
 }
 

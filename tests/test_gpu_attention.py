@@ -229,3 +229,48 @@ def test_repeats_bit_for_bit(ops):
         assert torch.equal(p, o) and torch.equal(l, lse)
         h = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
         assert all(torch.equal(h[n], g[n]) for n in g)
+
+
+# batch, q_len, kv_len, q_heads, kv_heads, D, window, sinks: few blocks of queries
+# (with more than 512 keys each: in parts), and enough to occupy the chip
+SIZES = [
+    (1, 700, 700, 4, 1, 64, 600, 40), (1, 640, 1300, 4, 2, 128, 513, 33), (2, 577, 577, 3, 3, 96, 0, 0),
+    (1, 130, 901, 2, 2, 32, 800, 100), (1, 40, 1999, 8, 2, 128, 1500, 65), (1, 700, 600, 6, 2, 72, 0, 0),
+    (14, 300, 300, 8, 2, 64, 70, 33), (9, 650, 700, 5, 5, 40, 96, 1), (13, 260, 500, 14, 7, 128, 130, 64),
+    (70, 65, 65, 4, 2, 96, 0, 0),
+]
+
+
+@pytest.mark.parametrize("B,n,m,Hq,Hk,D,window,sinks", SIZES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_few_blocks_and_many(ops, io, B, n, m, Hq, Hk, D, window, sinks):
+    print(f"attention {io} {B} x {n} of {m}, heads {Hq}/{Hk} x {D}, window {window} sinks {sinks}", flush=True)
+    r = np.random.default_rng(n + m + D)
+    q, k, v, do = (draw(r, (B, l, h, D), io) for l, h in ((n, Hq), (m, Hk), (m, Hk), (n, Hq)))
+    see = {"window": window, "sinks": sinks, "scale": 0.125}
+    o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+    torch.cuda.synchronize()
+    for b in {0, B // 2, B - 1}:
+        a = window, sinks, 0.125, b
+        check_forward(io, o[b], lse[b], q[b], k[b], v[b], *a)
+        check_backward(io, [g[x][b] for x in ("dq", "dk", "dv")], q[b], k[b], v[b], o[b], lse[b], do[b], *a)
+    assert torch.equal(ops.window_attn_fwd(q, k, v, **see)[0], o)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_scores_in_parts(ops, io, D):
+    # one part's scores far above the other's: the sharp end comes first, last, and in turns of 64 keys
+    r = np.random.default_rng(D)
+    L = 900
+    turns = np.where(np.arange(L) // 64 % 2 == 0, 0.1, 10.0)
+    q, v, do = (draw(r, (1, L, 2, D), io) for _ in range(3))
+    for ramp in (np.linspace(0.2, 12, L), np.linspace(12, 0.2, L), turns, 10.1 - turns):
+        k = (draw(r, (1, L, 2, D), "f32") * torch.from_numpy(ramp.astype(np.float32)).cuda()[None, :, None, None]).to(IO[io])
+        for window, sinks in ((0, 0), (600, 33)):
+            see = {"window": window, "sinks": sinks, "scale": 1.0}
+            o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+            check_forward(io, o[0], lse[0], q[0], k[0], v[0], window, sinks, 1.0)
+            g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
+            check_backward(io, [g[x][0] for x in ("dq", "dk", "dv")], q[0], k[0], v[0], o[0], lse[0], do[0], window, sinks, 1.0)
