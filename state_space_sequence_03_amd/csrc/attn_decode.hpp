@@ -58,11 +58,17 @@ struct CacheView {
     e = i < n0 ? end0 : end1;
     if (e > x + 32) e = x + 32;
   }
+  // whether every new token sees the 32 slots from x on (e: the tile's end)
+  __device__ __forceinline__ bool all_seen(int x, int e, int tokens, int window) const {
+    if (e - x < 32) return false;
+    if (e <= sinks) return e - 1 <= n;
+    const int r = x - sinks, rel = r <= rem ? newer + r : newer + r - ring;
+    return r >= 0 && (r <= rem) == (r + 31 <= rem) && rel + 31 <= 0 && tokens - 1 - rel < window;
+  }
   // whether new token t sees what slot x holds
   __device__ __forceinline__ bool seen(int x, int t, int window) const {
-    if (x < sinks) return x - n <= t;
-    const int r = x - sinks, rel = r <= rem ? newer + r : newer + r - ring;
-    return rel <= t && t - rel < window;
+    const int r = x - sinks, rel = newer + (r <= rem ? r : r - ring);
+    return r < 0 ? x - n <= t : (rel <= t) & (t - rel < window);
   }
 };
 
@@ -73,7 +79,12 @@ struct CacheView {
 // run, and needs no other wave until the end, when the waves' results are joined.  The new tokens' keys and
 // values are written to the cache by the wave that then reads their slots.
 //
-// Bound by HBM: the slots seen are read once per 32 columns.
+// Bound by HBM: the slots seen are read once per 32 columns.  Batch 256, 16/4
+// heads of 128, 1028 slots: 105 us, 5.1 TB/s, what a copy reaches.  Where each wave
+// has a tile or two, by the time that one takes from its lengths to its result:
+// 32768 slots of one sequence 20 us, 3.3 TB/s; 8 new tokens of 32 sequences, 32/8
+// heads of 64, about 2000 slots: 27 us.  (Without the branch around the masks, every
+// tile's 250 instructions for them came to 110, 23 and 31 us.)
 template <typename T, int DP, int DU>
 __global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 1)) void attn_decode_kernel(AttnDecodeArgs a) {
   using KV = Tile<T, DP, DU, 32, 1>;
@@ -164,9 +175,14 @@ __global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 
     for (int st = 0; st < KV::KS; ++st) sc = mma32<T>(k[st], q.v[st], sc);
     float z[16];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int j = x + v / 4 * 8 + 4 * h + v % 4;
-      z[v] = j < e && view.seen(j, tok, a.window) ? sc[v] : -INFINITY;
+    for (int v = 0; v < 16; ++v) z[v] = sc[v];
+    if (!view.all_seen(x, e, a.tokens, a.window)) {
+      asm volatile("");  // a branch, not selects in every step
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int j = x + v / 4 * 8 + 4 * h + v % 4;
+        z[v] = (j < e) & view.seen(j, tok, a.window) ? z[v] : -INFINITY;
+      }
     }
     float p[16];
     soft.template step<16>(z, c, acc, p);
@@ -275,26 +291,31 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(AttnDecodeArgs a)
   io<T>::store4(a.o, row * a.o_stride + (id - row * a.q_heads) * a.dim + d, f);
 }
 
-// The same for few splits: 32 threads per row and head.
+// The same for up to 4 splits: 32 threads per row and head, thread i with split
+// i's statistics.  (With 16 of them its row after row of partial sums takes 3 us
+// longer than the other kernel; with 2 and 8192 rows, 8 rows to a block save 7.)
 template <typename T>
 __global__ __launch_bounds__(256) void attn_decode_join_few_kernel(AttnDecodeArgs a) {
-  const int64_t all = a.batch * a.tokens * a.q_heads, id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int d = (threadIdx.x & 31) * 4;
-  if (id >= all || d >= a.dim) return;
+  const int64_t all = a.batch * a.tokens * a.q_heads, mine = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t id = mine < all ? mine : all - 1;  // a wave's threads all take part in the sums
+  const int i0 = threadIdx.x & 31, d = i0 * 4;
   const float* stat = a.part + all * a.splits * a.dim + 2 * id * a.splits;
-  const float* part = a.part + id * a.splits * a.dim + d;
-  const float c = a.scale * kLog2e;
-  float m = -INFINITY, sum = 0.0f;
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, stat[2 * i]);
+  const float* part = a.part + id * a.splits * a.dim + (d < a.dim ? d : 0);
+  const float own = i0 < a.splits ? stat[2 * i0] : -INFINITY;
+  float m = own;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const float weight = own == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((own - m) * (a.scale * kLog2e));
+  const float sum = lane_sum<1, 32>(i0 < a.splits ? weight * stat[2 * i0 + 1] : 0.0f);
   float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
   for (int i = 0; i < a.splits; ++i) {
-    const float w = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((stat[2 * i] - m) * c);
+    const float w = __shfl(weight, i, 32);
     const f32x4 x = *(const f32x4*)(part + (int64_t)i * a.dim);
-    sum += w * stat[2 * i + 1];
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] += w * x[j];
   }
+  if (mine >= all || d >= a.dim) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int j = 0; j < 4; ++j) f[j] *= inv;
@@ -310,7 +331,7 @@ hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((attn_decode_kernel<T, decltype(dp)::value, decltype(du)::value>), grid, block, 0, s, a);
   });
   const int64_t rows = a.batch * a.tokens * a.q_heads;
-  if (a.splits > 16) hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)rows), block, 0, s, a);
+  if (a.splits > 4) hipLaunchKernelGGL((attn_decode_join_kernel<T>), dim3((unsigned)rows), block, 0, s, a);
   else if (a.splits > 1)
     hipLaunchKernelGGL((attn_decode_join_few_kernel<T>), dim3((unsigned)((rows + 7) / 8)), block, 0, s, a);
   return hipGetLastError();
