@@ -163,3 +163,17 @@ def test_strides_and_captured_steps(ops):
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
         assert torch.equal(kc, plain[0]) and torch.equal(vc, plain[1]), i
+
+
+# one block, a few splits, many; tiles of the cache that every new token sees next to tiles that some do
+SPLITS = [
+    (1, 8, 2, 64, 0, 0, 320, [300]), (2, 4, 1, 128, 0, 0, 400, [383, 398]), (3, 8, 2, 72, 300, 40, 500, [100, 342, 499, 777]),
+    (8, 4, 4, 128, 700, 64, 800, [70, 763, 764, 1600]), (16, 4, 1, 64, 1500, 1, 1516, [1515, 5000]),
+    (1, 3, 3, 32, 0, 96, 4000, [3999, 4000, 9000]), (5, 6, 3, 96, 1000, 31, 1040, [20, 30, 31, 32, 1034, 1035, 1036, 2222]),
+]
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,window,sinks,capacity,lens", SPLITS)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_splits_and_full_tiles(ops, io, T, Hq, Hk, D, window, sinks, capacity, lens):
+    test_against_the_oracle(ops, io, T, Hq, Hk, D, window, sinks, capacity, lens)
