@@ -152,7 +152,7 @@ m3::AttnArgs args_of(const m3_attn_dims* d, const int64_t* starts) {
   a.dk_stride = or_width(d->dk_stride, wk);
   a.dv_stride = or_width(d->dv_stride, wk);
   a.piece = m3::attn_bwd_piece(a);
-  a.splits = m3::attn_bwd_splits(a);
+  a.splits = m3::attn_bwd_splits(bf16(d->io_dtype), a);
   return a;
 }
 

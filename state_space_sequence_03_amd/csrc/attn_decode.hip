@@ -38,17 +38,22 @@ int attn_bwd_piece(const AttnArgs& a) {
   n = (n + 127) / 128 * 128;
   return (int)(n < (1 << 25) ? n : 1 << 25);
 }
-// Blocks that share a tile of 128 keys, where there are too few of those: two
-// steps of 64 queries for each at least.  (1 x 2048 queries, 16/4 heads of 64, no
-// window: dk and dv 176 us with one, 47 with six; from 192 tiles on one each is
-// faster: 4 x 2048, window 512, 103 us, 124 with two.)
-int attn_bwd_splits(const AttnArgs& a) {
+// Blocks that share a tile of 128 keys (and a piece), where there are too few of
+// those: two steps of queries for each at least.  (1 x 2048 queries, 16/4 heads of
+// 64, no window: dk and dv 176 us with one, 47 with six; from 192 tiles on one each
+// is faster: 4 x 2048, window 512, 103 us, 124 with two.  With the pieces counted
+// 1 x 2048, 16/4 x 128, window 512, has 5 instead of 6: 61 -> 55 us.)  In fp32 a
+// wide head's block has a CU to itself, so one round of the chip is best: 4 x 512
+// queries, 2 heads of 128, window 64, with four 38 us, 60 with two; 2 x 777, 5 heads
+// of 72, with two 47 us, 55 with four.
+int attn_bwd_splits(int io_bf16, const AttnArgs& a) {
   const int64_t blocks = attn_items(a, true, 128) * a.kv_heads;
   if (blocks == 0 || blocks >= 192) return 1;
   int64_t rows = a.starts ? a.rows : a.q_len;
   if (a.window < kNoWindow && rows > (int64_t)a.window + 128) rows = (int64_t)a.window + 128;
-  const int64_t most = (rows + 63) / 64 * (a.q_heads / a.kv_heads) / 2;
-  int64_t n = (384 + blocks - 1) / blocks;
+  const int64_t step = io_bf16 ? 64 : 32, most = (rows + step - 1) / step * (a.q_heads / a.kv_heads) / 2;
+  const int64_t busy = blocks + attn_piece_blocks(a);
+  int64_t n = io_bf16 ? (384 + busy - 1) / busy : (a.dim > 64 ? 256 : 512) / busy;
   n = n < most ? n : most;
   return n < 1 ? 1 : n < 16 ? (int)n : 16;
 }

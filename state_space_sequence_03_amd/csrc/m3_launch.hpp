@@ -293,7 +293,7 @@ struct AttnArgs {
 };
 size_t attn_bwd_part_bytes(const AttnArgs& a);
 int attn_bwd_piece(const AttnArgs& a);
-int attn_bwd_splits(const AttnArgs& a);
+int attn_bwd_splits(int io_bf16, const AttnArgs& a);
 template <typename T>
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 template <typename T>
