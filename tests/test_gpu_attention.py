@@ -274,3 +274,10 @@ def test_large_scores_in_parts(ops, io, D):
             check_forward(io, o[0], lse[0], q[0], k[0], v[0], window, sinks, 1.0)
             g = ops.window_attn_bwd(q, k, v, o, lse, do, **see)
             check_backward(io, [g[x][0] for x in ("dq", "dk", "dv")], q[0], k[0], v[0], o[0], lse[0], do[0], window, sinks, 1.0)
+
+
+@pytest.mark.parametrize("lens,window,sinks,D", [([700, 1, 600, 0, 64], 0, 0, 64), ([900, 40, 530], 600, 33, 128),
+                                                 ([1], 0, 0, 32), ([513, 5], 1024, 3, 96)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_packed_sequences_in_parts(ops, io, lens, window, sinks, D):
+    test_packed_sequences(ops, io, lens, window, sinks, D)
