@@ -936,7 +936,7 @@ def mamba3_qk_norm_rope_bwd(q, k, dq_out, dk_out, gain_q=None, gain_k=None, eps=
     return out
 
 
-def _attn_dims(q, k, v, starts, window, sinks, scale):
+def _attn_dims(q, k, v, starts, window, sinks, scale, grads=False):
     """Dims of a windowed attention (strides of q, k, v set), pointers of q, k, v
     and starts, shapes of q and k, type, device."""
     io, dev, ps, rows, kv_rows, flags = q.dtype, q.device, None, 0, 0, 0
@@ -948,6 +948,9 @@ def _attn_dims(q, k, v, starts, window, sinks, scale):
             raise ValueError("q is (batch, q_len, heads, head_dim), k and v (batch, kv_len, heads, head_dim)")
         batch, q_len, kv_len = qs[0], qs[1], ks[1]
         (pk, sk, kv_rows), (pv, sv, rv) = _sequences("k", k, ks, io, dev), _sequences("v", v, ks, io, dev)
+        if kv_len == 1 and (grads or kv_rows != rv) and k.stride(0) <= 1 << 20 and v.stride(0) <= 1 << 20:
+            # single tokens may be anything evenly spaced
+            (pk, sk), (pv, sv), kv_rows, rv = _tokens("k", k, ks, io, dev), _tokens("v", v, ks, io, dev), 0, 0
         if kv_rows != rv:
             raise ValueError("k and v must have as many rows from sequence to sequence")
     else:
@@ -969,7 +972,7 @@ def _sequences(name, t, shape, dtype, device):
     tokens of longer sequences (a cache's)."""
     if not t.is_contiguous() and t.shape == shape and shape[0] > 1 and shape[1] > 0:
         row, between = shape[2] * shape[3], t.stride(0)
-        step = t.stride(1) if shape[1] > 1 else row
+        step = t.stride(1) if t.stride(1) >= row else row if shape[1] == 1 else 0
         if step > 0 and between % step == 0 and between // step > shape[1]:
             p, s = _tokens(name, t[0], shape[1:], dtype, device)
             return p, s, between // (s or row)
@@ -1019,7 +1022,7 @@ def mamba3_window_attn_bwd(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None
         return _on_stream(stream, q, mamba3_window_attn_bwd, q, k, v, o, lse, do, window=window, sinks=sinks,
                           scale=scale, starts=starts, want_dq=want_dq, want_dk=want_dk, want_dv=want_dv, dq=dq, dk=dk,
                           dv=dv, workspace=workspace)
-    dims, (pq, pk, pv, ps), qs, ks, io, dev = _attn_dims(q, k, v, starts, window, sinks, scale)
+    dims, (pq, pk, pv, ps), qs, ks, io, dev = _attn_dims(q, k, v, starts, window, sinks, scale, True)
     po, dims.o_stride = _tokens("o", o, qs, io, dev)
     pdo, dims.do_stride = _tokens("do", do, qs, io, dev)
     pl = _vec("lse", lse, qs[:-1], _torch().float32, dev)

@@ -230,3 +230,23 @@ def test_decode_refusals(fake):
 def test_slots(fake):
     got = ops.window_cache_slots(torch.arange(12), 2, 7)
     assert got.tolist() == [0, 1, 2, 3, 4, 5, 6, 2, 3, 4, 5, 6]
+
+
+def test_single_tokens_of_a_projection(fake):
+    # sequences of one token each: slices of a projection's heads are evenly spaced tokens, not parts of a cache
+    qkv = heads(Hq + 2 * Hk, B, 1)
+    q, k, v = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hk], qkv[:, :, Hq + Hk:]
+    width = (Hq + 2 * Hk) * D
+    single = qkv[:, 0, Hq:Hq + Hk].unsqueeze(1)
+    for keys, stride in ((k, width), (heads(Hk, B, 1), 0), (single, width)):
+        o, lse = ops.window_attn_fwd(q, keys, v, want_lse=True)
+        assert set(ops.window_attn_bwd(q, keys, v, o, lse, o)) == {"dq", "dk", "dv"}
+        for name, args in fake.calls:
+            dims = args[0]
+            assert (dims.q_stride, dims.k_stride, dims.v_stride, dims.kv_rows) == (width, stride, width, 0), name
+        fake.calls.clear()
+    # the first tokens of caches too long for that: rows from sequence to sequence
+    cache = torch.empty_strided((B, 1, Hk, D), (1 << 21, Hk * D, D, 1), dtype=bf)
+    ops.window_attn_fwd(q, cache, cache)
+    dims = fake.calls[0][1][0]
+    assert dims.kv_rows == (1 << 21) // (Hk * D) and dims.k_stride in (0, Hk * D)
