@@ -84,36 +84,48 @@ __device__ __forceinline__ void turn(const NormRopeArgs& a, const float2* tab, f
   }
 }
 
-// Vector u of the tokens from t0 on: which operand, and its place in a matrix
-// of the two operands' row strides.
+// One of the vectors of a block's tokens, which are counted token by token, the
+// token's heads in order (queries', then keys'); a step goes VPB vectors on.
+template <int VPB>
 struct Place {
-  bool key;
-  int token;
-  int64_t row;
-  int head;
-  __device__ __forceinline__ Place(const NormRopeArgs& a, int64_t t0, int u) {
+  int token, head;
+  __device__ __forceinline__ Place(const NormRopeArgs& a, int u) {
     const int H = a.q_heads + a.k_heads;
     token = u / H;
-    row = t0 + token;
     head = u - token * H;
-    key = head >= a.q_heads;
-    if (key) head -= a.q_heads;
   }
+  __device__ __forceinline__ void step(const NormRopeArgs& a) {
+    const int H = a.q_heads + a.k_heads, over = VPB / H;  // of all threads alike
+    token += over;
+    head += VPB - over * H;
+    if (head >= H) {
+      head -= H;
+      ++token;
+    }
+  }
+  __device__ __forceinline__ bool key(const NormRopeArgs& a) const { return head >= a.q_heads; }
+  // its place in a matrix of the two operands' row strides, from token t0's row
+  // on: 64 tokens at most, of rows of 2^20 entries at most
   template <typename T>
-  __device__ __forceinline__ char* at(const NormRopeArgs& a, const void* q, const void* k, int64_t sq,
-                                      int64_t sk) const {
-    return (char*)(key ? k : q) + (row * (key ? sk : sq) + (int64_t)head * a.dim) * io<T>::BYTES;
+  __device__ __forceinline__ char* at(const NormRopeArgs& a, const void* q, const void* k, int64_t sq, int64_t sk,
+                                      int64_t t0) const {
+    const bool kv = key(a);
+    char* base = kv ? (char*)k + t0 * sk * io<T>::BYTES : (char*)q + t0 * sq * io<T>::BYTES;
+    const int e = __mul24(token, kv ? (int)sk : (int)sq) + __mul24(kv ? head - a.q_heads : head, a.dim);
+    return base + (uint32_t)e * (uint32_t)io<T>::BYTES;
   }
 };
 
 // 1 / sqrt(mean x^2 + eps) of a vector held by LPV lanes (entries past its
-// width are 0).
+// width are 0).  v_rsq_f32 is good to one unit in the last place; of numbers
+// below the normal ones it takes no root.
 template <int V, int LPV>
-__device__ __forceinline__ float rms(const float* f, int dim, float eps) {
+__device__ __forceinline__ float rms(const float* f, float per, float eps) {
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) s += f[j] * f[j];
-  return 1.0f / sqrtf(lane_sum<1, LPV>(s) / (float)dim + eps);
+  const float m = lane_sum<1, LPV>(s) * per + eps;
+  return m >= 0x1p-126f ? __builtin_amdgcn_rsqf(m) : 1.0f / sqrtf(m);
 }
 
 template <typename T, int LPV, bool HALVES>
@@ -125,25 +137,28 @@ __global__ __launch_bounds__(256) void norm_rope_fwd_kernel(NormRopeArgs a) {
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int n = a.rows - t0 < a.tokens ? (int)(a.rows - t0) : a.tokens;
   const int vectors = n * (a.q_heads + a.k_heads);
+  const float per = 1.0f / (float)a.dim;
   u32x4 raw = {0u, 0u, 0u, 0u};
-  int u = slot;
-  if (u < vectors) raw = row_raw<T>(Place(a, t0, u).at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
+  Place<VPB> next(a, slot);
+  auto load = [&] { raw = row_raw<T>(next.template at<T>(a, a.q, a.k, a.q_stride, a.k_stride, t0), c, a.dim); };
+  if (slot < vectors) load();
   float g[2][V];
   col_load<V>(a.gain_q, c, a.dim, 1.0f, g[0]);
   col_load<V>(a.gain_k, c, a.dim, 1.0f, g[1]);
   fill_table(a, t0, n, tab);
   __syncthreads();
-  while (u < vectors) {
-    const Place at(a, t0, u);
+  for (int u = slot; u < vectors; u += VPB) {
+    const Place<VPB> at = next;
+    const bool key = at.key(a);
     float f[V];
     unpack_raw<T>(raw, f);
-    u += VPB;
-    if (u < vectors) raw = row_raw<T>(Place(a, t0, u).at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
-    const float r = rms<V, LPV>(f, a.dim, a.eps);
+    next.step(a);
+    if (u + VPB < vectors) load();
+    const float r = rms<V, LPV>(f, per, a.eps);
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] *= r * (at.key ? g[1][j] : g[0][j]);
+    for (int j = 0; j < V; ++j) f[j] *= r * (key ? g[1][j] : g[0][j]);
     turn<V, HALVES, 1>(a, tab + at.token * (a.rope / 2), xs + (HALVES ? slot * LPV * V : 0), c, f);
-    row_store<T>(at.at<T>(a, a.q_out, a.k_out, a.q_out_stride, a.k_out_stride), c, a.dim, f);
+    row_store<T>(at.template at<T>(a, a.q_out, a.k_out, a.q_out_stride, a.k_out_stride, t0), c, a.dim, f);
   }
 }
 
@@ -155,6 +170,7 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormRopeArgs a) {
   __shared__ float2 tab[kTable];
   __shared__ __attribute__((aligned(16))) float xs[256 * V];
   const int lane = threadIdx.x % LPV, slot = threadIdx.x / LPV, c = lane * V;
+  const float per = 1.0f / (float)a.dim;
   float g[2][V], sum[2][V];
   col_load<V>(a.gain_q, c, a.dim, 1.0f, g[0]);
   col_load<V>(a.gain_k, c, a.dim, 1.0f, g[1]);
@@ -164,38 +180,38 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormRopeArgs a) {
     const int n = a.rows - t0 < a.tokens ? (int)(a.rows - t0) : a.tokens;
     const int vectors = n * (a.q_heads + a.k_heads);
     u32x4 rx = {0u, 0u, 0u, 0u}, ry = rx;
-    int u = slot;
+    Place<VPB> next(a, slot);
     auto load = [&] {
-      const Place at(a, t0, u);
-      rx = row_raw<T>(at.at<T>(a, a.q, a.k, a.q_stride, a.k_stride), c, a.dim);
-      ry = row_raw<T>(at.at<T>(a, a.dq_out, a.dk_out, a.q_out_stride, a.k_out_stride), c, a.dim);
+      rx = row_raw<T>(next.template at<T>(a, a.q, a.k, a.q_stride, a.k_stride, t0), c, a.dim);
+      ry = row_raw<T>(next.template at<T>(a, a.dq_out, a.dk_out, a.q_out_stride, a.k_out_stride, t0), c, a.dim);
     };
-    if (u < vectors) load();
+    if (slot < vectors) load();
     fill_table(a, t0, n, tab);
     __syncthreads();
-    while (u < vectors) {
-      const Place at(a, t0, u);
+    for (int u = slot; u < vectors; u += VPB) {
+      const Place<VPB> at = next;
+      const bool key = at.key(a);
       float x[V], d[V];
       unpack_raw<T>(rx, x);
       unpack_raw<T>(ry, d);
-      u += VPB;
-      if (u < vectors) load();
-      const float r = rms<V, LPV>(x, a.dim, a.eps);
+      next.step(a);
+      if (u + VPB < vectors) load();
+      const float r = rms<V, LPV>(x, per, a.eps);
       turn<V, HALVES, -1>(a, tab + at.token * (a.rope / 2), xs + slot * LPV * V, c, d);
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         x[j] *= r;
         const float w = d[j] * x[j];
-        if (at.key) sum[1][j] += w;
+        if (key) sum[1][j] += w;
         else sum[0][j] += w;
-        d[j] *= at.key ? g[1][j] : g[0][j];
+        d[j] *= key ? g[1][j] : g[0][j];
         s += d[j] * x[j];
       }
-      s = lane_sum<1, LPV>(s) / (float)a.dim;
+      s = lane_sum<1, LPV>(s) * per;
 #pragma unroll
       for (int j = 0; j < V; ++j) d[j] = r * (d[j] - x[j] * s);
-      row_store<T>(at.at<T>(a, a.q_out, a.k_out, a.dq_stride, a.dk_stride), c, a.dim, d);
+      row_store<T>(at.template at<T>(a, a.q_out, a.k_out, a.dq_stride, a.dk_stride, t0), c, a.dim, d);
     }
     __syncthreads();  // the table is read
   }
