@@ -8,10 +8,11 @@ template hipError_t launch_attn_decode<bf16_t>(const AttnDecodeArgs&, hipStream_
 template hipError_t launch_attn_decode<float>(const AttnDecodeArgs&, hipStream_t);
 
 // Enough blocks to occupy the chip, each wave with a tile of 32 slots at least;
-// fewer than 12 tiles are one block's, which needs no second launch.  (One
-// sequence, 4 heads of keys of 128: 512 slots in 4 splits 10.5 us, in 2 11.5, in 1
-// 14; 256 slots in 1 8.4.  Twice as many blocks at a width of 64, as registers
-// allow: 64 sequences of 1028 slots 37 us instead of 32.)
+// fewer than 16 tiles are one block's, which needs no second launch.  (One
+// sequence, 4 heads of keys of 128: 512 slots in 4 splits 11.2 us, in 2 11.8, in 1
+// 12.0; 384 in 3 10.9, in 1 10.6; 1024 in 8 10.9, in 4 12.7, in 1 17.9.  Twice as
+// many blocks at a width of 64, as registers allow: 64 sequences of 1028 slots 37
+// us instead of 32.)
 int attn_decode_splits(int io_bf16, const AttnDecodeArgs& a) {
   const int64_t groups = ((int64_t)a.q_heads / a.kv_heads * a.tokens + 31) / 32;
   const int64_t blocks = a.batch * a.kv_heads * groups, room = io_bf16 || a.dim <= 64 ? 512 : 256;
@@ -19,7 +20,7 @@ int attn_decode_splits(int io_bf16, const AttnDecodeArgs& a) {
   if (a.window < kNoWindow && slots > (int64_t)a.sinks + a.window + a.tokens - 1)
     slots = (int64_t)a.sinks + a.window + a.tokens - 1;
   int64_t n = blocks > 0 ? (room + blocks - 1) / blocks : 1;
-  const int64_t tiles = (slots + 31) / 32, most = tiles < 12 ? 1 : tiles / 4;
+  const int64_t tiles = (slots + 31) / 32, most = tiles < 16 ? 1 : tiles / 4;
   n = n < most ? n : most;
   return n < 1 ? 1 : n < kMaxSplits ? (int)n : kMaxSplits;
 }

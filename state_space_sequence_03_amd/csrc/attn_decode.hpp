@@ -80,11 +80,12 @@ struct CacheView {
 // values are written to the cache by the wave that then reads their slots.
 //
 // Bound by HBM: the slots seen are read once per 32 columns.  Batch 256, 16/4
-// heads of 128, 1028 slots: 105 us, 5.1 TB/s, what a copy reaches.  Where each wave
+// heads of 128, 1028 slots: 104 us, 5.2 TB/s, what a copy reaches.  Where each wave
 // has a tile or two, by the time that one takes from its lengths to its result:
-// 32768 slots of one sequence 20 us, 3.3 TB/s; 8 new tokens of 32 sequences, 32/8
-// heads of 64, about 2000 slots: 27 us.  (Without the branch around the masks, every
-// tile's 250 instructions for them came to 110, 23 and 31 us.)
+// 32768 slots of one sequence 16 us and 4 for the join, 3.5 TB/s; 8 new tokens of 32
+// sequences, 32/8 heads of 64, about 2000 slots: 20.5 and 4 us.  (Without the branch
+// around the masks, whose 250 instructions every tile then takes: 109, 18.5 and
+// 23.7.)
 template <typename T, int DP, int DU>
 __global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 1)) void attn_decode_kernel(AttnDecodeArgs a) {
   using KV = Tile<T, DP, DU, 32, 1>;
