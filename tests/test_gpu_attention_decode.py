@@ -177,3 +177,20 @@ SPLITS = [
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_splits_and_full_tiles(ops, io, T, Hq, Hk, D, window, sinks, capacity, lens):
     test_against_the_oracle(ops, io, T, Hq, Hk, D, window, sinks, capacity, lens)
+
+
+@pytest.mark.parametrize("window", [0, 60])
+def test_very_long_sequences(ops, window):
+    # positions past 32 bits: what lies at the same place of the ring is the same
+    r = np.random.default_rng(8)
+    sinks, capacity, T, small = 4, 100, 5, [997, 1000, 1031, 4, 95]
+    ring = capacity - sinks
+    q, k, v = draw(r, (5, T, 4, 64), "bf16"), draw(r, (5, T, 2, 64), "bf16"), draw(r, (5, T, 2, 64), "bf16")
+    kc, vc = draw(r, (5, capacity, 2, 64), "bf16"), draw(r, (5, capacity, 2, 64), "bf16")
+    got = []
+    for turns in (0, 1 << 26, 1 << 40):
+        c = kc.clone(), vc.clone()
+        lens = torch.tensor([n + ring * (turns if n > 200 else 0) for n in small], device="cuda")
+        got.append((ops.window_attn_decode(q, k, v, *c, lens, window=window, sinks=sinks),) + c)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))

@@ -162,3 +162,50 @@ def test_example(ops):
     assert off < 2e-2
     # fp32: third derivatives' part, about step^2 = 2^-16, and the sums' roundings over 2 step
     assert error < 5e-3
+
+
+def test_rows_far_apart(ops):
+    # the widest rows there may be, their bytes past 32 bits: as with contiguous rows, and nothing beside them written
+    L, Hq, Hk, D, wide = 2200, 4, 2, 64, 1 << 20
+    print(f"rows {wide} entries apart, {L} of them", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    rows = torch.zeros(L, wide, device="cuda", dtype=torch.bfloat16)
+    at = iter(range(0, wide, 4096))
+
+    def spot(heads, values=None):
+        c = next(at)
+        t = rows[:, c:c + heads * D].unflatten(1, (heads, D))[None]
+        if values is not None:
+            t.copy_(values)
+        return t
+
+    rand = lambda heads: torch.randn(1, L, heads, D, device="cuda", generator=g).bfloat16()
+    q, k, v, do = rand(Hq), rand(Hk), rand(Hk), rand(Hq)
+    turn = {"theta": torch.rand(D // 2, device="cuda", generator=g), "halves": True}
+    see = {"window": 300, "sinks": 40}
+    far = [spot(h, t) for h, t in ((Hq, q), (Hk, k), (Hk, v), (Hq, do))]
+    spots = [spot(h) for h in (Hq, Hk, Hq, Hq, Hk, Hk, Hq, Hk)]
+    qr, kr = ops.qk_norm_rope_fwd(q, k, **turn)
+    ops.qk_norm_rope_fwd(far[0], far[1], q_out=spots[0], k_out=spots[1], **turn)
+    o, lse = ops.window_attn_fwd(qr, kr, v, want_lse=True, **see)
+    _, lse2 = ops.window_attn_fwd(spots[0], spots[1], far[2], o=spots[2], want_lse=True, **see)
+    d = ops.window_attn_bwd(qr, kr, v, o, lse, do, **see)
+    ops.window_attn_bwd(spots[0], spots[1], far[2], spots[2], lse2, far[3], dq=spots[3], dk=spots[4], dv=spots[5], **see)
+    n = ops.qk_norm_rope_bwd(q, k, d["dq"], d["dk"], **turn)
+    m = ops.qk_norm_rope_bwd(far[0], far[1], spots[3], spots[4], dq=spots[6], dk=spots[7], **turn)
+    torch.cuda.synchronize()
+    for got, want in zip(spots + [lse2, m["dgain_q"], m["dgain_k"]],
+                         (qr, kr, o, d["dq"], d["dk"], d["dv"], n["dq"], n["dk"], lse, n["dgain_q"], n["dgain_k"])):
+        assert torch.equal(got, want)
+    for t in far + spots:
+        t.zero_()
+    assert not bool(rows.view(torch.int32).any())
+    # a cache with slots as far apart
+    caches = [spot(Hk, t) for t in (k, v)]
+    plain = [k.clone(), v.clone()]
+    new = [t[:, :5] for t in (q, k, v)]
+    lens = torch.tensor([5 * L - 7], device="cuda")
+    got = ops.window_attn_decode(*(t.contiguous() for t in new), *caches, lens, window=L - 100, sinks=40)
+    want = ops.window_attn_decode(*(t.contiguous() for t in new), *plain, lens, window=L - 100, sinks=40)
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(caches, plain))
