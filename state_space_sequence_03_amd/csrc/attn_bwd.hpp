@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 //
 // The sinks are seen from the whole sequence.  Where that is longer than
 // a.piece queries, each 32 keys with sinks among them are left to blocks of
-// their own (the first `pieces`), each with a.piece queries, of which each wave
+// their own (the last `pieces`), each with a.piece queries, of which each wave
 // takes every fourth 32; the four sums go to the workspace in fp32 and are
 // joined in order.
 //
@@ -64,10 +64,10 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // its sums go to the workspace as well.
 //
 // Two waves share a SIMD, which the registers just allow (fragments three
-// products ahead: 560 to 620 us for 8 x 4096 queries, 16/4 heads of 128, window
+// products ahead: 510 to 600 us for 8 x 4096 queries, 16/4 heads of 128, window
 // 1024, as the clock is; next to 620, six ahead with spills 740, one wave per SIMD
 // 780).  There the matrix cores work in 44 % of the cycles and the vector units in
-// 29 %, and 1248 blocks for 512 places leave a sixth of the CUs' time idle.
+// 29 %.
 template <typename T, int DP, int DU, int BQ>
 __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(
     AttnArgs a, int64_t items, int64_t pieces) {
@@ -80,20 +80,22 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
   const int sunk = (a.sinks + 31) / 32;
-  const bool cut = blockIdx.x < pieces;
+  const uint32_t tiles = gridDim.x - (uint32_t)pieces;
+  const bool cut = blockIdx.x >= tiles;
+  const uint32_t bx = cut ? blockIdx.x - tiles : blockIdx.x;
   AttnSeq s;
   int jw, piece = 0, split = 0;  // jw: the wave's first key
   int64_t hk;
   uint32_t item = 0;
   if (cut) {
-    const uint32_t at = blockIdx.x / (uint32_t)a.splits, id = at / (uint32_t)a.kv_heads;
-    split = (int)(blockIdx.x % (uint32_t)a.splits);
+    const uint32_t at = bx / (uint32_t)a.splits, id = at / (uint32_t)a.kv_heads;
+    split = (int)(bx % (uint32_t)a.splits);
     hk = at % (uint32_t)a.kv_heads;
     jw = (int)(id % (uint32_t)sunk) * 32;
     if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
     if (jw >= s.nk) return;
   } else {
-    const uint32_t id = xcd_order(blockIdx.x - (uint32_t)pieces, gridDim.x - (uint32_t)pieces);
+    const uint32_t id = xcd_order(bx, tiles);
     int t;
     item = id / (uint32_t)a.splits;
     split = (int)(id % (uint32_t)a.splits);
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
   if (cut || a.splits > 1) {
     // per split of a piece, and behind those of an item: (dk, dv; wave; 32 keys; dim)
-    const int64_t at = cut ? blockIdx.x : pieces + (int64_t)item * a.splits + split;
+    const int64_t at = cut ? bx : pieces + (int64_t)item * a.splits + split;
     float* part = a.part + (at * 8 + wave) * 32 * a.dim + (int64_t)(lane & 31) * a.dim;
 #pragma unroll
     for (int d = 0; d < QD::CT; ++d) {
@@ -311,9 +313,11 @@ __global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64
 }
 
 // dq of 32 NW queries, 32 NW / HT positions of HT heads, by KW parties as in the
-// forward: each wave holds 32 of them as the columns of its products (scores = K q^T, dp = V do^T,
-// dq^T += K^T ds) and walks the keys they see as the forward does.  It comes
-// first and leaves the queries' statistics to the other kernel.
+// forward: each wave holds 32 of them as the columns of its products
+// (scores = K q^T, dp = V do^T, dq^T += K^T ds) and walks the tiles of keys that
+// the block's queries see, but for halves that its own do not.  It comes first and
+// leaves the queries' statistics to the other kernel.  8 x 4096 queries, 16/4 heads
+// of 128, window 1024: 400 to 460 us, 0.8 to 0.9 PFLOP/s of three products.
 template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
 __global__ __launch_bounds__(64 * NW * KW, NW * KW > 4 || (KW == 1 && (io<T>::BYTES == 2 || DP == 64)) ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;

@@ -28,11 +28,13 @@ size_t attn_decode_part_bytes(const AttnDecodeArgs& a) {
   return a.splits == 1 ? 0 : (size_t)a.batch * a.tokens * a.q_heads * a.splits * (a.dim + 2) * 4;
 }
 
-// Queries of a piece of 32 keys with sinks among them: half of what sees a tile
-// behind the sinks, so that its block is done well before a tile's, and so many
-// that there are 8192 pieces at most.
+// Queries of a piece of 32 keys with sinks among them: a quarter of what sees a
+// tile behind the sinks, so that the pieces, which come last, even out what the
+// tiles leave (8 x 4096 queries, 16/4 heads of 128, window 1024: dk and dv 522 us,
+// with halves 520, and first 541; 1 x 2048, window 512: 50, 55, 55), and so many that
+// there are 8192 pieces at most.
 int attn_bwd_piece(const AttnArgs& a) {
-  int64_t n = ((a.window < (1 << 24) ? a.window : 1 << 24) + 128) / 2;
+  int64_t n = ((a.window < (1 << 24) ? a.window : 1 << 24) + 128) / 4;
   const int64_t work = a.rows * ((a.sinks + 31) / 32) * a.kv_heads;
   if (n < 256) n = 256;
   if (n < work / 4096) n = work / 4096;
