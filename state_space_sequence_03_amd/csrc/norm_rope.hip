@@ -254,7 +254,9 @@ void launch_lanes(bool bwd, const NormRopeArgs& a, unsigned blocks, hipStream_t 
 }
 
 // Tokens per block: enough vectors for a few passes of the block, while the
-// grid still covers the chip twice over.
+// grid still covers the chip twice over.  (Passes of 1024 lanes in all: forward of
+// 32768 tokens of 20 heads of 128 63 us, backward of 40 heads of 64 111; of 640: 68
+// and 121, of 2048: 68 and 114.)
 int tokens_per_block(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int64_t rope) {
   const int64_t per = heads * ((dim + (io_bf16 ? 7 : 3)) / (io_bf16 ? 8 : 4));  // lanes of a token
   int64_t t = (1024 + per - 1) / per;
@@ -267,7 +269,7 @@ int tokens_per_block(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int6
 
 int64_t norm_rope_parts(int io_bf16, int64_t rows, int64_t heads, int64_t dim, int64_t rope) {
   const int64_t t = tokens_per_block(io_bf16, rows, heads, dim, rope), groups = (rows + t - 1) / t;
-  return groups < 1024 ? groups : 1024;
+  return groups < 1024 ? groups : 1024;  // the backward above: with 512 136 us, 768 114, 2048 116
 }
 
 hipError_t launch_norm_rope(int io_bf16, bool bwd, NormRopeArgs a, hipStream_t s) {
