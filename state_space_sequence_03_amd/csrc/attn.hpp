@@ -302,7 +302,8 @@ struct RowStream {
         (void*)base, 0, (uint32_t)((rows - 1) * ldb + width * io<T>::BYTES), 0x00020000);
 #pragma unroll
     for (int s = 0; s < KS; ++s)
-      v[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, 2 * s < last ? voff + s * 32 : kFar, 0, 0));
+      v[s] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, 2 * s < last ? voff + s * 32 : kFar, 0, 0));
 #endif
   }
 };
@@ -431,16 +432,19 @@ struct Softmax {
 // part's waves (true for them): sums acc, and for a softmax (SOFT) its reference
 // m and sum l.  Each part leaves its sums in its own BYTES of LDS.
 template <int KW, int NW, int BYTES, bool SOFT, int CT>
-__device__ __forceinline__ bool join_parts(char* lds, f32x16 (&acc)[CT], float& m, float& l, float c, int part, int wave,
-                                           int lane) {
+__device__ __forceinline__ bool join_parts(char* lds, f32x16 (&acc)[CT], float& m, float& l, float c, int part,
+                                           int wave, int lane) {
   static_assert(NW * CT * 4096 <= BYTES, "a part's sums fit its LDS");
   __shared__ float stat[SOFT ? KW : 1][NW][2][64];
   attn_settle();  // the tiles are read
   if (part > 0) {
     f32x4* x = (f32x4*)(lds + part * BYTES + wave * CT * 4096) + lane;
 #pragma unroll
-    for (int i = 0; i < CT * 4; ++i)
-      x[i * 64] = f32x4{acc[i / 4][i % 4 * 4], acc[i / 4][i % 4 * 4 + 1], acc[i / 4][i % 4 * 4 + 2], acc[i / 4][i % 4 * 4 + 3]};
+    for (int i = 0; i < CT * 4; ++i) {
+      const f32x16& o = acc[i / 4];
+      const int e = i % 4 * 4;
+      x[i * 64] = f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
+    }
     if constexpr (SOFT) {
       stat[part][wave][0][lane] = m;
       stat[part][wave][1][lane] = l;

@@ -104,14 +104,16 @@ m3_status check(const m3_attn_dims* d, bool backward) {
     return M3_ERR_ALIGN;
   if (packed(d)) {
     if (d->rows < 0) return M3_ERR_SHAPE;
-    if (d->rows > kMaxRows || times(d->rows / 128 + (d->batch < d->rows ? d->batch : d->rows), d->q_heads) > kMaxRows - 32768)
+    const int64_t tiles = d->rows / 128 + (d->batch < d->rows ? d->batch : d->rows);
+    if (d->rows > kMaxRows || times(tiles, d->q_heads) > kMaxRows - 32768)
       return M3_ERR_UNSUPPORTED;
   } else {
     if (d->q_len < 0 || d->kv_len < 0 || (d->kv_rows != 0 && d->kv_rows < d->kv_len)) return M3_ERR_SHAPE;
     if (d->q_len > kMaxRows || d->kv_len > kMaxRows || times(d->batch, d->q_len) > kMaxRows ||
         times(times(d->batch, (d->q_len + 127) / 128), d->q_heads) > kMaxRows ||
         times(d->batch, d->kv_len) > kMaxRows ||
-        times(times(d->batch, (d->kv_len + 127) / 128), d->kv_heads) > kMaxRows - 32768 || d->kv_rows > (int64_t(1) << 40))
+        times(times(d->batch, (d->kv_len + 127) / 128), d->kv_heads) > kMaxRows - 32768 ||
+        d->kv_rows > (int64_t(1) << 40))
       return M3_ERR_UNSUPPORTED;
   }
   // the backward's rows of statistics, sixteen to a block

@@ -119,7 +119,8 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
   r0 = r0 / BQ * BQ;  // whole tiles, so that a piece's last one ends with it
   const int per = r1 < r0 ? 0 : (r1 - r0) / BQ + 1, all = per * G;
-  const int begin = (int)((int64_t)all * split / a.splits), count = (int)((int64_t)all * (split + 1) / a.splits) - begin;
+  const int begin = (int)((int64_t)all * split / a.splits);
+  const int count = (int)((int64_t)all * (split + 1) / a.splits) - begin;
 
   const int64_t row = s.k0 + (in ? j : s.nk - 1);
   RowRegs<T, DU> k, v;
@@ -319,7 +320,8 @@ __global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64
 // leaves the queries' statistics to the other kernel.  8 x 4096 queries, 16/4 heads
 // of 128, window 1024: 400 to 460 us, 0.8 to 0.9 PFLOP/s of three products.
 template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
-__global__ __launch_bounds__(64 * NW * KW, NW * KW > 4 || (KW == 1 && (io<T>::BYTES == 2 || DP == 64)) ? 2 : 1) void attn_dq_kernel(AttnArgs a, int64_t items) {
+__global__ __launch_bounds__(64 * NW * KW, NW * KW > 4 || (KW == 1 && (io<T>::BYTES == 2 || DP == 64)) ? 2 : 1)
+void attn_dq_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT, HALF = 32 * KV::ROWB;
   __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each part

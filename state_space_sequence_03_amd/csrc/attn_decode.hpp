@@ -87,7 +87,8 @@ struct CacheView {
 // around the masks, whose 250 instructions every tile then takes: 109, 18.5 and
 // 23.7.)
 template <typename T, int DP, int DU>
-__global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 1)) void attn_decode_kernel(AttnDecodeArgs a) {
+__global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 1)) void attn_decode_kernel(
+    AttnDecodeArgs a) {
   using KV = Tile<T, DP, DU, 32, 1>;
   constexpr int NW = 4, ES = io<T>::BYTES, STEPS = 32 / KV::CK, PART = 2 * KV::BYTES;
   static_assert(32 * DP * 4 <= PART, "a wave's result fits its part");

@@ -23,7 +23,8 @@ namespace m3 {
 // neighbours save the rest of the sinks' tile and of the first of the window's: 103
 // -> 96 us in the last of these, 29 -> 31 where there are few blocks and no window.
 template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
-__global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void attn_fwd_kernel(AttnArgs a, int64_t items) {
+__global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void attn_fwd_kernel(AttnArgs a,
+                                                                                                int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT;
   __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each
@@ -145,7 +146,8 @@ void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(items * (a.q_heads / HT)));
   with_width(a.dim, [&](auto dp, auto du) {
     constexpr int DP = decltype(dp)::value, K = attn_parts<T, DP>(NW, KW), BN = io<T>::BYTES == 2 ? 64 : 32;
-    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, decltype(du)::value, BN, HT, NW, K>), grid, dim3(64 * NW * K), 0, s, a, items);
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, decltype(du)::value, BN, HT, NW, K>), grid, dim3(64 * NW * K), 0, s, a,
+                       items);
   });
 }
 

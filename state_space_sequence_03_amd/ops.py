@@ -1070,7 +1070,8 @@ def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sink
                           sinks=sinks, scale=scale, o=o, workspace=workspace)
     io, dev, qs, ks, cs = q.dtype, q.device, q.shape, k.shape, k_cache.shape
     if len(qs) != 4 or len(ks) != 4 or len(cs) != 4 or ks[:2] != qs[:2] or cs[0] != qs[0] or cs[2:] != ks[2:]:
-        raise ValueError("q, k, v are (batch, tokens, heads, head_dim), the caches (batch, capacity, heads of k, head_dim)")
+        raise ValueError("q, k, v are (batch, tokens, heads, head_dim), "
+                         "the caches (batch, capacity, heads of k, head_dim)")
     _, Hq, D = _heads_of("q", q, 4)
     pq, sq = _tokens("q", q, qs, io, dev)
     if ks[3] != D:
