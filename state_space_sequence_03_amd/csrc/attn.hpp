@@ -92,7 +92,8 @@ inline int64_t attn_items(const AttnArgs& a, bool keys, int tile) {
 // fewer for a query what the parts' join costs is not made up for: 300 queries
 // 8.4 -> 8.8).  fp32 kernels, bound by their products, first take blocks of one
 // wave (2 x 777 queries, 5 heads of 72, window 100: forward 35 -> 28 us, dq 53 ->
-// 36; and 18, 23 in two parts, while those blocks are no more than the CUs).
+// 36), and of several parts while those leave CUs idle: in four parts 15 and 18; 1 x
+// 1500, 8 heads of 64, no window, in two 68 and 90 instead of 110 and 159.
 template <typename T, typename F>
 void attn_by_size(const AttnArgs& a, F&& f) {
   using std::integral_constant;
@@ -103,7 +104,9 @@ void attn_by_size(const AttnArgs& a, F&& f) {
   const int64_t blocks = attn_items(a, false, 128) * a.q_heads;
   if constexpr (io<T>::BYTES == 4) {
     if (blocks < 256) {
-      if (attn_items(a, false, 32) * a.q_heads <= 256) f(one, one, four);
+      const int64_t waves = attn_items(a, false, 32) * a.q_heads;
+      if (waves <= 256) f(one, one, four);
+      else if (waves <= 512) f(one, one, two);
       else f(one, one, one);
       return;
     }
@@ -117,12 +120,6 @@ void attn_by_size(const AttnArgs& a, F&& f) {
   else if (G % 2 == 0) f(two, four, one);
   else f(one, four, one);
 }
-// Parts of the keys for which a block's LDS has room.
-template <typename T, int DP>
-constexpr int attn_parts(int waves, int parts) {
-  return waves == 1 && DP == 128 && parts > 2 ? 2 : parts;
-}
-
 // Pieces of the sequences that are longer than one, at most.
 inline int64_t attn_pieces(const AttnArgs& a) {
   if (a.sinks == 0 || a.window >= kNoWindow) return 0;
@@ -375,6 +372,14 @@ __device__ __forceinline__ void attn_settle() {
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// The same for loads and reads that no other wave has a part in.
+__device__ __forceinline__ void attn_settle_alone() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
 }

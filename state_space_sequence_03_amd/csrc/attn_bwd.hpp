@@ -320,14 +320,18 @@ __global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64
 // leaves the queries' statistics to the other kernel.  8 x 4096 queries, 16/4 heads
 // of 128, window 1024: 400 to 460 us, 0.8 to 0.9 PFLOP/s of three products.
 template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
-__global__ __launch_bounds__(64 * NW * KW, NW * KW > 4 || (KW == 1 && (io<T>::BYTES == 2 || DP == 64)) ? 2 : 1)
-void attn_dq_kernel(AttnArgs a, int64_t items) {
+__global__ __launch_bounds__(64 * NW * KW, NW == 1 || (io<T>::BYTES == 4 && DP == 128) ? 1 : 2) void attn_dq_kernel(
+    AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT, HALF = 32 * KV::ROWB;
-  __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each part
+  // wide parties of one wave take the values into registers: LDS has room for four
+  constexpr bool ALONE = NW == 1 && DP == 128;
+  static_assert(!ALONE || NT == 1, "a run at a time");
+  constexpr int PART = (ALONE ? 2 : 4) * KV::BYTES;  // K K or K V K V of each
+  __shared__ __attribute__((aligned(1024))) char lds[KW * PART];
   const int lane = threadIdx.x & 63;
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all % NW, part = all / NW;
-  char* smem = lds + part * 4 * KV::BYTES;
+  char* smem = lds + part * PART;
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x), kg = id / (uint32_t)(G / HT);
@@ -370,7 +374,9 @@ void attn_dq_kernel(AttnArgs a, int64_t items) {
 
   KV kt, vt;
   kt.init(a.k_stride, a.dim, lane, wave);
-  vt.init(a.v_stride, a.dim, lane, wave);
+  RowStream<T, DU> vs;
+  if constexpr (ALONE) vs.init(a.v_stride, a.dim, lane);
+  else vt.init(a.v_stride, a.dim, lane, wave);
   const char* kb = (const char*)a.k + (s.k0 * a.k_stride + hk * a.dim) * ES;
   const char* vb = (const char*)a.v + (s.k0 * a.v_stride + hk * a.dim) * ES;
   int first = p0 - a.window + 1;
@@ -380,8 +386,11 @@ void attn_dq_kernel(AttnArgs a, int64_t items) {
   auto first_key = [&](int n) { return (n < ns ? n : first + n - ns) * BN; };
   auto load = [&](int n, int buf) {
     const int64_t j0 = first_key(n);
-    kt.load(kb + j0 * a.k_stride * ES, s.nk - (int)j0, a.dim, smem + buf * 2 * KV::BYTES, wave);
-    vt.load(vb + j0 * a.v_stride * ES, s.nk - (int)j0, a.dim, smem + (buf * 2 + 1) * KV::BYTES, wave);
+    const int rows = s.nk - (int)j0;
+    char* to = smem + buf * (PART / 2);
+    kt.load(kb + j0 * a.k_stride * ES, rows, a.dim, to, wave);
+    if constexpr (ALONE) vs.load(vb + j0 * a.v_stride * ES, rows < 32 ? rows : 32, a.dim);
+    else vt.load(vb + j0 * a.v_stride * ES, rows, a.dim, to + KV::BYTES, wave);
   };
   f32x16 acc[KV::CT];
 #pragma unroll
@@ -390,18 +399,26 @@ void attn_dq_kernel(AttnArgs a, int64_t items) {
   if (part < count) load(part, 0);
   for (int i = 0; i * KW < count; ++i) {
     const int n = i * KW + part;
-    attn_settle();
+    if constexpr (ALONE) attn_settle_alone();
+    else attn_settle();
     if (KW > 1 && n >= count) continue;
+    uint4 v[ALONE ? KV::KS : 1];
+    if constexpr (ALONE)
+#pragma unroll
+      for (int st = 0; st < KV::KS; ++st) v[st] = vs.v[st];
     if (n + KW < count) load(n + KW, (i + 1) & 1);
 #pragma unroll 1
     for (int b = 0; b < NT; ++b) {
       const int j0 = first_key(n) + 32 * b;
       if (sees_none(w0, w1, j0, j0 + 31, a.window, a.sinks)) continue;
-      const char* kl = smem + (i & 1) * 2 * KV::BYTES + b * HALF;
+      const char* kl = smem + (i & 1) * (PART / 2) + b * HALF;
       const char* vl = kl + KV::BYTES;
       f32x16 x[2] = {f32x16{}, f32x16{}};  // scores, dp
       ahead<6, KV::KS * 2, 1, T>(
-          [&](int i) { return i & 1 ? vt.row(vl, 0, i / 2) : kt.row(kl, 0, i / 2); },
+          [&](int i) {
+            if constexpr (ALONE) return i & 1 ? v[i / 2] : kt.row(kl, 0, i / 2);
+            else return i & 1 ? vt.row(vl, 0, i / 2) : kt.row(kl, 0, i / 2);
+          },
           [&](int i, const uint4& f) { x[i & 1] = mma32<T>(f, i & 1 ? y.v[i / 2] : q.v[i / 2], x[i & 1]); });
       float ds[16];
 #pragma unroll
@@ -422,7 +439,7 @@ void attn_dq_kernel(AttnArgs a, int64_t items) {
   }
   if constexpr (KW > 1) {
     float none = 0.0f;
-    if (!join_parts<KW, NW, 4 * KV::BYTES, false>(lds, acc, none, none, c, part, wave, lane)) return;
+    if (!join_parts<KW, NW, PART, false>(lds, acc, none, none, c, part, wave, lane)) return;
   }
   char* out = (char*)a.dq + (row * a.dq_stride + hq * a.dim) * ES;
 #pragma unroll
@@ -449,8 +466,7 @@ void attn_bwd_run(const AttnArgs& a, hipStream_t s) {
   const dim3 block(256);
   if (a.dq)
     attn_by_size<T>(a, [&](auto ht, auto nw, auto kw) {
-      constexpr int NW = decltype(nw)::value;
-      attn_dq_run<T, DP, DU, decltype(ht)::value, NW, attn_parts<T, DP>(NW, decltype(kw)::value)>(a, s);
+      attn_dq_run<T, DP, DU, decltype(ht)::value, decltype(nw)::value, decltype(kw)::value>(a, s);
     });
   else if (vectors > 0)
     hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((vectors + 15) / 16)), block, 0, s, a);

@@ -23,14 +23,17 @@ namespace m3 {
 // neighbours save the rest of the sinks' tile and of the first of the window's: 103
 // -> 96 us in the last of these, 29 -> 31 where there are few blocks and no window.
 template <typename T, int DP, int DU, int BN, int HT, int NW, int KW>
-__global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void attn_fwd_kernel(AttnArgs a,
-                                                                                                int64_t items) {
+__global__ __launch_bounds__(64 * NW * KW, NW == 1 ? 1 : 2) void attn_fwd_kernel(AttnArgs a, int64_t items) {
   using KV = Tile<T, DP, DU, BN, NW>;
   constexpr int ES = io<T>::BYTES, NT = BN / 32, STEPS = 32 / KV::CK, BM = 32 * NW / HT;
-  __shared__ __attribute__((aligned(1024))) char lds[KW * 4 * KV::BYTES];  // K V K V of each
+  // wide parties of one wave take the keys into registers: LDS has room for four
+  constexpr bool ALONE = NW == 1 && DP == 128;
+  static_assert(!ALONE || NT == 1, "a run at a time");
+  constexpr int PART = (ALONE ? 2 : 4) * KV::BYTES;  // V V or K V K V of each
+  __shared__ __attribute__((aligned(1024))) char lds[KW * PART];
   const int lane = threadIdx.x & 63;
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all % NW, part = all / NW;
-  char* smem = lds + part * 4 * KV::BYTES;
+  char* smem = lds + part * PART;
   const int h = lane >> 5;
   const int G = a.q_heads / a.kv_heads;
   // heads that share keys are neighbours, then the tiles of a sequence, the
@@ -53,7 +56,9 @@ __global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void 
   q.load((const char*)a.q + (row * a.q_stride + hq * a.dim) * ES, in, a.dim, h);
 
   KV kt, vt;
-  kt.init(a.k_stride, a.dim, lane, wave);
+  RowStream<T, DU> ks;
+  if constexpr (ALONE) ks.init(a.k_stride, a.dim, lane);
+  else kt.init(a.k_stride, a.dim, lane, wave);
   vt.init(a.v_stride, a.dim, lane, wave);
   const char* kb = (const char*)a.k + (s.k0 * a.k_stride + hk * a.dim) * ES;
   const char* vb = (const char*)a.v + (s.k0 * a.v_stride + hk * a.dim) * ES;
@@ -64,9 +69,15 @@ __global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void 
   // first keys of tile n's runs (past every position: there is none), which are
   // loaded
   auto load = [&](int n, int (&at)[NT], int buf) {
-    char* to = smem + buf * 2 * KV::BYTES;
+    char* to = smem + buf * (PART / 2);
     const int next = (first + n * NT - ns) * 32;
-    if (n * NT >= ns && next + BN <= s.nk) {  // one after the other, as most are
+    if constexpr (ALONE) {
+      const int64_t j = n < ns ? n * 32 : next;
+      const int rows = s.nk - (int)j < 32 ? s.nk - (int)j : 32;
+      at[0] = (int)j;
+      ks.load(kb + j * a.k_stride * ES, rows, a.dim);
+      vt.load(vb + j * a.v_stride * ES, rows, a.dim, to, wave);
+    } else if (n * NT >= ns && next + BN <= s.nk) {  // one after the other, as most are
 #pragma unroll
       for (int b = 0; b < NT; ++b) at[b] = next + 32 * b;
       kt.load(kb + (int64_t)next * a.k_stride * ES, BN, a.dim, to, wave);
@@ -93,16 +104,24 @@ __global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void 
   if (part < count) load(part, ahead_at, 0);
   for (int i = 0; i * KW < count; ++i) {
     const int n = i * KW + part;
-    attn_settle();
+    if constexpr (ALONE) attn_settle_alone();
+    else attn_settle();
     if (KW > 1 && n >= count) continue;
+    uint4 k[ALONE ? KV::KS : 1];
+    if constexpr (ALONE)
+#pragma unroll
+      for (int st = 0; st < KV::KS; ++st) k[st] = ks.v[st];
 #pragma unroll
     for (int b = 0; b < NT; ++b) at[b] = ahead_at[b];
     if (n + KW < count) load(n + KW, ahead_at, (i + 1) & 1);
-    const char* kl = smem + (i & 1) * 2 * KV::BYTES;
-    const char* vl = kl + KV::BYTES;
+    const char* kl = smem + (i & 1) * (PART / 2);
+    const char* vl = ALONE ? kl : kl + KV::BYTES;
     f32x16 sc[NT];
     ahead<6, KV::KS * NT, 1, T>(
-        [&](int i) { return kt.row(kl, i % NT, i / NT); },
+        [&](int i) {
+          if constexpr (ALONE) return k[i];
+          else return kt.row(kl, i % NT, i / NT);
+        },
         [&](int i, const uint4& f) { sc[i % NT] = mma32<T>(f, q.v[i / NT], i < NT ? f32x16{} : sc[i % NT]); });
     float z[NT * 16], e[NT * 16];
 #pragma unroll
@@ -125,7 +144,7 @@ __global__ __launch_bounds__(64 * NW * KW, KW == 1 || NW * KW > 4 ? 2 : 1) void 
         [&](int i, const uint4& f) { acc[i % KV::CT] = mma32<T>(f, w[i / KV::CT], acc[i % KV::CT]); });
   }
   if constexpr (KW > 1)
-    if (!join_parts<KW, NW, 4 * KV::BYTES, true>(lds, acc, soft.m, soft.l, c, part, wave, lane)) return;
+    if (!join_parts<KW, NW, PART, true>(lds, acc, soft.m, soft.l, c, part, wave, lane)) return;
   const float l = swap_sum32(soft.l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing: 0
   if (a.lse && in && h == 0) a.lse[row * a.q_heads + hq] = l == 0.0f ? -INFINITY : soft.m * a.scale + logf(l);
@@ -145,8 +164,8 @@ void attn_fwd_run(const AttnArgs& a, hipStream_t s) {
   const int64_t items = attn_items(a, false, 32 * NW / HT);
   const dim3 grid((unsigned)(items * (a.q_heads / HT)));
   with_width(a.dim, [&](auto dp, auto du) {
-    constexpr int DP = decltype(dp)::value, K = attn_parts<T, DP>(NW, KW), BN = io<T>::BYTES == 2 ? 64 : 32;
-    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, decltype(du)::value, BN, HT, NW, K>), grid, dim3(64 * NW * K), 0, s, a,
+    constexpr int DP = decltype(dp)::value, BN = io<T>::BYTES == 2 ? 64 : 32;
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, decltype(du)::value, BN, HT, NW, KW>), grid, dim3(64 * NW * KW), 0, s, a,
                        items);
   });
 }
