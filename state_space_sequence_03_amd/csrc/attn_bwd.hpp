@@ -233,11 +233,12 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
   }
 }
 
-// The sums of 32 keys' pieces joined in order: the blocks of the pieces (and
-// blockIdx.z) share the keys' entries, 128 at a time; eight groups of threads
-// each add an eighth of the sums, four entries to a thread.
+// The sums of 32 keys' pieces joined in order: the blocks of the pieces (eight
+// each, z) share the keys' entries, 128 at a time; eight groups of threads each
+// add an eighth of the sums, four entries to a thread.
+constexpr int kJoinZ = 8;
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, int z) {
   __shared__ f32x4 sums[8][32];
   const int sunk = (a.sinks + 31) / 32;
   const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;  // of a piece, all its splits
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int64_t step = (int64_t)sunk * a.kv_heads * a.splits * one;  // from piece to piece
   const float* part = a.part + (int64_t)blockIdx.x * a.splits * one - piece * step + (key ? 0 : 4 * half);
   const int n = keys * a.dim, parts = a.splits * 4, g = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int c = (piece * gridDim.z + blockIdx.z) * 128; c < n; c += pieces * gridDim.z * 128) {
+  for (int c = (piece * kJoinZ + z) * 128; c < n; c += pieces * kJoinZ * 128) {
     const int e = c + lane * 4;
     f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
     if (e < n) {
@@ -285,21 +286,22 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 
 // The splits of 128 keys joined in order (those of the sinks that are summed in
 // pieces excepted): a block per item, dk and dv by blockIdx.y, a quarter of the
-// keys by blockIdx.z.
+// keys by z.
+constexpr int kJoinSplitsZ = 4;
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64_t items, int64_t pieces) {
+__device__ __forceinline__ void join_splits(const AttnArgs& a, int64_t items, int64_t pieces, int z) {
   const int64_t hk = blockIdx.x / (uint32_t)items;
   AttnSeq s;
   int t;
   if (!attn_item<true>(a, blockIdx.x % (uint32_t)items, 128, 0, s, t)) return;
-  const int j0 = t * 128 + blockIdx.z * 32;
+  const int j0 = t * 128 + z * 32;
   if (s.nq > a.piece && j0 < (a.sinks + 31) / 32 * 32) return;
   const bool key = blockIdx.y == 0;
   void* out = key ? a.dk : a.dv;
   if (!out) return;
   const int keys = s.nk - j0 < 32 ? s.nk - j0 : 32, n = keys * a.dim;
   const int64_t wave = 32 * a.dim;
-  const float* part = a.part + ((pieces + (int64_t)blockIdx.x * a.splits) * 8 + (key ? 0 : 4) + blockIdx.z) * wave;
+  const float* part = a.part + ((pieces + (int64_t)blockIdx.x * a.splits) * 8 + (key ? 0 : 4) + z) * wave;
   for (int e = (int)threadIdx.x * 4; e < n; e += 1024) {
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -310,6 +312,20 @@ __global__ __launch_bounds__(256) void attn_join_splits_kernel(AttnArgs a, int64
     }
     const int j = e / a.dim;
     io<T>::store4(out, (s.k0 + j0 + j) * (key ? a.dk_stride : a.dv_stride) + hk * a.dim + e - j * a.dim, x);
+  }
+}
+
+// Both in one launch (z from z0 on), or the one that there is: `joined` blocks
+// of pieces, `split` of items.  (1 x 1500 queries, 8/2 heads of 128, window 200: dk
+// and dv 42 us with two launches, 36 so.)
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int64_t items, int64_t pieces, int64_t joined,
+                                                        int64_t split, int z0) {
+  const int z = blockIdx.z + z0;
+  if (z < kJoinZ) {
+    if (blockIdx.x < joined) join_pieces<T>(a, z);
+  } else if (blockIdx.x < split) {
+    join_splits<T>(a, items, pieces, z - kJoinZ);
   }
 }
 
@@ -474,10 +490,11 @@ void attn_bwd_run(const AttnArgs& a, hipStream_t s) {
   if ((!a.dk && !a.dv) || tiles == 0) return;
   hipLaunchKernelGGL((attn_dkv_kernel<T, DP, DU, io<T>::BYTES == 2 ? 64 : 32>),
                      dim3((unsigned)(pieces + blocks * a.splits)), block, 0, s, a, tiles, pieces);
-  if (pieces > 0)
-    hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)(pieces / a.splits), 2, 8), block, 0, s, a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((attn_join_splits_kernel<T>), dim3((unsigned)blocks, 2, 4), block, 0, s, a, tiles, pieces);
+  const int64_t joined = pieces / a.splits, split = a.splits > 1 ? blocks : 0;
+  if (joined == 0 && split == 0) return;
+  const int z0 = joined > 0 ? 0 : kJoinZ, z1 = split > 0 ? kJoinZ + kJoinSplitsZ : kJoinZ;
+  hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)(joined > split ? joined : split), 2, z1 - z0), block, 0, s, a,
+                     tiles, pieces, joined, split, z0);
 }
 
 template <typename T>
