@@ -776,10 +776,15 @@ def _tokens(name, t, shape, dtype, device):
     and tokens evenly further apart (a slice of the heads of a wider tensor)."""
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         _expect(name, t, shape, dtype, device)
+    return _spacing(name, t, shape)
+
+
+def _spacing(name, t, shape):
+    """_tokens of an operand whose shape, type and device are known to be right."""
     if t.is_contiguous():
         return t.data_ptr(), 0
     st = t.stride()
-    heads, dim = shape[-2:]
+    heads, dim = shape[-2], shape[-1]
     if (dim == 1 or st[-1] == 1) and (heads == 1 or st[-2] == dim):
         step = None  # elements between tokens; dimensions of one entry say nothing
         inner = 1    # tokens that the dimensions looked at so far hold
@@ -799,10 +804,10 @@ def _tokens(name, t, shape, dtype, device):
     raise ValueError(f"{name}: must be contiguous, or with heads side by side and evenly spaced tokens")
 
 
-def _heads_of(name, t, least):
-    if t.dim() < least or t.shape[-1] == 0:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (..., heads, head_dim)")
-    return t.shape[:-2], t.shape[-2], t.shape[-1]
+def _heads_of(name, shape, least):
+    if len(shape) < least or shape[-1] == 0:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected (..., heads, head_dim)")
+    return shape[:-2], shape[-2], shape[-1]
 
 
 def _norm_rope_dims(q, k, gain_q, gain_k, theta, pos, halves):
@@ -813,24 +818,27 @@ def _norm_rope_dims(q, k, gain_q, gain_k, theta, pos, halves):
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is required")
-    io, dev, f32 = x.dtype, x.device, torch.float32
-    lead, Hq, D = _heads_of("q" if q is not None else "k", x, 3)
+    io, dev, f32, shape = x.dtype, x.device, torch.float32, x.shape
+    lead, Hq, D = _heads_of("q" if q is not None else "k", shape, 3)
     qs = ks = pq = pk = None
     sq = sk = Hk = 0
     if q is not None:
-        qs = q.shape
-        pq, sq = _tokens("q", q, qs, io, dev)
+        qs = shape
+        pq, sq = _spacing("q", q, qs)
     else:
         Hq = 0
     if k is not None:
         ks = k.shape
-        if len(ks) != len(lead) + 2 or ks[:-2] != lead or ks[-1] != D:
+        if ks[:-2] != lead or ks[-1] != D:
             raise ValueError(f"k: shape {tuple(ks)}, expected {tuple(lead)} tokens of heads of {D}")
+        if k.dtype is not io or k.device != dev:
+            _expect("k", k, ks, io, dev)
         Hk = ks[-2]
-        pk, sk = _tokens("k", k, ks, io, dev)
+        pk, sk = _spacing("k", k, ks)
     rope = 0
     if theta is not None:
-        rope = 2 * theta.shape[0] if theta.dim() == 1 else -1
+        ts = theta.shape
+        rope = 2 * ts[0] if len(ts) == 1 else -1
         if not 0 <= rope <= D:
             raise ValueError(f"theta: shape {tuple(theta.shape)}, expected at most (head_dim / 2,) = ({D // 2},)")
         theta = _vec("theta", theta, (rope // 2,), f32, dev)
@@ -941,8 +949,8 @@ def _attn_dims(q, k, v, starts, window, sinks, scale, grads=False):
     and starts, shapes of q and k, type, device."""
     io, dev, ps, rows, kv_rows, flags = q.dtype, q.device, None, 0, 0, 0
     qs, ks = q.shape, k.shape
-    lead, Hq, D = _heads_of("q", q, 3)
-    pq, sq = _tokens("q", q, qs, io, dev)
+    lead, Hq, D = _heads_of("q", qs, 3)
+    pq, sq = _spacing("q", q, qs)
     if starts is None:
         if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[3] != D:
             raise ValueError("q is (batch, q_len, heads, head_dim), k and v (batch, kv_len, heads, head_dim)")
@@ -1072,8 +1080,8 @@ def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sink
     if len(qs) != 4 or len(ks) != 4 or len(cs) != 4 or ks[:2] != qs[:2] or cs[0] != qs[0] or cs[2:] != ks[2:]:
         raise ValueError("q, k, v are (batch, tokens, heads, head_dim), "
                          "the caches (batch, capacity, heads of k, head_dim)")
-    _, Hq, D = _heads_of("q", q, 4)
-    pq, sq = _tokens("q", q, qs, io, dev)
+    _, Hq, D = _heads_of("q", qs, 4)
+    pq, sq = _spacing("q", q, qs)
     if ks[3] != D:
         raise ValueError(f"k: head_dim {ks[3]}, expected {D}")
     pk, sk = _tokens("k", k, ks, io, dev)
