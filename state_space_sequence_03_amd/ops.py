@@ -983,7 +983,9 @@ def _sequences(name, t, shape, dtype, device):
         step = t.stride(1) if t.stride(1) >= row else row if shape[1] == 1 else 0
         if step > 0 and between % step == 0 and between // step > shape[1]:
             p, s = _tokens(name, t[0], shape[1:], dtype, device)
-            return p, s, between // (s or row)
+            # a single token says nothing about the rows it is one of: its own width, or else what divides the distance
+            unit = s or (row if between % row == 0 else step)
+            return p, 0 if unit == row else unit, between // unit
     return _tokens(name, t, shape, dtype, device) + (0,)
 
 

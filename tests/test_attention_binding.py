@@ -250,3 +250,38 @@ def test_single_tokens_of_a_projection(fake):
     ops.window_attn_fwd(q, cache, cache)
     dims = fake.calls[0][1][0]
     assert dims.kv_rows == (1 << 21) // (Hk * D) and dims.k_stride in (0, Hk * D)
+
+
+# heads of a row, those taken, slots of a cache: the distance of the sequences is a multiple of the row taken or not
+@pytest.mark.parametrize("all_heads,taken,slots", [(7, 2, 5), (6, 4, 3), (5, 3, 5), (3, 2, 3), (5, 2, 5), (8, 2, 9), (2, 2, 9)])
+@pytest.mark.parametrize("length", [1, 2])
+def test_sequences_lie_where_their_keys_do(fake, all_heads, taken, slots, length):
+    # the first tokens of a cache of wider rows: what the library is told leads to every sequence's first key
+    n = 3
+    cache = heads(all_heads, n, slots)
+    wide = heads(all_heads * slots, n, 1)  # the same memory layout, single tokens of very wide rows
+    q = heads(2 * taken, n, length)
+    for keys in ([cache[:, :length, :taken], cache[:, :length, -taken:]],
+                 [wide[:, :, :taken], wide[:, :, -taken:]] if length == 1 else []):
+        if not keys:
+            continue
+        k, v = keys
+        o, lse = ops.window_attn_fwd(q, k, v, want_lse=True)
+        ops.window_attn_bwd(q, k, v, o, lse, o, want_dk=False, want_dv=False)
+        for name, args in fake.calls:
+            dims = args[0]
+            for stride in (dims.k_stride, dims.v_stride):
+                assert (dims.kv_rows or length) * (stride or taken * D) == k.stride(0) == v.stride(0), name
+        fake.calls.clear()
+
+
+def test_single_keys_too_far_apart(fake):
+    # a distance past the widest row there may be: by the rows it divides into, or else as evenly spaced tokens, whose
+    # stride the library refuses
+    row, q = Hk * D, heads(Hq, B, 1)
+    for step, between in ((3 * row, 3 * row << 16), (3 * row + 8, (3 * row + 8) << 16), (1 << 21, 1 << 22), (3 * row, (1 << 21) + 8)):
+        k = torch.empty_strided((B, 1, Hk, D), (between, step, D, 1), dtype=bf)
+        ops.window_attn_fwd(q, k, k)
+        dims = fake.calls[-1][1][0]
+        assert (dims.kv_rows or 1) * (dims.k_stride or row) == between
+        assert dims.k_stride <= 1 << 20 or dims.kv_rows == 0

@@ -165,6 +165,23 @@ def test_keys_of_a_longer_cache(ops):
     assert torch.equal(got, want) and bool(torch.isfinite(got).all())
 
 
+@pytest.mark.parametrize("all_heads,taken,slots", [(7, 2, 5), (6, 4, 3), (5, 3, 5), (3, 2, 3), (8, 2, 9)])
+def test_first_keys_of_a_cache(ops, all_heads, taken, slots):
+    # one key of each sequence, the sequences a whole number of its row apart or not: as with contiguous keys
+    r = np.random.default_rng(17)
+    kv = draw(r, (4, slots, all_heads, 64), "bf16")
+    q, do = draw(r, (4, 3, 2 * taken, 64), "bf16"), draw(r, (4, 3, 2 * taken, 64), "bf16")
+    k, v = kv[:, :1, :taken], kv[:, :1, -taken:]
+    plain = k.contiguous(), v.contiguous()
+    want, lse = ops.window_attn_fwd(q, *plain, want_lse=True)
+    got, lse2 = ops.window_attn_fwd(q, k, v, want_lse=True)
+    assert torch.equal(got, want) and torch.equal(lse2, lse) and torch.equal(got[:, 2, ::2], v[:, 0])
+    g, h = ops.window_attn_bwd(q, *plain, want, lse, do), ops.window_attn_bwd(q, k, v, got, lse2, do)
+    assert all(torch.equal(g[n], h[n]) for n in g)
+    one = ops.window_attn_bwd(q, k, v, got, lse2, do, want_dk=False, want_dv=False)
+    assert torch.equal(one["dq"], g["dq"])
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_large_scores(ops, io):
     # softmaxes that are nearly one-hot, rising and falling along the keys; the
