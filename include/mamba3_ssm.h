@@ -537,7 +537,9 @@ typedef struct {
  * kv_rows) rows of which the first kv_len are keys; starts is ignored.  With it:
  * q, k, v and o have `rows` rows, sequence b those from starts[b] to
  * starts[b + 1] - 1 (batch + 1 entries, rising, on the device; queries and keys
- * have the same); rows of no sequence are neither read nor written.
+ * have the same); rows of no sequence are neither read nor written.  Starts that
+ * do not rise, or lie past the rows, give undefined results, but no access
+ * outside the operands and the workspace.
  * lse: nullable (tokens, q_heads) fp32, written when given (the backward takes
  * it).
  * Alignment: io pointers, and rows (strides), 16 bytes; starts 8.  batch times

@@ -235,10 +235,12 @@ __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void at
 
 // The sums of 32 keys' pieces joined in order: the blocks of the pieces (eight
 // each, z) share the keys' entries, 128 at a time; eight groups of threads each
-// add an eighth of the sums, four entries to a thread.
+// add an eighth of the sums, four entries to a thread.  joined: blocks of all
+// pieces, whose sums there are; starts that do not rise make up sequences with more
+// pieces than that.
 constexpr int kJoinZ = 8;
 template <typename T>
-__device__ __forceinline__ void join_pieces(const AttnArgs& a, int z) {
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, uint32_t joined, int z) {
   __shared__ f32x4 sums[8][32];
   const int sunk = (a.sinks + 31) / 32;
   const uint32_t id = blockIdx.x / (uint32_t)a.kv_heads;  // of a piece, all its splits
@@ -249,7 +251,8 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, int z) {
   if (!attn_item<false>(a, id / (uint32_t)sunk, a.piece, a.piece, s, piece)) return;
   const int keys = s.nk - j0 < 32 ? s.nk - j0 : 32;
   if (keys <= 0) return;
-  const int pieces = (s.nq + a.piece - 1) / a.piece;
+  const int there = (int)(joined / (uint32_t)a.kv_heads / (uint32_t)sunk - id / (uint32_t)sunk) + piece;
+  const int whole = (s.nq + a.piece - 1) / a.piece, pieces = whole < there ? whole : there;
   const bool key = blockIdx.y == 0;
   void* out = key ? a.dk : a.dv;
   if (!out) return;
@@ -323,7 +326,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int64_t item
                                                         int64_t split, int z0) {
   const int z = blockIdx.z + z0;
   if (z < kJoinZ) {
-    if (blockIdx.x < joined) join_pieces<T>(a, z);
+    if (blockIdx.x < joined) join_pieces<T>(a, (uint32_t)joined, z);
   } else if (blockIdx.x < split) {
     join_splits<T>(a, items, pieces, z - kJoinZ);
   }

@@ -298,3 +298,24 @@ def test_large_scores_in_parts(ops, io, D):
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_packed_sequences_in_parts(ops, io, lens, window, sinks, D):
     test_packed_sequences(ops, io, lens, window, sinks, D)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_starts_that_do_not_rise(ops, io):
+    # 24 pieces of 256 queries where 3000 rows have 22 at most: the call stays within its workspace, and what it does
+    # not write there it does not read
+    rows, heads, D = 3000, 8, 64
+    print(f"starts that fall {io} {rows} rows", flush=True)
+    r = np.random.default_rng(18)
+    q, k, v, do = (draw(r, (rows, heads, D), io) for _ in range(4))
+    starts = torch.tensor([0, rows, 0, rows], device="cuda")
+    dims = ops.AttnDims(batch=3, rows=rows, q_heads=heads, kv_heads=heads, head_dim=D, window=20, sinks=4, scale=0.125,
+                        io_dtype=ops.M3_BF16 if io == "bf16" else ops.M3_F32, flags=ops.M3_FLAG_PACKED)
+    need = ops.window_attn_bwd_workspace_size(dims)
+    memory = torch.full((2 * need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN, read as fp32
+    see = {"window": 20, "sinks": 4, "scale": 0.125, "starts": starts}
+    o, lse = ops.window_attn_fwd(q, k, v, want_lse=True, **see)
+    g = ops.window_attn_bwd(q, k, v, o, lse, do, workspace=memory[:need], **see)
+    torch.cuda.synchronize()
+    assert bool((memory[need:] == 0xFF).all())
+    assert all(bool(torch.isfinite(t).all()) for t in (o, lse, *g.values()))
