@@ -520,7 +520,7 @@ typedef struct {
   int64_t sinks;           /* first tokens that stay visible behind the window */
   int64_t q_stride, k_stride, v_stride, o_stride;
   int64_t do_stride, dq_stride, dk_stride, dv_stride;  /* backward */
-  float scale;             /* of the scores: > 0 and finite */
+  float scale;             /* of the scores: > 0, at most 2.35e38 */
   int32_t io_dtype;
   int32_t flags;           /* 0 or M3_FLAG_PACKED */
   int32_t reserved;        /* must be 0 */

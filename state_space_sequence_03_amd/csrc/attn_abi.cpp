@@ -76,7 +76,7 @@ m3_status check_heads(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t 
     return M3_ERR_SHAPE;
   if (io_dtype != M3_F32 && io_dtype != M3_BF16) return M3_ERR_UNSUPPORTED;
   if (reserved != 0 || batch > kMaxRows || dim > 128 || dim % 8 != 0) return M3_ERR_UNSUPPORTED;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return M3_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || scale > 2.35e38f) return M3_ERR_UNSUPPORTED;  // scale log2(e) is finite
   return M3_OK;
 }
 bool off16(std::initializer_list<int64_t> strides, int32_t io_dtype) {

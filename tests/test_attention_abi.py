@@ -187,3 +187,12 @@ def test_dims_match_the_header(L, tmp_path):
     for s in names.values():
         want += [ctypes.sizeof(s)] + [getattr(s, f).offset for f, _ in s._fields_]
     assert got == want
+
+
+def test_scales_that_leave_the_range(L):
+    # the kernels take scores times scale log2(e): a scale whose product with it is infinite made NaN of scores of 0
+    for fn, names, dims in (("window_attn_fwd", FWD, attn), ("window_attn_bwd", BWD, attn), ("window_attn_decode", STEP, step)):
+        for scale in (2.36e38, 2.9e38, 3.0e38):
+            assert call(L, fn, names, dims(L, scale=scale)) == L.M3_ERR_UNSUPPORTED, (fn, scale)
+        for scale in (1e-40, 2.35e38):
+            assert call(L, fn, names, dims(L, scale=scale, batch=0)) == L.M3_OK, (fn, scale)
