@@ -1109,6 +1109,8 @@ def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sink
 def window_cache_slots(pos, sinks, capacity):
     """Slots of a cache of `capacity` slots where window_attn_decode keeps the
     tokens at positions pos (an integer tensor): for filling one after a prefill."""
+    if not 0 <= sinks < capacity:
+        raise ValueError(f"a cache of {capacity} slots has no ring behind {sinks} sinks")
     return _torch().where(pos < sinks, pos, sinks + (pos - sinks) % (capacity - sinks))
 
 

@@ -285,3 +285,10 @@ def test_single_keys_too_far_apart(fake):
         dims = fake.calls[-1][1][0]
         assert (dims.kv_rows or 1) * (dims.k_stride or row) == between
         assert dims.k_stride <= 1 << 20 or dims.kv_rows == 0
+
+
+def test_slots_of_a_cache_without_a_ring(fake):
+    # refused on the host: the remainder by 0 or less would give slots outside the cache
+    for sinks, capacity in ((4, 4), (5, 4), (0, 0), (-1, 4)):
+        refused(ValueError, ops.window_cache_slots, torch.arange(3), sinks, capacity)
+    assert ops.window_cache_slots(torch.arange(5), 3, 4).tolist() == [0, 1, 2, 3, 3]
