@@ -120,11 +120,13 @@ void attn_by_size(const AttnArgs& a, F&& f) {
   else if (G % 2 == 0) f(two, four, one);
   else f(one, four, one);
 }
-// Pieces of the sequences that are longer than one, at most.
+// Pieces of the sequences that are longer than one, at most: every whole piece of
+// all rows, and one that is not whole for each such sequence.
 inline int64_t attn_pieces(const AttnArgs& a) {
   if (a.sinks == 0 || a.window >= kNoWindow) return 0;
   if (!a.starts) return a.q_len > a.piece ? a.batch * ((a.q_len + a.piece - 1) / a.piece) : 0;
-  return a.rows / a.piece * 2;  // a sequence of more than a piece has fewer pieces than twice its whole ones
+  const int64_t whole = a.rows / a.piece;
+  return whole + (a.batch < whole ? a.batch : whole);
 }
 
 inline int64_t attn_piece_blocks(const AttnArgs& a) { return attn_pieces(a) * ((a.sinks + 31) / 32) * a.kv_heads; }

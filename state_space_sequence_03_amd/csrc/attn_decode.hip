@@ -48,14 +48,18 @@ int attn_bwd_piece(const AttnArgs& a) {
 // 1 x 2048, 16/4 x 128, window 512, has 5 instead of 6: 61 -> 55 us.)  In fp32 a
 // wide head's block has a CU to itself, so one round of the chip is best: 4 x 512
 // queries, 2 heads of 128, window 64, with four 38 us, 60 with two; 2 x 777, 5 heads
-// of 72, with two 47 us, 55 with four.
+// of 72, with two 47 us, 55 with four.  Of packed sequences every whole piece counts
+// twice: what most leave of the chip is too little for more (8000 queries in one,
+// 8/2 heads of 128, window 64: 64 us with the two that this gives, 76 with three).
 int attn_bwd_splits(int io_bf16, const AttnArgs& a) {
   const int64_t blocks = attn_items(a, true, 128) * a.kv_heads;
   if (blocks == 0 || blocks >= 192) return 1;
   int64_t rows = a.starts ? a.rows : a.q_len;
   if (a.window < kNoWindow && rows > (int64_t)a.window + 128) rows = (int64_t)a.window + 128;
   const int64_t step = io_bf16 ? 64 : 32, most = (rows + step - 1) / step * (a.q_heads / a.kv_heads) / 2;
-  const int64_t busy = blocks + attn_piece_blocks(a);
+  int64_t pieces = attn_piece_blocks(a);
+  if (a.starts && pieces > 0) pieces = a.rows / a.piece * 2 * ((a.sinks + 31) / 32) * a.kv_heads;
+  const int64_t busy = blocks + pieces;
   int64_t n = io_bf16 ? (384 + busy - 1) / busy : (a.dim > 64 ? 256 : 512) / busy;
   n = n < most ? n : most;
   return n < 1 ? 1 : n < 16 ? (int)n : 16;

@@ -196,3 +196,21 @@ def test_scales_that_leave_the_range(L):
             assert call(L, fn, names, dims(L, scale=scale)) == L.M3_ERR_UNSUPPORTED, (fn, scale)
         for scale in (1e-40, 2.35e38):
             assert call(L, fn, names, dims(L, scale=scale, batch=0)) == L.M3_OK, (fn, scale)
+
+
+def test_backward_workspace_of_packed_sequences(L):
+    # the pieces that there can be, and no more: those of equal lengths and one for every sequence; 8192 at most
+    def units(**kw):
+        d = attn(L, q_heads=64, kv_heads=8, head_dim=128, **kw)
+        rows = kw.get("rows") or kw["batch"] * kw["q_len"]
+        return (L.window_attn_bwd_workspace_size(d) - 2 * ((4 * 64 * rows + 255) // 256 * 256)) / (8 * 32 * 128 * 4)
+
+    packed = dict(flags=L.M3_FLAG_PACKED, window=16, sinks=130)
+    whole = units(batch=1, q_len=16384, kv_len=16384, window=16, sinks=130)
+    assert whole == 64 * 5 * 8
+    for batch in (1, 2, 21, 64, 5000):
+        assert units(batch=batch, rows=16384, **packed) == whole + min(batch, 64) * 5 * 8, batch
+    for batch in (1, 5000):
+        for rows in (65536, 1 << 18):
+            for sinks in (1, 130, 512, 3000):
+                assert units(batch=batch, rows=rows, **{**packed, "sinks": sinks}) <= 8192, (batch, rows, sinks)

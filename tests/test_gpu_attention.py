@@ -302,7 +302,7 @@ def test_packed_sequences_in_parts(ops, io, lens, window, sinks, D):
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_starts_that_do_not_rise(ops, io):
-    # 24 pieces of 256 queries where 3000 rows have 22 at most: the call stays within its workspace, and what it does
+    # 24 pieces of 256 queries where 3 sequences of 3000 rows have 14 at most: the call stays within its workspace, and what it does
     # not write there it does not read
     rows, heads, D = 3000, 8, 64
     print(f"starts that fall {io} {rows} rows", flush=True)
