@@ -486,7 +486,9 @@ typedef struct {
  * theta[pair]: (a cos w - b sin w, a sin w + b cos w).
  * gain_q, gain_k: nullable (D) (NULL: 1).  eps: >= 0 and finite.
  * theta: (rope_dim/2) fp32 angle rates, required unless rope_dim is 0.
- * pos: nullable (rows) positions, any sign.  Angles are taken in fp64.
+ * pos: nullable (rows) positions, any sign.  Angles are taken in fp64, squares
+ * summed in fp32: entries should lie below about 2^60 (a sum that overflows
+ * gives a head of zeros) and, without eps, above 2^-60.
  * q_out and k_out may be q and k themselves (same strides).
  * Alignment: an element's size (pos 8). */
 m3_status mamba3_qk_norm_rope_fwd(const m3_norm_rope_dims* d, const void* q, const void* k, const float* gain_q,
@@ -537,13 +539,17 @@ typedef struct {
  * kv_rows) rows of which the first kv_len are keys; starts is ignored.  With it:
  * q, k, v and o have `rows` rows, sequence b those from starts[b] to
  * starts[b + 1] - 1 (batch + 1 entries, rising, on the device; queries and keys
- * have the same); rows of no sequence are neither read nor written.  Starts that
- * do not rise, or lie past the rows, give undefined results, but no access
- * outside the operands and the workspace.
+ * have the same); rows of no sequence are not written, and what they hold does
+ * not matter.  Starts that do not rise, or lie past the rows, give undefined
+ * results, but no access outside the operands and the workspace.
  * lse: nullable (tokens, q_heads) fp32, written when given (the backward takes
  * it).
- * Alignment: io pointers, and rows (strides), 16 bytes; starts 8.  batch times
- * q_heads times 128-query tiles is at most 2^24 - 1. */
+ * Alignment: io pointers, and rows (strides), 16 bytes; starts 8.
+ * Limits (M3_ERR_UNSUPPORTED beyond them), n being 2^24 - 1:
+ *   equal lengths: batch q_len, batch kv_len and q_heads batch ceil(q_len / 128)
+ *   at most n, kv_heads batch ceil(kv_len / 128) at most n - 2^15, kv_rows at
+ *   most 2^40;
+ *   packed: q_heads (rows / 128 + the smaller of batch and rows) at most n - 2^15. */
 m3_status mamba3_window_attn_fwd(const m3_attn_dims* d, const void* q, const void* k, const void* v,
                                  const int64_t* starts, void* o, float* lse, void* stream);
 
@@ -551,11 +557,16 @@ m3_status mamba3_window_attn_fwd(const m3_attn_dims* d, const void* q, const voi
  * do o (o and lse as the forward gave them),
  *   ds = p (dp - delta),  dq = scale ds k,  dk = scale ds^T q,  dv = p^T do,
  * dk and dv summed over the query heads that share a head.  dq, dk, dv:
- * nullable, each by itself.  Keys that no query sees get zeros.
+ * nullable, each by itself.  Keys that no query sees get zeros.  dk and dv lie
+ * as k and v do: with kv_rows above kv_len their rows past kv_len are not
+ * written.
+ * Beside the forward's limits, tokens times ceil(q_heads / 16) is at most
+ * 2^24 - 1 (with 32 heads, half of the forward's tokens).
  * workspace: at least mamba3_window_attn_bwd_workspace_size(d) bytes (per query
  * and head two fp32 statistics, and partial sums of the sinks' keys, which
- * whole sequences see: those are summed in pieces side by side).  16-byte
- * aligned, as every io pointer. */
+ * whole sequences see: those are summed in pieces of at least 256 queries side
+ * by side, 1024 D bytes for each piece, 32 keys with sinks among them and head of
+ * keys, 8192 such sums at most).  16-byte aligned, as every io pointer. */
 m3_status mamba3_window_attn_bwd(const m3_attn_dims* d, const void* q, const void* k, const void* v, const void* o,
                                  const float* lse, const void* dout, const int64_t* starts, void* dq, void* dk,
                                  void* dv, void* workspace, size_t workspace_bytes, void* stream);
@@ -586,6 +597,11 @@ typedef struct {
  * With a window, capacity - sinks is at least window + T - 1 (M3_ERR_SHAPE
  * otherwise); without one, at least T, and every token sees all earlier ones
  * that the cache holds after the write.
+ * The last of the new tokens may be dropped (drafted ones that were refused) by a
+ * lens that does not count them: the next call writes over them.  The older
+ * tokens that they had overwritten are behind every later token's window; without
+ * a window this holds until the cache wraps, and not from then on: a dropped
+ * token would be seen at the position of the one it overwrote.
  * workspace: at least mamba3_window_attn_decode_workspace_size(d) bytes
  * (results of parts of a long cache; may be 0).
  * Alignment: io pointers, strides and the workspace 16 bytes, lens 8. */

@@ -1069,11 +1069,13 @@ def window_attn_decode_workspace_size(dims: AttnDecodeDims) -> int:
 
 def mamba3_window_attn_decode(q, k, v, k_cache, v_cache, lens, *, window=0, sinks=0, scale=None, o=None,
                               workspace=None, stream=None):
-    """The T new tokens q (batch, T, q_heads, D), k, v (batch, T, kv_heads, D),
-    written to the caches (batch, capacity, kv_heads, D) in place and attending
-    over them.  lens (batch, int64): tokens in each cache before the call
-    (negative: an idle sequence).  Position p lies in slot p below `sinks`, else
-    in slot sinks + (p - sinks) mod (capacity - sinks) (window_cache_slots).
+    """The T new tokens (M3_DECODE_MAX_TOKENS at most) q (batch, T, q_heads, D),
+    k, v (batch, T, kv_heads, D), written to the caches (batch, capacity, kv_heads,
+    D) in place and attending over them.  lens (batch, int64): tokens in each cache
+    before the call (negative: an idle sequence; fewer than the last call left
+    drops its last tokens, with a window or before the cache wraps).  Position p
+    lies in slot p below `sinks`, else in slot sinks + (p - sinks) mod (capacity -
+    sinks) (window_cache_slots).
     Returns o (batch, T, q_heads, D)."""
     if stream is not None:
         return _on_stream(stream, q, mamba3_window_attn_decode, q, k, v, k_cache, v_cache, lens, window=window,

@@ -214,3 +214,41 @@ def test_backward_workspace_of_packed_sequences(L):
         for rows in (65536, 1 << 18):
             for sinks in (1, 130, 512, 3000):
                 assert units(batch=batch, rows=rows, **{**packed, "sinks": sinks}) <= 8192, (batch, rows, sinks)
+
+
+def test_documented_limits(L):
+    # each limit and the next size; nothing is launched: an accepted call ends at a null pointer, or has no queries
+    N = (1 << 24) - 1
+
+    def fwd(**kw):
+        return call(L, "window_attn_fwd", FWD, attn(L, **{**dict(head_dim=8, window=0, sinks=0), **kw}), q=None)
+
+    def bwd(**kw):
+        return call(L, "window_attn_bwd", BWD, attn(L, **{**dict(head_dim=8, window=0, sinks=0), **kw}), q=None, k=None)
+
+    one = dict(q_heads=1, kv_heads=1)
+    tiles = dict(batch=N // 255, q_len=1, kv_len=0)  # 255 divides 2^24 - 1
+    keys = dict(batch=(N - 32768) // 255, q_len=0, kv_len=1)
+    packed = dict(one, flags=L.M3_FLAG_PACKED, rows=N)
+    for go in (fwd, bwd):
+        fits = L.M3_ERR_NULL
+        none = L.M3_OK if go is fwd else L.M3_ERR_NULL
+        assert go(**tiles, q_heads=255, kv_heads=255) == fits
+        assert go(**tiles, q_heads=256, kv_heads=256) == L.M3_ERR_UNSUPPORTED
+        assert go(**keys, q_heads=255, kv_heads=255) == none
+        assert go(**{**keys, "batch": keys["batch"] + 1}, q_heads=255, kv_heads=255) == L.M3_ERR_UNSUPPORTED
+        assert go(**one, batch=1, q_len=N, kv_len=N) == fits
+        for bad in (dict(batch=2, q_len=1 << 23, kv_len=1), dict(batch=2, q_len=1, kv_len=1 << 23)):
+            assert go(**one, **bad) == L.M3_ERR_UNSUPPORTED, bad
+        assert go(**one, batch=1, q_len=1, kv_len=1, kv_rows=1 << 40) == fits
+        assert go(**one, batch=1, q_len=1, kv_len=1, kv_rows=(1 << 40) + 1) == L.M3_ERR_UNSUPPORTED
+        most = N - 32768 - N // 128
+        assert go(**packed, batch=most) == fits
+        assert go(**packed, batch=most + 1) == L.M3_ERR_UNSUPPORTED
+    # the backward's statistics, sixteen heads of a token to a block
+    wide = dict(flags=L.M3_FLAG_PACKED, batch=1, q_heads=32, kv_heads=4)
+    assert fwd(**wide, rows=N // 2 + 1) == L.M3_ERR_NULL and bwd(**wide, rows=N // 2) == L.M3_ERR_NULL
+    assert bwd(**wide, rows=N // 2 + 1) == L.M3_ERR_UNSUPPORTED
+    # new tokens over a cache
+    for T, status in ((L.M3_DECODE_MAX_TOKENS, L.M3_ERR_NULL), (L.M3_DECODE_MAX_TOKENS + 1, L.M3_ERR_UNSUPPORTED)):
+        assert call(L, "window_attn_decode", STEP, step(L, tokens=T, capacity=100, window=30), q=None) == status

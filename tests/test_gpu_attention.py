@@ -165,6 +165,30 @@ def test_keys_of_a_longer_cache(ops):
     assert torch.equal(got, want) and bool(torch.isfinite(got).all())
 
 
+@pytest.mark.parametrize("n,m,window,sinks", [(300, 300, 40, 3), (40, 90, 0, 0), (700, 700, 60, 3)])
+def test_gradients_laid_out_as_a_cache(ops, n, m, window, sinks):
+    # the library's own call with kv_rows above kv_len: dk and dv lie as k and v do, their other rows stay as they were
+    r = np.random.default_rng(16)
+    B, Hq, Hk, D, rows = 2, 4, 2, 64, m + 37
+    q, do = draw(r, (B, n, Hq, D), "bf16"), draw(r, (B, n, Hq, D), "bf16")
+    k, v = draw(r, (B, rows, Hk, D), "bf16"), draw(r, (B, rows, Hk, D), "bf16")
+    k[:, m:] = v[:, m:] = float("nan")
+    see = {"window": window, "sinks": sinks, "scale": 0.125}
+    o, lse = ops.window_attn_fwd(q, k[:, :m], v[:, :m], want_lse=True, **see)
+    want = ops.window_attn_bwd(q, k[:, :m].contiguous(), v[:, :m].contiguous(), o, lse, do, **see)
+    dims = ops.AttnDims(batch=B, q_len=n, kv_len=m, kv_rows=rows, q_heads=Hq, kv_heads=Hk, head_dim=D, io_dtype=ops.M3_BF16,
+                        **see)
+    out = [torch.full_like(t, 5.0) for t in (q, k, v)]
+    memory = torch.empty(ops.window_attn_bwd_workspace_size(dims), dtype=torch.uint8, device="cuda")
+    at = [t.data_ptr() for t in (q, k, v, o, lse, do)]
+    st = ops.lib().mamba3_window_attn_bwd(dims, *at, None, *(t.data_ptr() for t in out), memory.data_ptr(), memory.numel(),
+                                          torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == ops.M3_OK and torch.equal(out[0], want["dq"])
+    assert torch.equal(out[1][:, :m], want["dk"]) and torch.equal(out[2][:, :m], want["dv"])
+    assert bool((out[1][:, m:] == 5.0).all()) and bool((out[2][:, m:] == 5.0).all())
+
+
 @pytest.mark.parametrize("all_heads,taken,slots", [(7, 2, 5), (6, 4, 3), (5, 3, 5), (3, 2, 3), (8, 2, 9)])
 def test_first_keys_of_a_cache(ops, all_heads, taken, slots):
     # one key of each sequence, the sequences a whole number of its row apart or not: as with contiguous keys

@@ -194,3 +194,24 @@ def test_very_long_sequences(ops, window):
         got.append((ops.window_attn_decode(q, k, v, *c, lens, window=window, sinks=sinks),) + c)
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("window,sinks,capacity,lens", [(60, 4, 71, [0, 30, 66, 70, 100, 1000]), (1, 0, 8, [0, 5, 8, 100]),
+                                                        (0, 3, 90, [0, 2, 60, 74])])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_dropped_tokens(ops, io, window, sinks, capacity, lens):
+    # 8 drafted tokens, 3 of which stay: what follows is the same as over a cache that never held the others
+    print(f"dropped tokens {io} window {window} capacity {capacity}", flush=True)
+    r = np.random.default_rng(9)
+    B, see = len(lens), {"window": window, "sinks": sinks}
+    kc, vc = draw(r, (B, capacity, 2, 64), io), draw(r, (B, capacity, 2, 64), io)
+    clean = kc.clone(), vc.clone()
+    draft = [draw(r, (B, 8, h, 64), io) for h in (4, 2, 2)]
+    n = torch.tensor(lens, device="cuda")
+    ops.window_attn_decode(*draft, kc, vc, n, **see)
+    ops.window_attn_decode(*(t[:, :3].contiguous() for t in draft), *clean, n, **see)
+    for T in (1, 8, 4):
+        new = [draw(r, (B, T, h, 64), io) for h in (4, 2, 2)]
+        n = n + (3 if T == 1 else 1)  # of the 8 one stays
+        got, want = (ops.window_attn_decode(*new, *c, n, **see) for c in ((kc, vc), clean))
+        assert torch.equal(got, want), T
