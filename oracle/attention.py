@@ -130,7 +130,10 @@ def attention_bound(q, k, v, window, sinks, scale, u_out, u_mid, see=None):
     top = np.where(see, np.abs(s), 0.0).max(-1, keepdims=True, initial=0.0)
     w = np.exp(s - np.where(lse.T == -np.inf, 0.0, lse.T)[..., None])
     # an exponent is a product, a difference and an exponential away from its
-    # score; the maximum it is taken from may lie 8 powers of two behind
+    # score; the reference m it is taken from may lie 12 powers of two behind the
+    # maximum, 8.4 in natural units: |m| <= top + 8.4 and |s - m| <= |s| + top + 8.4.
+    # Both are off by a unit at most, the scale's factor by another of |s - m|, the
+    # exponential by one: U32 (2 |s| + 3 top + 26.2) in all, within the four units here
     e = e + np.where(see, 4 * U32 * (np.abs(np.where(see, s, 0.0)) + top + 8), 0.0)
     mean = (w * e).sum(-1, keepdims=True)
     V = np.abs(_heads(v, q.shape[1]))

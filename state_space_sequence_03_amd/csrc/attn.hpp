@@ -308,7 +308,10 @@ struct RowStream {
 };
 
 // Step ks of a result (its rows 16 ks .. or 8 ks ..) as the operand that goes
-// with Tile::col.
+// with Tile::col.  For bf16 operands the weights p and the gradients ds are rounded
+// to bf16 here, once each, to the nearest: the matrix cores take fp32 at an eighth of
+// the rate, and what goes with them holds no more bits either.  Outputs are then 2.0 to
+// 2.6e-3 off the exact values, where their own rounding alone makes 1.5 to 1.8e-3.
 template <typename T>
 __device__ __forceinline__ uint4 result_step(const float* v, int ks) {
   if constexpr (io<T>::BYTES == 2) {

@@ -63,11 +63,11 @@ __device__ __forceinline__ void load_stats(const AttnArgs& a, int64_t at, int ro
 // share one, and a piece: each takes its part of the list of (head, queries) and
 // its sums go to the workspace as well.
 //
-// Two waves share a SIMD, which the registers just allow (fragments three
-// products ahead: 510 to 600 us for 8 x 4096 queries, 16/4 heads of 128, window
-// 1024, as the clock is; next to 620, six ahead with spills 740, one wave per SIMD
-// 780).  There the matrix cores work in 44 % of the cycles and the vector units in
-// 29 %.
+// Two waves share a SIMD, for which a width of 128 is four registers short in bf16
+// (20 bytes of a lane in scratch memory).  With fragments three products ahead 510 to
+// 600 us for 8 x 4096 queries, 16/4 heads of 128, window 1024, as the clock is; next
+// to 620; six ahead with spills 740; one wave per SIMD 780.  There the matrix cores
+// work in 47 % of the cycles and the vector units in 32 %.
 template <typename T, int DP, int DU, int BQ>
 __global__ __launch_bounds__(256, io<T>::BYTES == 2 || DP == 64 ? 2 : 1) void attn_dkv_kernel(
     AttnArgs a, int64_t items, int64_t pieces) {

@@ -83,9 +83,10 @@ struct CacheView {
 // heads of 128, 1028 slots: 104 us, 5.2 TB/s, what a copy reaches.  Where each wave
 // has a tile or two, by the time that one takes from its lengths to its result:
 // 32768 slots of one sequence 16 us and 4 for the join, 3.5 TB/s; 8 new tokens of 32
-// sequences, 32/8 heads of 64, about 2000 slots: 20.5 and 4 us.  (Without the branch
-// around the masks, whose 250 instructions every tile then takes: 109, 18.5 and
-// 23.7.)
+// sequences, 32/8 heads of 64, up to 2059 slots: 20.5 and 4 us (8 of 1035 slots each:
+// 25 in all for 32 sequences, 40 for 64, 72 for 128, 4.5 TB/s of what is added).
+// (Without the branch around the masks, whose 250 instructions every tile then takes:
+// 109, 18.5 and 23.7.)
 template <typename T, int DP, int DU>
 __global__ __launch_bounds__(256, (io<T>::BYTES == 2 ? 2 : 1) * (DP == 64 ? 2 : 1)) void attn_decode_kernel(
     AttnDecodeArgs a) {

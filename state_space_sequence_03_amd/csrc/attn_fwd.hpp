@@ -17,8 +17,8 @@ namespace m3 {
 // Bound by the vector units next to the matrix cores: two waves per SIMD (three to
 // a width of 64), so that one's softmax runs under another's products, overlap in
 // part only: at a width of 128 products alone would take 0.53 of the time, the
-// softmax 0.65.  1 x 32768 queries, 16/4 heads of 128, window 4096: 950 to 995 us,
-// 1.04 to 1.09 PFLOP/s; 8 x 4096, window 1024: 274 to 283, 0.87; packed documents,
+// softmax 0.65.  1 x 32768 queries, 16/4 heads of 128, window 4096: 950 to 1030 us,
+// 1.01 to 1.09 PFLOP/s; 8 x 4096, window 1024: 274 to 283, 0.87; packed documents,
 // 16384 rows, 32/8 heads of 64, window 512: 96.  Runs of 32 that need not be
 // neighbours save the rest of the sinks' tile and of the first of the window's: 103
 // -> 96 us in the last of these, 29 -> 31 where there are few blocks and no window.

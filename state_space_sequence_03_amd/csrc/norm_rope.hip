@@ -8,8 +8,10 @@
 // that hold it in registers, is read once and its result written once, queries
 // and keys in one launch.  32768 tokens, 16 + 4 heads of 128, bf16: 63 us, 5.3 TB/s
 // (71 with a division for each vector's place and root: the vector units were the
-// bound); backward of 8 x 4096 tokens, 32 + 8 heads of 64: 112 us, 4.5 TB/s, and 5
-// for the gains' sums; 256 tokens: 4.5 us, a launch.  The cosines and sines are taken once per token and
+// bound); backward of 8 x 4096 tokens, 32 + 8 heads of 64: 112 us, 4.5 TB/s of what
+// it needs (a lane's sums for the gains lie in scratch memory, whose traffic comes on
+// top: 644 MB instead of 504; without it 102), and 5 for their reduction; fp32 200 us, 5.0 TB/s; 256
+// tokens: 4.5 us, a launch.  The cosines and sines are taken once per token and
 // pair, shared by the token's heads through LDS; the angle is a product in 64
 // bits reduced to a fraction of a turn there, so that far positions lose
 // nothing.
